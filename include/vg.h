@@ -8,6 +8,10 @@
  *   vg_select_kv               sink + recent + top-k index list from them;
  *   vg_sparse_draft_attention  decode attention of one draft position over
  *                              the index list plus the dense tail.
+ * Three more fill the cache that these read:
+ *   vg_step_tables             block tables and slot maps from lengths;
+ *   vg_rope_append             rotary positions, new K/V rows to their slots;
+ *   vg_chunk_attention         attention of a chunk of new tokens.
  *
  * Sources (page title, section):
  *   Vegas: Self-Speculative Decoding with Verification-Guided Sparse
@@ -93,7 +97,8 @@ enum {
   VG_DEVERR_INDEX = 2,    /* selected index outside [0, tail_start)           */
   VG_DEVERR_COUNT = 4,    /* selected count outside [0, cap]                  */
   VG_DEVERR_TIMEOUT = 8,  /* a pipeline wait outlasted its bound (see below)   */
-  VG_DEVERR_LENGTH = 16   /* a device length exceeds its host-side bound      */
+  VG_DEVERR_LENGTH = 16,  /* a device length exceeds its host-side bound      */
+  VG_DEVERR_POOL = 32     /* the free list does not cover the pages asked for */
 };
 
 /* Paged KV cache.  Pages hold 16 consecutive positions of one sequence.
@@ -341,6 +346,129 @@ vg_status vg_verify_attention_noalloc(const vg_paged_kv* kv, const void* q,
                                       int num_q_heads, int max_prefix, float softmax_scale,
                                       void* out, int capture_mode, float* capture,
                                       int num_splits, int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Filling the cache: the three calls below bring a step's new tokens into the
+ * paged cache and attend them.  vg_step_tables runs once per step,
+ * vg_rope_append and vg_chunk_attention once per layer.
+ *
+ * Block tables and slot maps of a step, from the requests' lengths.
+ *   cached_lens, new_lens  int32 [batch]: tokens of each request that are in
+ *                the cache, and tokens that this step adds (0 allowed).
+ *   page_table   int32 [batch][max_pages_per_seq], resized in place.
+ *   owned        int32 [batch], in and out: pages each request holds (entries
+ *                [0, owned) of its table row).
+ *   free_pages   int32 [free_capacity], free_count int32 [1], in and out: the
+ *                free list, a stack whose end is free_pages[free_count - 1].
+ *   owned, free_pages and free_count are given together, or all NULL: the
+ *   table is then fixed, and every page that new tokens touch has to be there.
+ * With need_b = ceil((cached_b + new_b) / 16), in this order:
+ *   1. requests with owned_b > need_b push entries [need_b, owned_b) on the
+ *      free list (requests ascending, pages ascending); the entries become -1
+ *      (need_b = 0 returns all of a finished request's pages);
+ *   2. requests with owned_b < need_b pop the missing pages from the list's
+ *      end (requests ascending, pages ascending).  A request is refused, and
+ *      changes nothing, when the pages asked for by it and by all requests
+ *      before it outnumber the list.
+ * Written:
+ *   cu_tokens    int32 [batch + 1]: exclusive prefix sum of new_lens (clamped
+ *                to max_tokens), the requests' rows in the token buffer.
+ *   kv_lens      int32 [batch]: cached_b + new_b; 0 for a refused request.
+ *   positions, slots  int32 [max_tokens]: position of each token row and its
+ *                cache slot page_table[b][position / 16] * 16 + position % 16.
+ *                Rows of refused requests and rows past the last request hold
+ *                position 0 and slot -1.
+ * A request with a negative length, one that needs more than
+ * max_pages_per_seq pages, holds a number of pages outside
+ * [0, max_pages_per_seq], or whose rows end past max_tokens is refused and
+ * flagged VG_DEVERR_LENGTH; one that the free list does not cover is flagged
+ * VG_DEVERR_POOL, and so is everyone whose pages would change when the list's
+ * count is out of range or the returned pages do not fit free_capacity.  Page
+ * ids outside [0, num_pages) are flagged VG_DEVERR_PAGE: a request that would
+ * return one is refused, a token on one has slot -1.
+ * Outputs must not overlap inputs.  One kernel, or two past 4096 tokens.
+ * Supported: batch <= 8192.
+ * ------------------------------------------------------------------------- */
+vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, int batch,
+                         int32_t* page_table, int max_pages_per_seq, int num_pages,
+                         int32_t* owned, int32_t* free_pages, int free_capacity,
+                         int32_t* free_count, int max_tokens, int32_t* cu_tokens,
+                         int32_t* kv_lens, int32_t* positions, int32_t* slots,
+                         int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions and the append of new K/V rows to the cache.
+ * Token row t: every query and key head is turned by its position and the
+ * turned keys and the values are written to cache slot slots[t].
+ *   kv           the cache to write (its pages are written in spite of the
+ *                const; its page table is not used).
+ *   q, k, v      bf16 [num_tokens][heads][head_dim], the heads of a token
+ *                contiguous, q_stride / k_stride / v_stride elements between
+ *                tokens (a multiple of 8): slices of one fused projection will
+ *                do.  Bases 16-byte aligned.  num_q_heads may be 0 (no q).
+ *   q_out        bf16 [num_tokens][num_q_heads][head_dim], q_out_stride; may
+ *                be q itself.
+ *   positions    int32 [n_axes][num_tokens] (pos_stride elements between
+ *                axes), n_axes <= 8: text has one axis, images and video three
+ *                (time, height, width).
+ *   inv_freq     float32 [rot_dim / 2]; freq_axis int32 [rot_dim / 2] names
+ *                the axis whose position frequency i multiplies (NULL: axis 0;
+ *                out of range: VG_DEVERR_INDEX, and axis 0 is used).
+ *   rot_dim      leading dims that turn, a multiple of 16 in [0, head_dim]; the
+ *                rest passes unchanged.  0: nothing turns (positions and
+ *                inv_freq may be NULL) and the call only copies.
+ *   interleaved  0: dim i turns with i + rot_dim / 2; 1: 2i with 2i + 1.
+ *   slots        int32 [num_tokens]; a negative slot writes nothing to the
+ *                cache (padding; the query is still turned), one past the pool
+ *                is flagged VG_DEVERR_INDEX and skipped.  Of two tokens with
+ *                the same slot either may be the one that stays.
+ * Angles are formed in double and reduced to a turn; the rotation is float32,
+ * rounded once.
+ * ------------------------------------------------------------------------- */
+vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                         int64_t q_out_stride, int num_tokens, int num_q_heads,
+                         const int32_t* positions, int64_t pos_stride, int n_axes,
+                         const float* inv_freq, const int32_t* freq_axis, int rot_dim,
+                         int interleaved, const int32_t* slots, int32_t* error_flag,
+                         cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of a chunk of new tokens over the paged cache (prompts in one
+ * piece or in chunks, single tokens, or a mix: packed rows, one causal mask).
+ *   q, out       bf16 [num_tokens][num_q_heads][head_dim], q_stride and
+ *                out_stride elements between tokens (multiples of 8), bases
+ *                16-byte aligned; out must not overlap q.
+ *   cu_q         int32 [batch + 1]: token rows [cu_q[b], cu_q[b + 1]) belong
+ *                to sequence b.  Rows outside every sequence are not read or
+ *                written.
+ *   kv_lens      int32 [batch]: cached positions of sequence b, its new tokens
+ *                included (their K/V are in the cache).  Token i of n_b sits
+ *                at position kv_lens[b] - n_b + i and attends the positions up
+ *                to its own.  A row that attends nothing (kv_lens[b] < n_b
+ *                leaves the first rows without) is zero.
+ *   softmax_scale  > 0.
+ *   lse          NULL, or float32 [num_tokens][num_q_heads]: natural log of
+ *                the row's sum of exponentials, -inf for a row that attends
+ *                nothing.
+ * What lies in the cache past a row's own position does not reach the row,
+ * whatever it holds.  A sequence whose rows are not a range inside
+ * [0, num_tokens), or whose length is negative or longer than its table row,
+ * is flagged VG_DEVERR_LENGTH and its rows are left as they were (rows that
+ * offsets out of order give to two sequences hold either's).  Positions on a page id
+ * outside [0, num_pages) are flagged VG_DEVERR_PAGE and count as zero K and V.
+ * Results do not depend on what else is in the batch up to float32 rounding,
+ * and are the same on every run.
+ * Supported: head_dim 64/128, num_q_heads / num_kv_heads <= 16, batch <= 4096.
+ * ------------------------------------------------------------------------- */
+size_t vg_chunk_workspace_bytes(int batch, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim);
+
+vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, int64_t q_stride,
+                             const int32_t* cu_q, const int32_t* kv_lens, int batch,
+                             int num_tokens, int num_q_heads, float softmax_scale, void* out,
+                             int64_t out_stride, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t* error_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Failure detection: the bound on pipeline waits (host).

@@ -1,0 +1,314 @@
+// Block tables and slot maps of a step, built on the GPU from the requests'
+// lengths (sm_103a).
+//
+// With need_b = ceil((cached_b + new_b) / 16) pages, a request that holds more
+// gives the rest back to the free list and one that holds fewer takes pages
+// from its end; then token i of request b sits at position cached_b + i in
+// cache slot table[b][position / 16] * 16 + position % 16.
+//
+// The work is a few integers per request and per token, so the call is bound
+// by latency: dependent memory round trips and launches, not bytes.  One CTA
+// resizes the tables (the free list is one stack, and three prefix sums over
+// the requests fix every request's place in it): a thread owns IPT
+// neighbouring requests, so one pass of warp shuffles makes each sum.  The
+// same CTA then writes the tokens' positions and slots when there are at most
+// kOneCtaTokens of them (their lookups cost less than a second launch);
+// beyond that a second kernel spreads the tokens over the GPU.
+#include <limits.h>
+
+#include "vg_device.cuh"
+#include "vg_host.h"
+
+namespace vg {
+namespace {
+
+constexpr int kTableThreads = 1024;
+constexpr int kFillThreads = 256;
+constexpr int kMaxTableBatch = 8192;   // requests: 8 per thread
+constexpr int kOneCtaTokens = 4096;
+
+struct TableParams {
+  const int32_t* cached;
+  const int32_t* fresh;
+  int32_t* page_table;
+  int32_t* owned;
+  int32_t* free_pages;
+  int32_t* free_count;
+  int32_t* cu_tokens;
+  int32_t* kv_lens;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* error_flag;
+  int batch, width, num_pages, free_capacity, max_tokens;
+};
+
+// Inclusive sum of v over the CTA's threads in thread order.  `part` holds one
+// entry per warp and is free again when the call returns.
+template <typename T>
+__device__ __forceinline__ T cta_inclusive_sum(T v, T* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    T w = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    part[lane] = w;
+  }
+  __syncthreads();
+  if (warp > 0) v += part[warp - 1];
+  __syncthreads();
+  return v;
+}
+
+// Position and slot of token row t; ends[b] = clamped end row of request b.
+__device__ __forceinline__ void fill_token(const TableParams& p, const int32_t* ends, int t) {
+  int lo = 0, hi = p.batch;  // first request whose rows end past t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  int pos = 0, slot = -1;
+  if (lo < p.batch && __ldcg(p.kv_lens + lo) > 0) {
+    pos = __ldcg(p.cached + lo) + t - (lo > 0 ? ends[lo - 1] : 0);
+    const int page = __ldcg(p.page_table + (size_t)lo * p.width + pos / kPageSize);
+    if (page >= 0 && page < p.num_pages)
+      slot = page * kPageSize + pos % kPageSize;
+    else
+      flag_error(p.error_flag, VG_DEVERR_PAGE);
+  }
+  p.positions[t] = pos;
+  p.slots[t] = slot;
+}
+
+template <int IPT>
+__global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const TableParams p) {
+  extern __shared__ int32_t ends_s[];  // [batch]
+  __shared__ long long part64[32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int b0 = tid * IPT;
+  // a fixed table has no free list: every request keeps the pages it has
+  const bool fixed = p.owned == nullptr;
+  const int top0 = fixed ? 0 : *p.free_count;
+  int cached[IPT], fresh[IPT], own[IPT], need[IPT];
+  bool ok[IPT];
+  long long rows = 0;
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int b = b0 + i;
+    const bool in = b < p.batch;
+    cached[i] = in ? p.cached[b] : 0;
+    fresh[i] = in ? p.fresh[b] : 0;
+    own[i] = in && !fixed ? p.owned[b] : 0;
+    rows += max(fresh[i], 0);
+  }
+  // -------- rows of the packed token buffer
+  long long end = cta_inclusive_sum(rows, part64) - rows;
+  int back = 0;
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int b = b0 + i;
+    end += max(fresh[i], 0);
+    const long long len = (long long)cached[i] + fresh[i];
+    ok[i] = b < p.batch && cached[i] >= 0 && fresh[i] >= 0 &&
+            len <= (long long)p.width * kPageSize && end <= p.max_tokens && own[i] >= 0 &&
+            own[i] <= p.width;
+    need[i] = ok[i] ? (int)((len + kPageSize - 1) / kPageSize) : 0;
+    if (b < p.batch) {
+      const int e = (int)(end < p.max_tokens ? end : p.max_tokens);
+      ends_s[b] = e;
+      p.cu_tokens[b + 1] = e;
+      if (!ok[i]) flag_error(p.error_flag, VG_DEVERR_LENGTH);
+    }
+  }
+  if (tid == 0) p.cu_tokens[0] = 0;
+  if (!fixed) {
+    // -------- pages that go back: checked by whole warps, then pushed
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && own[i] > need[i]);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int lo = __shfl_sync(0xffffffffu, need[i], src);
+        const int hi = __shfl_sync(0xffffffffu, own[i], src);
+        const int b = __shfl_sync(0xffffffffu, b0, src) + i;
+        bool fine = true;
+        for (int j = lo + lane; j < hi; j += 32) {
+          const int page = p.page_table[(size_t)b * p.width + j];
+          fine &= page >= 0 && page < p.num_pages;
+        }
+        if (!__all_sync(0xffffffffu, fine) && lane == src) {
+          ok[i] = false;
+          flag_error(p.error_flag, VG_DEVERR_PAGE);
+        }
+      }
+      back += ok[i] ? max(own[i] - need[i], 0) : 0;
+    }
+    int grow = 0;  // a thread's own pages: at most 8 requests of < 2^27 pages
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) grow += ok[i] ? max(need[i] - own[i], 0) : 0;
+    const long long back_sum = cta_inclusive_sum((long long)back, part64);
+    long long want = cta_inclusive_sum((long long)grow, part64) - grow;  // asked for before this thread
+    __shared__ long long total_s;
+    if (tid == kTableThreads - 1) total_s = back_sum;
+    __syncthreads();
+    const long long back_all = total_s;
+    // a free list that is not one (its count is outside it, or the pages
+    // coming back do not fit) changes nobody's pages
+    const bool list_ok = top0 >= 0 && top0 + back_all <= p.free_capacity;
+    const int top = top0 + (int)back_all;
+    int at = top0 + (int)back_sum - back;  // this thread's first push
+    if (list_ok) {
+#pragma unroll
+      for (int i = 0; i < IPT; ++i) {
+        uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && own[i] > need[i]);
+        while (todo) {
+          const int src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int lo = __shfl_sync(0xffffffffu, need[i], src);
+          const int hi = __shfl_sync(0xffffffffu, own[i], src);
+          const int b = __shfl_sync(0xffffffffu, b0, src) + i;
+          const int to = __shfl_sync(0xffffffffu, at, src);
+          for (int j = lo + lane; j < hi; j += 32) {
+            int32_t* e = p.page_table + (size_t)b * p.width + j;
+            p.free_pages[to + j - lo] = *e;
+            *e = -1;
+          }
+        }
+        if (ok[i]) at += max(own[i] - need[i], 0);
+      }
+    }
+    __syncthreads();
+    // -------- pages that are taken: the k-th page asked for is the k-th from
+    // the list's end; a request past the end gets none
+    int taken = 0;
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      const int more = ok[i] ? max(need[i] - own[i], 0) : 0;
+      const bool moves = ok[i] && need[i] != own[i];
+      if (moves && (!list_ok || (more > 0 && want + more > top))) {
+        ok[i] = false;
+        flag_error(p.error_flag, VG_DEVERR_POOL);
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && more > 0);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int lo = __shfl_sync(0xffffffffu, own[i], src);
+        const int hi = __shfl_sync(0xffffffffu, need[i], src);
+        const int b = __shfl_sync(0xffffffffu, b0, src) + i;
+        const int from = top - 1 - (int)__shfl_sync(0xffffffffu, want, src);
+        for (int j = lo + lane; j < hi; j += 32) {
+          const int page = p.free_pages[from - (j - lo)];
+          const bool fine = page >= 0 && page < p.num_pages;
+          if (!fine) flag_error(p.error_flag, VG_DEVERR_PAGE);
+          p.page_table[(size_t)b * p.width + j] = fine ? page : -1;
+        }
+      }
+      want += more;
+      if (ok[i] && b0 + i < p.batch) {
+        if (need[i] != own[i]) p.owned[b0 + i] = need[i];
+        taken += more;
+      }
+    }
+    const long long all = cta_inclusive_sum((long long)taken, part64);
+    if (tid == kTableThreads - 1 && list_ok) *p.free_count = top - (int)all;
+  }
+#pragma unroll
+  for (int i = 0; i < IPT; ++i)
+    if (b0 + i < p.batch) p.kv_lens[b0 + i] = ok[i] ? cached[i] + fresh[i] : 0;
+  if (p.max_tokens > kOneCtaTokens) return;  // the fill kernel follows
+  __syncthreads();
+  for (int t = tid; t < p.max_tokens; t += kTableThreads) fill_token(p, ends_s, t);
+}
+
+// Positions and slots of many tokens (chained to the kernel above).
+__global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableParams p) {
+  extern __shared__ int32_t ends_s[];  // [batch]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  for (int b = threadIdx.x; b < p.batch; b += kFillThreads) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
+  __syncthreads();
+  const int t = blockIdx.x * kFillThreads + threadIdx.x;
+  if (t < p.max_tokens) fill_token(p, ends_s, t);
+}
+
+template <typename K>
+cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream,
+                           const TableParams& p) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+}  // namespace vg
+
+using namespace vg;
+
+extern "C" vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, int batch,
+                                    int32_t* page_table, int max_pages_per_seq, int num_pages,
+                                    int32_t* owned, int32_t* free_pages, int free_capacity,
+                                    int32_t* free_count, int max_tokens, int32_t* cu_tokens,
+                                    int32_t* kv_lens, int32_t* positions, int32_t* slots,
+                                    int32_t* error_flag, cudaStream_t stream) {
+  if (!cached_lens || !new_lens || !page_table || !cu_tokens || !kv_lens || batch <= 0 ||
+      max_pages_per_seq <= 0 || num_pages <= 0 || max_tokens < 0)
+    return VG_ERR_INVALID_ARGUMENT;
+  if (max_tokens > 0 && (!positions || !slots)) return VG_ERR_INVALID_ARGUMENT;
+  // the free list is given whole or not at all
+  if ((owned != nullptr) != (free_pages != nullptr) || (owned != nullptr) != (free_count != nullptr) ||
+      (owned && free_capacity <= 0))
+    return VG_ERR_INVALID_ARGUMENT;
+  // a slot number and a sequence length have to fit an int32
+  if (batch > kMaxTableBatch || num_pages > INT_MAX / kPageSize ||
+      max_pages_per_seq > INT_MAX / kPageSize)
+    return VG_ERR_UNSUPPORTED;
+  TableParams p = {};
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.page_table = page_table;
+  p.owned = owned;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.cu_tokens = cu_tokens;
+  p.kv_lens = kv_lens;
+  p.positions = positions;
+  p.slots = slots;
+  p.error_flag = error_flag;
+  p.batch = batch;
+  p.width = max_pages_per_seq;
+  p.num_pages = num_pages;
+  p.free_capacity = free_capacity;
+  p.max_tokens = max_tokens;
+  const size_t smem = (size_t)batch * sizeof(int32_t);  // at most 32 KB
+  cudaError_t e = batch <= kTableThreads
+                      ? launch_chained(step_tables_kernel<1>, 1, kTableThreads, smem, stream, p)
+                      : launch_chained(step_tables_kernel<8>, 1, kTableThreads, smem, stream, p);
+  if (e == cudaSuccess && max_tokens > kOneCtaTokens)
+    e = launch_chained(step_fill_kernel, ceil_div(max_tokens, kFillThreads), kFillThreads, smem,
+                       stream, p);
+  return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
+}

@@ -26,6 +26,7 @@ DEVERR_INDEX = 2
 DEVERR_COUNT = 4
 DEVERR_TIMEOUT = 8
 DEVERR_LENGTH = 16
+DEVERR_POOL = 32
 
 EXPORTED = (
     "vg_verify_workspace_bytes", "vg_verify_attention",
@@ -35,6 +36,7 @@ EXPORTED = (
     "vg_verify_noalloc_scratch_bytes", "vg_verify_attention_noalloc",
     "vg_sparse_verify_workspace_bytes", "vg_sparse_verify_attention",
     "vg_set_wait_limit_ns",
+    "vg_step_tables", "vg_rope_append", "vg_chunk_workspace_bytes", "vg_chunk_attention",
 )
 
 
@@ -57,6 +59,7 @@ def _load():
                           f"g.build()\"` (needs nvcc with sm_103a support)")
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    i64 = ctypes.c_int64
     kvp = ctypes.POINTER(PagedKVStruct)
     sig = {
         "vg_verify_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
@@ -77,6 +80,13 @@ def _load():
         "vg_sparse_verify_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
         "vg_sparse_verify_attention": (i32, [kvp, vp, vp, i32, i32, i32, i32, f32, vp, vp, i32, vp,
                                              i32, vp, sz, vp, vp]),
+        "vg_step_tables": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp, vp,
+                                 vp, vp]),
+        "vg_rope_append": (i32, [kvp, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp, i64, i32,
+                                 vp, vp, i32, i32, vp, vp, vp]),
+        "vg_chunk_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "vg_chunk_attention": (i32, [kvp, vp, i64, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp, sz,
+                                     vp, vp]),
         "vg_set_wait_limit_ns": (i32, [ctypes.c_uint64]),
         "vg_status_string": (ctypes.c_char_p, [i32]),
         "vg_version": (ctypes.c_char_p, []),
@@ -145,6 +155,10 @@ class PagedKV:
         P, H, S, D = self.k_pages.shape
         return PagedKVStruct(self.k_pages.data_ptr(), self.v_pages.data_ptr(),
                              self.page_table.data_ptr(), P, S, self.page_table.shape[1], H, D)
+
+    def pointer(self):
+        """struct() by reference, for a call that is made at once."""
+        return ctypes.byref(self.struct())
 
 
 # --------------------------------------------------------------------- verify
@@ -301,6 +315,141 @@ def sparse_draft_attention(kv: PagedKV, q, indices, counts, per_head, tail_start
                                        _ptr(workspace), ws_bytes, _ptr(error_flag),
                                        _stream(stream))
     _check("vg_sparse_draft_attention", s)
+    return out
+
+
+# ------------------------------------------------------------ filling the cache
+def _expect(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _int32(t, n, name):
+    """Device pointer of a contiguous int32 tensor of n elements (n None: any)."""
+    if not (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
+            and (n is None or t.numel() == n)):
+        raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} elements is needed")
+    return t.data_ptr()
+
+
+def _opt(t, n, name):
+    return None if t is None else _int32(t, n, name)
+
+
+def _heads(t, name):
+    """(pointer, tokens, heads, head_dim, elements between tokens) of bf16 rows
+    [T][H][d] whose heads are contiguous within a token."""
+    if t.dim() != 3 or t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name}: a bfloat16 GPU tensor [tokens][heads][head_dim] is needed")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n > 0 and (s2 != 1 or (s1 != d and h > 1)):
+        raise ValueError(f"{name}: the heads of a token have to be contiguous")
+    return t.data_ptr(), n, h, d, s0 if n > 1 else h * d
+
+
+def _device_stream(t, stream):
+    """Raw stream for a call on tensor t's device: the given one, or that
+    device's current stream."""
+    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+
+
+def _call(fn, t, *args):
+    """Call an entry point with t's device current."""
+    if t.device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(t.device):
+            status = fn(*args)
+    if status != 0:
+        raise VGError(fn.__name__, status)
+
+
+def step_tables(page_table, num_pages, cached_lens, new_lens, cu_tokens, kv_lens, positions, slots,
+                owned=None, free_pages=None, free_count=None, error_flag=None, stream=None):
+    """vg_step_tables: resize the block tables to cached_lens + new_lens tokens
+    per request and write each new token's position and cache slot.
+
+    page_table int32 [B][max_pages]; owned, free_pages, free_count (int32 [B],
+    [capacity], [1]) are updated in place, or all None for a fixed table.
+    Outputs: cu_tokens [B + 1], kv_lens [B], positions and slots [max_tokens]."""
+    _expect(page_table.dim() == 2, "page_table: [batch][max_pages] is needed")
+    B, width = page_table.shape
+    _expect(slots.numel() == positions.numel(), "positions and slots differ in length")
+    _call(_lib.vg_step_tables, page_table, _int32(cached_lens, B, "cached_lens"),
+          _int32(new_lens, B, "new_lens"), B, _int32(page_table, None, "page_table"), width,
+          int(num_pages), _opt(owned, B, "owned"), _opt(free_pages, None, "free_pages"),
+          0 if free_pages is None else free_pages.numel(), _opt(free_count, 1, "free_count"),
+          positions.numel(), _int32(cu_tokens, B + 1, "cu_tokens"), _int32(kv_lens, B, "kv_lens"),
+          _int32(positions, None, "positions"), _int32(slots, None, "slots"),
+          _opt(error_flag, None, "error_flag"), _device_stream(page_table, stream))
+    return cu_tokens, kv_lens, positions, slots
+
+
+def rope_append(kv: PagedKV, q, k, v, slots, q_out=None, positions=None, inv_freq=None,
+                freq_axis=None, interleaved=False, error_flag=None, stream=None):
+    """vg_rope_append: turn q and k by their positions, write k and v to the
+    cache slots and the turned queries to q_out (None: over q).
+
+    q [T][Hq][d] (or None), k and v [T][Hkv][d] bf16, slices of a fused
+    projection included; slots int32 [T]; positions int32 [T] or [axes][T];
+    inv_freq float32 [rot / 2] (None: nothing turns); freq_axis int32 [rot / 2]."""
+    kp, T, H, d, ks = _heads(k, "k")
+    vp, Tv, Hv, dv, vs = _heads(v, "v")
+    _expect(T == Tv and H == Hv == kv.num_kv_heads and d == dv == kv.head_dim,
+            "k and v do not match each other or the cache")
+    qp = op = None
+    Hq = qs = os_ = 0
+    if q is not None:
+        qp, Tq, Hq, dq, qs = _heads(q, "q")
+        op, To, Ho, do, os_ = (qp, Tq, Hq, dq, qs) if q_out is None else _heads(q_out, "q_out")
+        _expect(Tq == To == T and Ho == Hq and dq == do == d, "q or q_out does not match k")
+    pos = freq = None
+    axes, ps, rot = 0, 0, 0
+    if inv_freq is not None:
+        _expect(inv_freq.dtype is torch.float32 and inv_freq.is_cuda and inv_freq.is_contiguous(),
+                "inv_freq: a contiguous float32 GPU tensor is needed")
+        _expect(positions is not None, "positions are needed with inv_freq")
+        _expect(positions.dtype is torch.int32 and positions.is_cuda and positions.dim() <= 2
+                and positions.shape[-1] == T and (T < 2 or positions.stride(-1) == 1),
+                "positions: int32 [tokens] or [axes][tokens] on the GPU is needed")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        ps = T if axes == 1 else positions.stride(0)
+        pos, freq, rot = positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel()
+    _call(_lib.vg_rope_append, k, kv.pointer(), qp, qs, kp, ks, vp, vs, op, os_, T, Hq, pos, ps,
+          axes, freq, _opt(freq_axis, rot // 2, "freq_axis"), rot, 1 if interleaved else 0,
+          _int32(slots, T, "slots"), _opt(error_flag, None, "error_flag"),
+          _device_stream(k, stream))
+    return q if q_out is None else q_out
+
+
+def chunk_workspace_bytes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(_lib.vg_chunk_workspace_bytes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim))
+
+
+def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None, workspace=None,
+                    error_flag=None, stream=None):
+    """vg_chunk_attention: causal attention of packed rows of new tokens over
+    the paged cache.  q and out [T][Hq][d] bf16, cu_q int32 [B + 1], kv_lens
+    int32 [B] (new tokens included), lse (optional) float32 [T][Hq].
+    workspace: uint8 tensor of chunk_workspace_bytes() (allocated here when not
+    given)."""
+    qp, T, Hq, d, qs = _heads(q, "q")
+    op, To, Ho, do, os_ = _heads(out, "out")
+    _expect(T == To and Hq == Ho and d == do == kv.head_dim, "out or the cache does not match q")
+    B = kv_lens.numel()
+    _expect(kv.page_table.shape[0] == B, "the cache's page table has another batch size")
+    if lse is not None:
+        _expect(lse.dtype is torch.float32 and lse.is_cuda and lse.is_contiguous()
+                and lse.numel() == T * Hq, "lse: a contiguous float32 GPU tensor [T][Hq] is needed")
+    if workspace is None:
+        workspace = torch.empty(max(chunk_workspace_bytes(B, T, Hq, kv.num_kv_heads, d), 1),
+                                dtype=torch.uint8, device=q.device)
+    _call(_lib.vg_chunk_attention, q, kv.pointer(), qp, qs, _int32(cu_q, B + 1, "cu_q"),
+          _int32(kv_lens, B, "kv_lens"), B, T, Hq, softmax_scale, op, os_,
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _opt(error_flag, None, "error_flag"),
+          _device_stream(q, stream))
     return out
 
 
