@@ -2,107 +2,1019 @@
 //
 // Row (token i of sequence b, query head q) sits at position
 // P = kv_len_b - n_b + i and computes softmax(scale q . k_j) v over the
-// positions j <= P: one warp per row, lanes over the head's dimensions, the
-// running maximum, sum and output in registers (fp32).
+// positions j <= P.
+//
+// Design (one persistent CTA per SM):
+//  * A unit is two 128-row tiles of one KV head of one sequence: the
+//    floor(128 / g) tokens of a tile times their g query heads, packed token
+//    by token, so K and V are read once for all heads of the group.  Its work
+//    is the 128-position tiles up to its last row's position.
+//  * All units' tiles form one line (sequence, KV head, row tiles), cut into
+//    equal shares, one per CTA: any mix of long prompts and single tokens is
+//    balanced to a tile.  KV heads outrank row tiles on the line so that the
+//    CTAs of a long prompt stream the same few heads, which L2 holds.  A unit
+//    that a cut divides leaves fp32 partials (m, l, O) in the workspace; a
+//    small chained kernel merges them.  Every CTA finds its own share from
+//    the lengths, so the call needs no plan from the host.
+//  * Two softmax warpgroups, one row per thread, each with its own S (128
+//    fp32 columns of tensor memory, P written back over it as bf16) and O:
+//    while one does its exponentials the tensor cores run the other's
+//    O += P V and S = Q K^T.  A unit of one row tile (single tokens) gives
+//    both warpgroups the same rows and alternate position tiles; O's rows are
+//    in the same tensor-memory lanes, so their merge needs only (m, l) from
+//    the other side.
+//  * S(t + 1) of a warpgroup is issued after its P(t) V, so its arrival also
+//    says that O may be rescaled.  The exponent reference moves only when a
+//    row maximum grows by more than 2^8: P stays below 2^8 times a weight of
+//    one, exact range in bf16 and far from the fp32 range in l and O.
+//  * A producer warp streams K and V tiles (page by page, TMA, 128-byte
+//    swizzle) through a ring of stages and publishes the CTA's units; one
+//    thread issues every tensor-core operation.
+//  * Position tiles that some row of the unit does not attend in full (the
+//    diagonal and the end of the cache) pass through two checking warps
+//    first: a weight of zero times a NaN or an infinity in V would still
+//    spoil the row, so they zero V past the length and take non-finite values
+//    out of the tile, noting per dimension the first position of each kind;
+//    rows that attend it get it back at the end.
+#include <math.h>
+
 #include "vg_device.cuh"
 #include "vg_host.h"
 
 namespace vg {
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kTile = 128;             // positions of a KV tile, rows of a row tile
+constexpr int kPagesPerTile = kTile / kPageSize;
+constexpr int kChunkThreads = 384;
+constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax)
+constexpr int kMaxBatch = 4096;
+constexpr float kRescale = 8.f;        // log2 growth of a row maximum that moves the reference
+constexpr int kRowsMax = 2 * kTile;    // rows of a unit
 
 struct ChunkParams {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k_pages;
-  const __nv_bfloat16* v_pages;
   const int32_t* page_table;
   const int32_t* cu_q;
   const int32_t* kv_lens;
   __nv_bfloat16* out;
   float* lse;
+  float* part_o;      // [grid][2][rows][HD]
+  float* part_ml;     // [grid][2][rows][2]
+  struct MergeUnit* merge;  // [grid]
   int32_t* error_flag;
-  int64_t q_stride, out_stride;
+  int64_t out_stride;
+  uint64_t wait_ns;
   float scale_log2;
-  int batch, num_tokens, num_q_heads, num_kv_heads, num_pages, width;
+  int batch, num_tokens, num_q_heads, num_kv_heads, group, num_pages, width, rows;
+};
+
+// A unit that several CTAs share, written by the CTA where it begins.
+struct MergeUnit {
+  int parts;          // 0: none
+  int tok0, ntok, h;
+};
+
+// A unit of work as the CTA's roles see it.
+struct Unit {
+  int tok0, ntok;     // first token row, tokens (at most 2 * tile_tokens)
+  int pos0;           // position of the first token (may be negative)
+  int len;            // positions of the sequence
+  int h;
+  int kt0, kt1;       // position tiles of this CTA; kt0 == kt1: no more units
+  int n0;             // position tiles of the first row tile
+  int two;            // two row tiles (else one, position tiles alternate)
+  int part;           // partial slot of the workspace, -1: writes its rows
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kRowWarps * 32) chunk_rows_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32;  // elements of the head per lane
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
-      if (p.cu_q[b] < 0 || p.cu_q[b + 1] < p.cu_q[b] || p.cu_q[b + 1] > p.num_tokens ||
-          p.kv_lens[b] < 0 || p.kv_lens[b] > p.width * kPageSize)
-        flag_error(p.error_flag, VG_DEVERR_LENGTH);
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int t = (int)(row / p.num_q_heads), qh = (int)(row % p.num_q_heads);
-  if (t >= p.num_tokens) return;
-  int lo = 0, hi = p.batch;  // first sequence that ends past t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_q[mid + 1] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  const int b = lo;
-  if (b >= p.batch) return;
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], len = p.kv_lens[b];
-  if (q0 < 0 || q0 > t || q1 > p.num_tokens || len < 0 || len > p.width * kPageSize) return;
-  const int n = len - (q1 - q0) + (t - q0) + 1;  // attended positions
-  const int h = qh / (p.num_q_heads / p.num_kv_heads);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+struct ChunkLayout {
+  static constexpr int kHalves = HD / 64;
+  static constexpr int kHalfBytes = kTile * 128;
+  static constexpr int kStageBytes = kHalves * kHalfBytes;
+  static constexpr int kStages = HD == 128 ? 5 : 10;
+  static constexpr int kQBytes = kStageBytes;          // one row tile
+  static constexpr int kRing = 2 * kQBytes;
+  static constexpr int kSmall = kRing + kStages * kStageBytes;
+  // small area: barriers, units, (m, l) exchange, non-finite notes
+  static constexpr int kBars = kSmall;
+  static constexpr int kBarCount = 4 * kStages + 15;
+  static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
+  static constexpr int kFlags = kUnits + 2 * 48;
+  static constexpr int kNotes = kFlags + 32;
+  static constexpr int kMl = kNotes + 2 * 3 * HD * 2;
+  static constexpr int kBytes = kMl + kTile * 8;
+  static constexpr int kSCol = 0, kOCol = 2 * kTile;
+};
+static_assert(ChunkLayout<128>::kBytes <= 227 * 1024 && ChunkLayout<64>::kBytes <= 227 * 1024, "");
+static_assert(sizeof(Unit) <= 48, "");
+
+struct ChunkBars {
+  // Ring stages: `full` (a K tile, or a V tile that needs no check, has
+  // landed), `landed` (a V tile to check has), `clean` (it was checked),
+  // `empty`.  Each use of a stage completes a phase of one of the first two
+  // only, so their parities are counted per stage (a bit mask), and whoever
+  // waits on one of them waits for every phase of it.
+  uint64_t *full, *landed, *clean, *empty;  // [stages]
+  uint64_t *sfull, *pfull, *ofull;         // [2]
+  uint64_t *qfull, *qempty, *ufull, *uempty, *xfull, *xdone, *drain;
+};
+
+__device__ __forceinline__ ChunkBars chunk_bars(uint64_t* b, int stages) {
+  ChunkBars r;
+  r.full = b;
+  r.landed = b + stages;
+  r.clean = b + 2 * stages;
+  r.empty = b + 3 * stages;
+  b += 4 * stages;
+  r.sfull = b;
+  r.pfull = b + 2;
+  r.ofull = b + 4;
+  r.ufull = b + 6;
+  r.uempty = b + 8;
+  r.qfull = b + 10;
+  r.qempty = b + 11;
+  r.xfull = b + 12;
+  r.xdone = b + 13;
+  r.drain = b + 14;
+  return r;
+}
+
+// Position tiles up to position `pos`, at least one (a unit whose rows attend
+// nothing still writes them).
+__device__ __forceinline__ int tiles_to(int pos) { return pos < 0 ? 1 : pos / kTile + 1; }
+
+// Rows and lengths of sequence b; n = 0 when it has none or makes no sense.
+__device__ __forceinline__ bool sequence_of(const ChunkParams& p, int b, int& q0, int& n, int& len) {
+  q0 = p.cu_q[b];
+  const int q1 = p.cu_q[b + 1];
+  len = p.kv_lens[b];
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_tokens && len >= 0 && len <= p.width * kPageSize;
+  n = ok ? q1 - q0 : 0;
+  return ok;
+}
+
+// Position tiles of row-tile pair `rt` (tu tokens each) of a sequence.
+__device__ __forceinline__ int unit_tiles(int n, int len, int tu, int rt) {
+  return tiles_to(len - n + min((rt + 1) * tu, n) - 1);
+}
+
+// Whether some row of the unit does not attend all of tile kt (its first row
+// ends before the tile does): V is then checked.
+__device__ __forceinline__ bool checked_tile(const Unit& un, int kt) {
+  return kt * kTile + kTile - 1 > un.pos0;
+}
+
+__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
+  return mbar_wait_checked(bar, parity, p.wait_ns, p.error_flag);
+}
+// The same for a whole warp, which stays together.
+__device__ __forceinline__ bool chunk_wait_warp(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
+  return __all_sync(0xffffffffu, chunk_wait(bar, parity, p));
+}
+
+// 64 consecutive columns of this warp's lanes, load and wait in one statement
+// (no register is read before it has landed).
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A V entry with its non-finite value given back: rel = the row's token within
+// the unit, notes = first token distance of a NaN, +inf, -inf in dimension c.
+template <int HD>
+__device__ __forceinline__ float noted(float v, const uint16_t* notes, int c, int rel) {
+  const bool n = rel >= notes[c], pi = rel >= notes[HD + c], ni = rel >= notes[2 * HD + c];
+  if (n || (pi && ni)) return NAN;
+  return pi ? INFINITY : ni ? -INFINITY : v;
+}
+
+// ---------------------------------------------------------------- softmax
+// One warp of warpgroup S (0 or 1) through all units of the CTA.
+template <int HD>
+__device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBars& bars,
+                                             const Unit* units, const int* note_flags,
+                                             const uint16_t* notes_s, float2* ml_s, uint32_t tmem,
+                                             int wg, int warp, int lane) {
+  using Lay = ChunkLayout<HD>;
+  const int g = p.group, tt = kTile / g;
+  const int r = (warp & 3) * 32 + lane;  // row within the tile
+  const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  const uint32_t scol = trow + Lay::kSCol + wg * kTile;
+  const uint32_t ocol = trow + Lay::kOCol + wg * HD;
+  const int tok_r = r / g, head_r = r - tok_r * g;
+  uint32_t sc = 0, oc = 0, xc = 0;
+  for (uint32_t u = 0;; ++u) {
+    const int slot = u & 1;
+    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
+    const Unit un = units[slot];
+    if (un.kt0 == un.kt1) return;
+    const int tok = un.two ? wg * tt + tok_r : tok_r;       // token within the unit
+    const bool valid = tok_r < tt && tok < un.ntok;
+    const int lim = valid ? un.pos0 + tok : -1;             // last attended position
+    const bool rows = __any_sync(0xffffffffu, valid);       // a warp without rows only keeps step
+    const int first = un.two ? un.kt0 : un.kt0 + wg;
+    const int step = un.two ? 1 : 2;
+    const int end = un.two && wg == 0 ? min(un.kt1, un.n0) : un.kt1;
+    float m_used = -INFINITY, lsum = 0.f;
+    for (int kt = first; kt < end; kt += step) {
+      if (!chunk_wait_warp(&bars.sfull[wg], sc & 1, p)) return;
+      ++sc;
+      tc_fence_after();
+      if (rows) {
+        uint32_t a[64], b[64];
+        tmem_ld64(scol, a);
+        tmem_ld64(scol + 64, b);
+        const int rem = lim - kt * kTile;  // last attended column
+        const bool whole = __all_sync(0xffffffffu, rem >= kTile - 1 || !valid);
+        if (!whole) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[t * p.q_stride + (int64_t)qh * HD + lane * E + e]) * p.scale_log2;
-    o[e] = 0.f;
-  }
-  for (int j = 0; j < n; ++j) {
-    const int page = p.page_table[(size_t)b * p.width + j / kPageSize];
-    float k[E], v[E];
-    const bool ok = page >= 0 && page < p.num_pages;
-    if (!ok && lane == 0) flag_error(p.error_flag, VG_DEVERR_PAGE);
-    const size_t at = ok ? (((size_t)page * p.num_kv_heads + h) * kPageSize + j % kPageSize) * HD + lane * E : 0;
-    float s = 0.f;
+          for (int j = 0; j < 64; ++j)
+            if (j > rem) a[j] = 0xff800000u;
+        }
+        float mx[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      k[e] = ok ? __bfloat162float(p.k_pages[at + e]) : 0.f;
-      v[e] = ok ? __bfloat162float(p.v_pages[at + e]) : 0.f;
-      s = fmaf(q[e], k[e], s);
+        for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(a[j]);
+#pragma unroll
+        for (int j = 8; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(a[j]));
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j + 64 > rem) b[j] = 0xff800000u;
+        }
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(b[j]));
+#pragma unroll
+        for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+          for (int j = 0; j < w; ++j) mx[j] = fmaxf(mx[j], mx[j + w]);
+        const float m_tile = mx[0] * p.scale_log2;  // scale > 0: the maximum commutes with it
+        const bool need = m_tile > m_used + kRescale;
+        if (__any_sync(0xffffffffu, need)) {
+          const float mn = need ? m_tile : m_used;
+          if (kt != first) {  // P(t - 1) V is done: S(t) was issued after it
+            const float corr = mn == -INFINITY ? 1.f : ex2(m_used - mn);
+            lsum *= corr;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tmem_ld16(ocol + c, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= corr;
+              tmem_st16(ocol + c, o);
+            }
+            tmem_st_wait();
+          }
+          m_used = mn;
+        }
+        const float nref = -safe_ref(m_used);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int e = (q & 1) * 32 + 2 * j;
+            const float s0 = __uint_as_float(q < 2 ? a[e] : b[e]);
+            const float s1 = __uint_as_float(q < 2 ? a[e + 1] : b[e + 1]);
+            const float p0 = ex2(fmaf(s0, p.scale_log2, nref));
+            const float p1 = ex2(fmaf(s1, p.scale_log2, nref));
+            acc[(j & 1) * 2] += p0;
+            acc[(j & 1) * 2 + 1] += p1;
+            pk[j] = pack_bf16(p0, p1);
+          }
+          tmem_st16u(scol + q * 16, pk);
+        }
+        lsum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pfull[wg]);
     }
+    // -------- epilogue
+    const bool has = end > first;
+    if (has) {
+      if (!chunk_wait_warp(&bars.ofull[wg], oc & 1, p)) return;
+      ++oc;
+      tc_fence_after();
+    }
+    const bool other = !un.two && un.kt0 + 1 < un.kt1;  // alternate tiles: both sides have O
+    float w_own = 1.f, w_other = 0.f, m_all = m_used, l_all = lsum;
+    if (other) {
+      if (wg == 1) {
+        ml_s[r] = make_float2(m_used, lsum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.xfull);
+      } else {
+        if (!chunk_wait_warp(bars.xfull, xc & 1, p)) return;
+        tc_fence_after();
+        const float2 o = ml_s[r];
+        m_all = fmaxf(m_used, o.x);
+        const float ref = safe_ref(m_all);
+        w_own = ex2(m_used - ref);
+        w_other = ex2(o.x - ref);
+        l_all = w_own * lsum + w_other * o.y;
+      }
+    }
+    if (rows && (un.two || wg == 0)) {
+      const bool noted_half[2] = {note_flags[slot * 2] != 0, note_flags[slot * 2 + 1] != 0};
+      const uint16_t* notes = notes_s + slot * 3 * HD;
+      const bool direct = un.part < 0;
+      const int t = un.tok0 + tok, qh = un.h * g + head_r;
+      const int prow = (un.two ? wg * kTile : 0) + r;       // row of the partial
+      const float inv = direct ? (l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN) : 1.f;
+      const float f_own = has ? w_own * inv : 0.f, f_other = w_other * inv;
+      float* po = direct ? nullptr : p.part_o + ((size_t)un.part * p.rows + prow) * HD;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 16) {
+        float o[16];
+        if (has) {
+          tmem_ld16(ocol + c, o);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float m_new = fmaxf(m, s), ref = safe_ref(m_new);
-    const float corr = ex2(m - ref), w = ex2(s - ref);
-    l = l * corr + w;
+          for (int j = 0; j < 16; ++j) o[j] *= f_own;
+        } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * corr + w * v[e];
-    m = m_new;
+          for (int j = 0; j < 16; ++j) o[j] = 0.f;
+        }
+        if (other) {
+          float x[16];
+          tmem_ld16(ocol + HD + c, x);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = fmaf(x[j], f_other, o[j]);
+        }
+        if (noted_half[c >= HD / 2]) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = noted<HD>(o[j], notes, c + j, tok);
+        }
+        if (valid && direct) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + t * p.out_stride + (int64_t)qh * HD + c);
+          dst[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+          dst[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
+        } else if (valid) {
+          float4* dst = reinterpret_cast<float4*>(po + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+        __syncwarp();
+      }
+      if (valid && direct && p.lse)
+        p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
+      if (valid && !direct)
+        reinterpret_cast<float2*>(p.part_ml)[(size_t)un.part * p.rows + prow] = make_float2(m_all, l_all);
+    }
+    if (other) {
+      if (wg == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.xdone);
+      } else if (!chunk_wait_warp(bars.xdone, xc & 1, p)) {
+        return;
+      }
+      ++xc;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.uempty[slot]);
   }
-  const float inv = n > 0 ? 1.f / l : 0.f;
+}
+
+// ------------------------------------------------------- tensor-core issue
+template <int HD>
+struct MmaIssuer {
+  using Lay = ChunkLayout<HD>;
+  const ChunkParams& p;
+  const ChunkBars& bars;
+  uint32_t tmem, ring, q;
+  static constexpr uint32_t kIdQk = umma_idesc_bf16(kTile, kTile, 0, 0);
+  static constexpr uint32_t kIdPv = umma_idesc_bf16(kTile, HD, 0, 1);
+
+  // S of warpgroup `wg` = Q (row tile qt) K^T of the stage
+  __device__ __forceinline__ void qk(int wg, int qt, int stage) {
+    const uint32_t kb = ring + stage * Lay::kStageBytes, qb = q + qt * Lay::kQBytes;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.out[t * p.out_stride + (int64_t)qh * HD + lane * E + e] = __float2bfloat16(o[e] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)t * p.num_q_heads + qh] = n > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    for (int ks = 0; ks < HD / 16; ++ks) {
+      const uint32_t off = (ks >> 2) * Lay::kHalfBytes + (ks & 3) * 32;
+      umma_bf16(tmem + Lay::kSCol + wg * kTile, umma_smem_desc(qb + off, 16, 1024),
+                umma_smem_desc(kb + off, 16, 1024), kIdQk, ks > 0);
+    }
+    umma_commit(&bars.sfull[wg]);
+  }
+  // O of warpgroup `wg` (+)= P V of the stage
+  __device__ __forceinline__ void pv(int wg, int stage, bool accumulate) {
+    const uint32_t vb = ring + stage * Lay::kStageBytes;
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+      umma_bf16_ts(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
+                   umma_smem_desc(vb + ks * 16 * 128, Lay::kHalfBytes, 1024), kIdPv,
+                   accumulate || ks > 0);
+  }
+};
+
+template <int HD>
+__device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& bars,
+                                         const Unit* units, uint32_t tmem, uint32_t ring, uint32_t q) {
+  using Lay = ChunkLayout<HD>;
+  constexpr int NST = Lay::kStages;
+  MmaIssuer<HD> mma{p, bars, tmem, ring, q};
+  uint32_t pc[2] = {0, 0}, full = 0, clean = 0;  // parities
+  uint32_t tiles = 0;                            // position tiles before this unit
+  for (uint32_t u = 0;; ++u) {
+    const int slot = u & 1;
+    if (!chunk_wait(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
+    const Unit un = units[slot];
+    mbar_arrive(&bars.uempty[slot]);
+    if (un.kt0 == un.kt1) return true;
+    if (!chunk_wait(bars.qfull, u & 1, p)) return false;
+    const int n = un.kt1 - un.kt0;
+    const int e0 = un.two ? min(un.kt1, un.n0) - un.kt0 : n;  // tiles of warpgroup 0 (two row tiles)
+    // The stage of the unit's j-th K or V tile once it may be read, or -1.
+    auto ready = [&](uint32_t i, uint64_t* bar, uint32_t& parity) -> int {
+      const uint32_t st = i % NST, par = (parity >> st) & 1;
+      parity ^= 1u << st;
+      return chunk_wait(&bar[st], par, p) ? (int)st : -1;
+    };
+    auto k_ready = [&](int j) { return ready(2 * (tiles + j), bars.full, full); };
+    auto v_ready = [&](int j) {
+      return checked_tile(un, un.kt0 + j) ? ready(2 * (tiles + j) + 1, bars.clean, clean)
+                                          : ready(2 * (tiles + j) + 1, bars.full, full);
+    };
+    auto p_ready = [&](int wg) { return chunk_wait(&bars.pfull[wg], pc[wg]++ & 1, p); };
+    if (un.two) {
+      int st = k_ready(0);
+      if (st < 0) return false;
+      tc_fence_after();
+      if (e0 > 0) mma.qk(0, 0, st);
+      mma.qk(1, 1, st);
+      umma_commit(&bars.empty[st]);
+      if (n == 1) umma_commit(bars.qempty);
+      for (int j = 0; j < n; ++j) {
+        int sv = -1, sk = -1;
+#pragma unroll
+        for (int wg = 0; wg < 2; ++wg) {
+          const int e = wg == 0 ? e0 : n;
+          if (j < e) {
+            if (!p_ready(wg)) return false;
+            if (sv < 0 && (sv = v_ready(j)) < 0) return false;
+            tc_fence_after();
+            mma.pv(wg, sv, j > 0);
+            if (j == e - 1) umma_commit(&bars.ofull[wg]);
+          }
+          if (j + 1 < e) {
+            if (sk < 0 && (sk = k_ready(j + 1)) < 0) return false;
+            tc_fence_after();
+            mma.qk(wg, wg, sk);
+          }
+        }
+        umma_commit(&bars.empty[sv]);
+        if (j + 1 < n) umma_commit(&bars.empty[sk]);
+        if (j + 2 == n) umma_commit(bars.qempty);
+      }
+    } else {
+      for (int j = 0; j < min(n, 2); ++j) {
+        const int st = k_ready(j);
+        if (st < 0) return false;
+        tc_fence_after();
+        mma.qk(j, 0, st);
+        umma_commit(&bars.empty[st]);
+      }
+      if (n <= 2) umma_commit(bars.qempty);
+      for (int j = 0; j < n; ++j) {
+        const int wg = j & 1;
+        if (!p_ready(wg)) return false;
+        const int sv = v_ready(j);
+        if (sv < 0) return false;
+        tc_fence_after();
+        mma.pv(wg, sv, j > 1);
+        if (j >= n - 2) umma_commit(&bars.ofull[wg]);
+        umma_commit(&bars.empty[sv]);
+        if (j + 2 < n) {
+          const int sk = k_ready(j + 2);
+          if (sk < 0) return false;
+          tc_fence_after();
+          mma.qk(wg, 0, sk);
+          umma_commit(&bars.empty[sk]);
+          if (j + 3 == n) umma_commit(bars.qempty);
+        }
+      }
+    }
+    tiles += n;
+  }
+}
+
+// ------------------------------------------------------------ V checks
+// Warp `half` of two owns half of the dimensions of every checked V tile.
+template <int HD>
+__device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars& bars,
+                                           const Unit* units, int* note_flags, uint16_t* notes_s,
+                                           uint8_t* ring, int half, int lane) {
+  using Lay = ChunkLayout<HD>;
+  constexpr int NST = Lay::kStages;
+  constexpr int CPW = HD / 16;       // 16-byte pieces of a row per warp
+  constexpr int RPI = 32 / CPW;      // rows per pass
+  uint32_t tiles = 0, landed = 0;
+  for (uint32_t u = 0;; ++u) {
+    const int slot = u & 1;
+    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
+    const Unit un = units[slot];
+    if (un.kt0 == un.kt1) return;
+    uint16_t* notes = notes_s + slot * 3 * HD;
+    bool noting = false;
+    if (lane == 0) note_flags[slot * 2 + half] = 0;
+    // the checked tiles are the last ones, from the first that has a position
+    // past the first row's
+    const int from = max(un.kt0, un.pos0 < 0 ? 0 : (un.pos0 + 1) / kTile);
+    for (int kt = from; kt < un.kt1; ++kt) {
+      const uint32_t st = (2 * (tiles + kt - un.kt0) + 1) % NST;
+      if (!chunk_wait_warp(&bars.landed[st], (landed >> st) & 1, p)) return;
+      landed ^= 1u << st;
+      uint8_t* tile = ring + st * Lay::kStageBytes;
+      const int ch = half * CPW + lane % CPW;  // piece of the row
+      bool bad = false;
+#pragma unroll 4
+      for (int r0 = 0; r0 < kTile; r0 += RPI) {
+        const int row = r0 + lane / CPW, pos = kt * kTile + row;
+        uint4* at = reinterpret_cast<uint4*>(tile + sw128_offset(row, ch, kTile));
+        if (pos >= un.len) {
+          *at = make_uint4(0u, 0u, 0u, 0u);
+        } else if (pos > un.pos0) {
+          const uint4 v = *at;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            bad |= (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
+        }
+      }
+      if (__any_sync(0xffffffffu, bad)) {
+        if (!noting) {  // clear this warp's notes: no position sees them
+          for (int c = lane; c < 3 * HD / 2; c += 32)
+            notes[c / (HD / 2) * HD + half * (HD / 2) + c % (HD / 2)] = 0xffff;
+          noting = true;
+          if (lane == 0) note_flags[slot * 2 + half] = 1;
+        }
+        __syncwarp();
+        // a lane per dimension, rows in order
+        for (int c = half * (HD / 2) + lane; c < (half + 1) * (HD / 2); c += 32) {
+          for (int row = 0; row < kTile; ++row) {
+            const int pos = kt * kTile + row;
+            if (pos <= un.pos0 || pos >= un.len) continue;
+            uint16_t* e = reinterpret_cast<uint16_t*>(tile + sw128_offset(row, c >> 3, kTile)) + (c & 7);
+            const uint16_t x = *e;
+            if ((x & 0x7f80) != 0x7f80) continue;
+            const int kind = (x & 0x7f) ? 0 : x & 0x8000 ? 2 : 1;
+            const int rel = min(pos - un.pos0, 0xfffe);
+            if (rel < notes[kind * HD + c]) notes[kind * HD + c] = (uint16_t)rel;
+            *e = 0;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.clean[st]);
+    }
+    tiles += un.kt1 - un.kt0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.uempty[slot]);
+  }
+}
+
+// -------------------------------------------------------------- the CTA's share
+struct Share {
+  long long unit_at;  // line position where the first unit begins
+  long long x1;       // end of the share on the line
+  int share, b, h, rt, kt0;
+};
+
+// Every CTA finds where its share of the line begins.  `cost` is scratch for
+// the batch (position tiles of one KV head of each sequence, then their
+// running sums over the line).
+__device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost, Share* out) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int tu = 2 * (kTile / p.group);
+  for (int b0 = tid - lane; b0 < p.batch; b0 += kChunkThreads) {
+    const int b = b0 + lane;
+    int q0 = 0, n = 0, len = 0;
+    if (b < p.batch && !sequence_of(p, b, q0, n, len) && blockIdx.x == 0)
+      flag_error(p.error_flag, VG_DEVERR_LENGTH);
+    const int nrt = (int)(((long long)n + tu - 1) / tu);
+    long long c = 0;
+    if (nrt <= 4)
+      for (int rt = 0; rt < nrt; ++rt) c += unit_tiles(n, len, tu, rt);
+    uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4);
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int sn = __shfl_sync(0xffffffffu, n, src), sl = __shfl_sync(0xffffffffu, len, src);
+      const int sr = __shfl_sync(0xffffffffu, nrt, src);
+      long long s = 0;
+      for (int rt = lane; rt < sr; rt += 32) s += unit_tiles(sn, sl, tu, rt);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == src) c = s;
+    }
+    if (b < p.batch) cost[b] = c;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    long long total = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      long long v = b < p.batch ? cost[b] * p.num_kv_heads : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+      }
+      v += total;
+      if (b < p.batch) cost[b] = v;
+      total = __shfl_sync(0xffffffffu, v, 31);
+    }
+    __syncwarp();
+    const long long share = (total + gridDim.x - 1) / gridDim.x;
+    const long long x0 = share * blockIdx.x;
+    Share s = {};
+    s.share = (int)share;
+    s.x1 = min(total, x0 + share);
+    s.b = -1;
+    if (x0 < total) {
+      int b = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const uint32_t past = __ballot_sync(0xffffffffu, b0 + lane < p.batch && cost[b0 + lane] > x0);
+        if (past) {
+          b = b0 + __ffs(past) - 1;
+          break;
+        }
+      }
+      const long long base = b > 0 ? cost[b - 1] : 0;
+      const long long per_head = (cost[b] - base) / p.num_kv_heads;
+      const int h = (int)((x0 - base) / per_head);
+      const long long y = x0 - base - h * per_head;
+      int q0, n, len;
+      sequence_of(p, b, q0, n, len);
+      const int nrt = (int)(((long long)n + tu - 1) / tu);
+      long long before = 0;  // tiles of the row tiles before rt0
+      int rt = 0;
+      for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
+        const long long own = rt0 + lane < nrt ? unit_tiles(n, len, tu, rt0 + lane) : 0;
+        long long v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long w = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += w;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + v > y);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          rt = rt0 + l;
+          before += __shfl_sync(0xffffffffu, v - own, l);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, v, 31);
+      }
+      s.b = b;
+      s.h = h;
+      s.rt = rt;
+      s.kt0 = (int)(y - before);
+      s.unit_at = x0 - s.kt0;
+    }
+    if (lane == 0) *out = s;
+  }
+  __syncthreads();
+}
+
+// ----------------------------------------------------------------- producer
+// Walks the CTA's units, publishes them and streams their Q, K and V.  On a
+// wait that was given up it stops, then waits (bounded) for its own copies.
+template <int HD>
+__device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkBars& bars,
+                                              const Share& s, const CUtensorMap& tmq,
+                                              const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                              Unit* units, uint8_t* smem, int lane) {
+  using Lay = ChunkLayout<HD>;
+  constexpr int NST = Lay::kStages;
+  constexpr int kBoxes = Lay::kHalves * kPagesPerTile;  // TMA boxes of a tile
+  const int g = p.group, tt = kTile / g, tu = 2 * tt;
+  const uint64_t keep = l2_policy_evict_first();
+  uint8_t* ring = smem + Lay::kRing;
+  const int pi = lane & 7, dh = lane >> 3;
+  int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
+  long long at = s.unit_at;  // line position of the current unit's first tile
+  int q0, n, len;
+  sequence_of(p, b, q0, n, len);
+  uint32_t ri = 0, u = 0, full = 0, landed = 0;
+  bool live = true;
+  MergeUnit cut = {};
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    int go = 1;
+    if (lane == 0) go = chunk_wait(bar, parity, p);
+    return __shfl_sync(0xffffffffu, go, 0) != 0;
+  };
+  while (live) {
+    const bool more = at + kt0 < s.x1;
+    const int slot = u & 1;
+    if (u >= 2 && !wait(&bars.uempty[slot], ((u >> 1) - 1) & 1)) {
+      live = false;
+      break;
+    }
+    Unit un = {};
+    if (more) {
+      un.tok0 = q0 + rt * tu;
+      un.ntok = min(tu, n - rt * tu);
+      un.pos0 = len - n + rt * tu;
+      un.len = len;
+      un.h = h;
+      un.two = un.ntok > tt;
+      un.n0 = tiles_to(un.pos0 + min(tt, un.ntok) - 1);
+      const int tiles = tiles_to(un.pos0 + un.ntok - 1);
+      un.kt0 = kt0;
+      un.kt1 = (int)min((long long)tiles, s.x1 - at);
+      un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
+      if (kt0 == 0 && un.kt1 < tiles) {
+        cut.parts = (int)((at + tiles - 1) / s.share) - (int)blockIdx.x + 1;
+        cut.tok0 = un.tok0;
+        cut.ntok = un.ntok;
+        cut.h = h;
+      }
+      at += tiles;  // the next unit's
+    }
+    if (lane == 0) {
+      units[slot] = un;
+      mbar_arrive(&bars.ufull[slot]);
+    }
+    __syncwarp();
+    if (!more) break;
+    // page ids of four tiles at a time, one per lane
+    const int npages = (len + kPageSize - 1) / kPageSize;
+    auto fetch = [&](int kt) -> int {
+      const int lp = kt * kPagesPerTile + lane;
+      if (lp >= npages || kt + (lane >> 3) >= un.kt1) return p.num_pages;  // zeros
+      const int id = p.page_table[(size_t)b * p.width + lp];
+      if (id >= 0 && id < p.num_pages) return id;
+      flag_error(p.error_flag, VG_DEVERR_PAGE);
+      return p.num_pages;
+    };
+    int ids = fetch(un.kt0), ids_next = fetch(un.kt0 + 4);
+    if (u >= 1 && !wait(bars.qempty, (u - 1) & 1)) {
+      live = false;
+      break;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kHalves * tt * g * 128);
+      for (int t = 0; t < (un.two ? 2 : 1); ++t)
+        for (int x = 0; x < Lay::kHalves; ++x)
+          tma_load_3d(smem + t * Lay::kQBytes + x * Lay::kHalfBytes, &tmq, bars.qfull, x * 64, h * g,
+                      un.tok0 + t * tt);
+    }
+    __syncwarp();
+    for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
+      const int w = (kt - un.kt0) & 3;
+      if (w == 0 && kt > un.kt0) {
+        ids = ids_next;
+        ids_next = fetch(kt + 4);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, w * 8 + pi);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t st = ri % NST;
+        if (ri >= NST && !wait(&bars.empty[st], ((ri / NST) - 1) & 1)) {
+          live = false;
+          break;
+        }
+        uint64_t* bar = &(v && checked_tile(un, kt) ? bars.landed : bars.full)[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, Lay::kStageBytes);
+        __syncwarp();
+        if (lane < kBoxes)
+          tma_load_4d(ring + st * Lay::kStageBytes + dh * Lay::kHalfBytes + pi * kPageSize * 128,
+                      v ? &tmv : &tmk, bar, dh * 64, 0, h, id, keep);
+        __syncwarp();
+        if (bar == &bars.full[st])
+          full ^= 1u << st;
+        else
+          landed ^= 1u << st;
+        ++ri;
+      }
+    }
+    ++u;
+    kt0 = 0;
+    if (++rt * tu >= n) {
+      rt = 0;
+      if (++h == p.num_kv_heads) {
+        h = 0;
+        do {
+          if (++b >= p.batch) break;
+          sequence_of(p, b, q0, n, len);
+        } while (n == 0);
+      }
+    }
+  }
+  if (lane == 0) {
+    p.merge[blockIdx.x] = cut;
+    if (!live) {
+      for (int st = 0; st < NST; ++st) {
+        mbar_wait(&bars.full[st], ((full >> st) & 1) ^ 1);
+        mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
+      }
+      if (u > 0) mbar_wait(bars.qfull, (u - 1) & 1);
+    }
+  }
+  __syncwarp();
 }
 
 template <int HD>
-cudaError_t launch_rows(const ChunkParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                 const __grid_constant__ CUtensorMap tmv, const ChunkParams p) {
+  using Lay = ChunkLayout<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const ChunkBars bars = chunk_bars(reinterpret_cast<uint64_t*>(smem + Lay::kBars), Lay::kStages);
+  Unit* units = reinterpret_cast<Unit*>(smem + Lay::kUnits);
+  int* note_flags = reinterpret_cast<int*>(smem + Lay::kFlags);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + Lay::kFlags + 16);
+  uint16_t* notes = reinterpret_cast<uint16_t*>(smem + Lay::kNotes);
+  float2* ml = reinterpret_cast<float2*>(smem + Lay::kMl);
+  if (warp == kProducer && lane == 0) {
+    tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the share is found in memory that the ring takes over afterwards
+  Share* share_s = reinterpret_cast<Share*>(smem + Lay::kMl);
+  find_share(p, reinterpret_cast<long long*>(smem), share_s);
+  const Share share = *share_s;
+  if (share.b < 0) {  // no work for this CTA
+    if (tid == 0) p.merge[blockIdx.x] = MergeUnit{};
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < Lay::kStages; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+      mbar_init(&bars.landed[i], 1);
+      mbar_init(&bars.clean[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.sfull[i], 1);
+      mbar_init(&bars.pfull[i], 4);
+      mbar_init(&bars.ofull[i], 1);
+      mbar_init(&bars.ufull[i], 1);
+      mbar_init(&bars.uempty[i], 8 + 1 + 2);
+    }
+    mbar_init(bars.qfull, 1);
+    mbar_init(bars.qempty, 1);
+    mbar_init(bars.xfull, 4);
+    mbar_init(bars.xdone, 4);
+    mbar_init(bars.drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == kMma) tmem_alloc(tmem_at, 512);
+  fence_proxy_async_smem();  // the scratch was written by ordinary stores, the ring is not
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  if (warp < 8) {
+    softmax_role<HD>(p, bars, units, note_flags, notes, ml, tmem, warp >> 2, warp, lane);
+  } else if (warp == kProducer) {
+    producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, smem, lane);
+  } else if (warp == kMma) {
+    if (lane == 0) {
+      const uint32_t base = smem_u32(smem);
+      if (!mma_role<HD>(p, bars, units, tmem, base + Lay::kRing, base)) {
+        // abandoned: wait (bounded) for every tensor-core operation issued
+        umma_commit(bars.drain);
+        mbar_wait(bars.drain, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    check_role<HD>(p, bars, units, note_flags, notes, smem + Lay::kRing, warp - kChecker, lane);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();  // every access to tensor memory of this CTA is done
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the units that several CTAs share: a warp per row, weights
+// 2^(m - max m) of the parts, which sit in slot 1 of the CTA where the unit
+// begins and in slot 0 of the following ones.
+constexpr int kMergeWarps = 8;
+
+template <int HD>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
+  constexpr int E = HD / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the partial
+  const MergeUnit mu = p.merge[c];
+  const int g = p.group, tt = kTile / g;
+  const int tile = row / kTile, r = row - tile * kTile, tok_r = r / g;
+  const int tok = mu.ntok > tt ? tile * tt + tok_r : tok_r;
+  if (mu.parts == 0 || tok_r >= tt || tok >= mu.ntok || (tile && mu.ntok <= tt)) return;
+  auto at = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.rows + row; };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float m = -INFINITY;
+  for (int i = lane; i < mu.parts; i += 32) m = fmaxf(m, __ldcg(&ml[at(i)]).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = safe_ref(m);
+  float l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i0 = 0; i0 < mu.parts; i0 += 32) {
+    float w_l = 0.f, l_l = 0.f;
+    if (i0 + lane < mu.parts) {
+      const float2 x = __ldcg(&ml[at(i0 + lane)]);
+      w_l = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
+      l_l = w_l * x.y;
+    }
+    if (w_l != 0.f) l += l_l;
+    const int n = min(32, mu.parts - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, w_l, i);
+      const float* src = p.part_o + at(i0 + i) * HD + lane * E;
+      float v[E];
+      if (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = x.x, v[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = w != 0.f ? fmaf(w, v[e], acc[e]) : acc[e];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
+  const int t = mu.tok0 + tok, qh = mu.h * g + r - tok_r * g;
+  __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(int64_t)t * p.num_q_heads + qh] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+struct ChunkPlan {
+  int grid, rows;
+  size_t off_ml, off_merge, bytes;
+};
+
+ChunkPlan make_chunk_plan(int num_tokens, int group, int head_dim) {
+  ChunkPlan pl;
+  pl.grid = device_sm_count();
+  pl.rows = num_tokens > kTile / group ? kRowsMax : kTile;  // one row tile holds every unit
+  const size_t rows = (size_t)pl.grid * 2 * pl.rows;
+  pl.off_ml = align_up(rows * head_dim * sizeof(float), 256);
+  pl.off_merge = align_up(pl.off_ml + rows * 2 * sizeof(float), 256);
+  pl.bytes = pl.off_merge + align_up(pl.grid * sizeof(MergeUnit), 256);
+  return pl;
+}
+
+template <int HD>
+cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const ChunkParams& p, cudaStream_t stream) {
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        chunk_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkLayout<HD>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)p.num_tokens * p.num_q_heads + kRowWarps - 1) / kRowWarps));
-  cfg.blockDim = dim3(kRowWarps * 32);
+  cfg.gridDim = dim3(pl.grid);
+  cfg.blockDim = dim3(kChunkThreads);
+  cfg.dynamicSmemBytes = ChunkLayout<HD>::kBytes;
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_rows_kernel<HD>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<HD>, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)p.num_tokens * p.group;  // no unit has more
+  cfg.gridDim = dim3(pl.grid, ceil_div((int)(rows < pl.rows && pl.rows == kTile ? rows : pl.rows), kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<HD>, p);
 }
 
 }  // namespace
@@ -112,8 +1024,11 @@ using namespace vg;
 
 extern "C" size_t vg_chunk_workspace_bytes(int batch, int num_tokens, int num_q_heads,
                                            int num_kv_heads, int head_dim) {
-  (void)batch, (void)num_tokens, (void)num_q_heads, (void)num_kv_heads, (void)head_dim;
-  return 0;
+  if (batch <= 0 || num_tokens <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
+  return make_chunk_plan(num_tokens, num_q_heads / num_kv_heads, head_dim).bytes;
 }
 
 extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, int64_t q_stride,
@@ -122,7 +1037,6 @@ extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, in
                                         void* out, int64_t out_stride, float* lse, void* workspace,
                                         size_t workspace_bytes, int32_t* error_flag,
                                         cudaStream_t stream) {
-  (void)workspace, (void)workspace_bytes;
   const vg_status st = check_paged_kv(kv);
   if (st != VG_OK) return st;
   if (!cu_q || !kv_lens || batch <= 0 || num_tokens < 0 || num_q_heads <= 0 ||
@@ -134,27 +1048,38 @@ extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, in
   if (!q || !out || (reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) ||
       q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
     return VG_ERR_INVALID_ARGUMENT;
-  if (num_q_heads / kv->num_kv_heads > 16 || batch > 4096 || kv->max_pages_per_seq > (1 << 26))
-    return VG_ERR_UNSUPPORTED;
+  const int g = num_q_heads / kv->num_kv_heads;
+  if (g > 16 || batch > kMaxBatch || kv->max_pages_per_seq > (1 << 26)) return VG_ERR_UNSUPPORTED;
+  const ChunkPlan pl = make_chunk_plan(num_tokens, g, kv->head_dim);
+  if (!workspace || workspace_bytes < pl.bytes) return VG_ERR_WORKSPACE_TOO_SMALL;
+  CUtensorMap tq, tk, tv;
+  if (!page_pool_tensor_map(kv->k_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tk) ||
+      !page_pool_tensor_map(kv->v_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tv) ||
+      !token_rows_tensor_map(q, num_tokens, num_q_heads, kv->head_dim, q_stride, g, kTile / g, &tq))
+    return VG_ERR_LAUNCH;
   ChunkParams p = {};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_pages = static_cast<const __nv_bfloat16*>(kv->k_pages);
-  p.v_pages = static_cast<const __nv_bfloat16*>(kv->v_pages);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.page_table = kv->page_table;
   p.cu_q = cu_q;
   p.kv_lens = kv_lens;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pl.off_ml);
+  p.merge = reinterpret_cast<MergeUnit*>(ws + pl.off_merge);
   p.error_flag = error_flag;
-  p.q_stride = q_stride;
   p.out_stride = out_stride;
+  p.wait_ns = wait_report_ns();
   p.scale_log2 = softmax_scale * kLog2e;
   p.batch = batch;
   p.num_tokens = num_tokens;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = kv->num_kv_heads;
+  p.group = g;
   p.num_pages = kv->num_pages;
   p.width = kv->max_pages_per_seq;
-  const cudaError_t e = kv->head_dim == 128 ? launch_rows<128>(p, stream) : launch_rows<64>(p, stream);
+  p.rows = pl.rows;
+  const cudaError_t e = kv->head_dim == 128 ? launch_chunk<128>(pl, tq, tk, tv, p, stream)
+                                             : launch_chunk<64>(pl, tq, tk, tv, p, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }

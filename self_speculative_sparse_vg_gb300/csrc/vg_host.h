@@ -28,6 +28,13 @@ uint64_t wait_report_ns();
 bool page_pool_tensor_map(const void* base, int num_pages, int num_kv_heads, int head_dim,
                           CUtensorMap* out);
 
+// 3-D tiled TMA descriptor over packed token rows [num_tokens][num_heads]
+// [head_dim] bf16 with token_stride elements between tokens, box = 64 dims x
+// box_heads x box_tokens with the 128-byte swizzle (tokens past the end read
+// zeros).  Made anew on every call.
+bool token_rows_tensor_map(const void* base, int num_tokens, int num_heads, int head_dim,
+                           int64_t token_stride, int box_heads, int box_tokens, CUtensorMap* out);
+
 // Basic checks of a vg_paged_kv; VG_OK or an error status.
 vg_status check_paged_kv(const vg_paged_kv* kv);
 

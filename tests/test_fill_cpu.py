@@ -83,6 +83,11 @@ def test_chunk_attention_refusals(vg):
     assert call(hq=136, qs=136 * 128, os=136 * 128) == 2 and call(b=4097) == 2
     assert call(kv=_kv(vg, head_dim=256)) == 2 and call(kv=_kv(vg, k=0x1008)) == 1
     assert call(n=0) == 0
+    need = vg._lib.vg_chunk_workspace_bytes(2, 5, 32, 8, 128)
+    assert need > 0 and call() == 3 and call(ws=FAKE, wsb=need - 1) == 3
+    for bad in ((0, 5, 32, 8, 128), (2, 0, 32, 8, 128), (2, 5, 33, 8, 128), (2, 5, 32, 8, 96),
+                (2, 5, 136, 8, 128)):
+        assert vg._lib.vg_chunk_workspace_bytes(*bad) == 0, bad
 
 
 def test_binding_refusals(vg):

@@ -263,3 +263,13 @@ def test_length_shorter_than_the_cache():
     """kv_lens cuts the cache: later slots of the same pages are not seen."""
     c = Cache([250, 90], 2, 128, seed=16)
     check_chunk(c, [20, 33], 8, kv_lens=[131, 33])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 64), (2, 1, 128)])
+def test_long_shares(Hq, Hkv, d):
+    """Enough positions that every CTA streams many tiles (its ring goes round
+    many times) before the ones that need care: ends of sequences inside a
+    tile, the diagonal of a chunk, single tokens beside chunks."""
+    lens = [29999, 30001, 23456, 30000, 27777, 31000, 12345, 30123]
+    new = [1, 1, 70, 1, 33, 1, 6, 300 // Hq]
+    check_chunk(Cache(lens, Hkv, d, seed=17), new, Hq)
