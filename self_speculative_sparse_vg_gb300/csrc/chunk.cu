@@ -160,8 +160,8 @@ __device__ __forceinline__ int unit_tiles(int n, int len, int tu, int rt) {
 
 // Whether some row of the unit does not attend all of tile kt (its first row
 // ends before the tile does): V is then checked.
-__device__ __forceinline__ bool checked_tile(const Unit& un, int kt) {
-  return kt * kTile + kTile - 1 > un.pos0;
+__device__ __forceinline__ bool checked_tile(int pos0, int kt) {
+  return kt * kTile + kTile - 1 > pos0;
 }
 
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
@@ -385,125 +385,143 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
 }
 
 // ------------------------------------------------------- tensor-core issue
+// The warp runs in step (every value it uses is the same in all lanes) and an
+// elected lane issues.
 template <int HD>
 struct MmaIssuer {
   using Lay = ChunkLayout<HD>;
-  const ChunkParams& p;
   const ChunkBars& bars;
-  uint32_t tmem, ring, q;
+  uint32_t tmem, ring_lo, q_lo, v_lo;  // low descriptor words of stage 0 and of Q
   static constexpr uint32_t kIdQk = umma_idesc_bf16(kTile, kTile, 0, 0);
   static constexpr uint32_t kIdPv = umma_idesc_bf16(kTile, HD, 0, 1);
+  static constexpr uint32_t kHi = umma_desc_hi(1024);
 
   // S of warpgroup `wg` = Q (row tile qt) K^T of the stage
-  __device__ __forceinline__ void qk(int wg, int qt, int stage) {
-    const uint32_t kb = ring + stage * Lay::kStageBytes, qb = q + qt * Lay::kQBytes;
+  __device__ __forceinline__ void qk(int wg, int qt, uint32_t stage) {
+    const uint32_t k = ring_lo + stage * (Lay::kStageBytes >> 4);
+    const uint32_t q = q_lo + qt * (Lay::kQBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
-      const uint32_t off = (ks >> 2) * Lay::kHalfBytes + (ks & 3) * 32;
-      umma_bf16(tmem + Lay::kSCol + wg * kTile, umma_smem_desc(qb + off, 16, 1024),
-                umma_smem_desc(kb + off, 16, 1024), kIdQk, ks > 0);
+      const uint32_t off = ((ks >> 2) * Lay::kHalfBytes + (ks & 3) * 32) >> 4;
+      umma_bf16_elect(tmem + Lay::kSCol + wg * kTile, q + off, kHi, k + off, kHi, kIdQk, ks > 0);
     }
-    umma_commit(&bars.sfull[wg]);
+    umma_commit_elect(&bars.sfull[wg]);
   }
   // O of warpgroup `wg` (+)= P V of the stage
-  __device__ __forceinline__ void pv(int wg, int stage, bool accumulate) {
-    const uint32_t vb = ring + stage * Lay::kStageBytes;
+  __device__ __forceinline__ void pv(int wg, uint32_t stage, bool accumulate) {
+    const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
-      umma_bf16_ts(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
-                   umma_smem_desc(vb + ks * 16 * 128, Lay::kHalfBytes, 1024), kIdPv,
-                   accumulate || ks > 0);
+      umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
+                         v + ks * (16 * 128 >> 4), kHi, kIdPv, accumulate || ks > 0);
   }
 };
 
 template <int HD>
 __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& bars,
-                                         const Unit* units, uint32_t tmem, uint32_t ring, uint32_t q) {
+                                         const Unit* units, uint32_t tmem, uint32_t ring, uint32_t q,
+                                         int lane) {
   using Lay = ChunkLayout<HD>;
-  constexpr int NST = Lay::kStages;
-  MmaIssuer<HD> mma{p, bars, tmem, ring, q};
-  uint32_t pc[2] = {0, 0}, full = 0, clean = 0;  // parities
-  uint32_t tiles = 0;                            // position tiles before this unit
+  constexpr uint32_t NST = Lay::kStages;
+  MmaIssuer<HD> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
+                    umma_desc_lo(ring, Lay::kHalfBytes)};
+  uint32_t pc0 = 0, pc1 = 0, full = 0, clean = 0;  // parities
+  uint32_t at = 0;                                 // stage of the unit's first K tile
+  auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
-    if (!chunk_wait(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
-    const Unit un = units[slot];
-    mbar_arrive(&bars.uempty[slot]);
-    if (un.kt0 == un.kt1) return true;
-    if (!chunk_wait(bars.qfull, u & 1, p)) return false;
-    const int n = un.kt1 - un.kt0;
-    const int e0 = un.two ? min(un.kt1, un.n0) - un.kt0 : n;  // tiles of warpgroup 0 (two row tiles)
-    // The stage of the unit's j-th K or V tile once it may be read, or -1.
-    auto ready = [&](uint32_t i, uint64_t* bar, uint32_t& parity) -> int {
-      const uint32_t st = i % NST, par = (parity >> st) & 1;
-      parity ^= 1u << st;
-      return chunk_wait(&bar[st], par, p) ? (int)st : -1;
+    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
+    const int kt0 = same(units[slot].kt0), kt1 = same(units[slot].kt1), n0 = same(units[slot].n0);
+    const int pos0 = same(units[slot].pos0), two = same(units[slot].two);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.uempty[slot]);
+    if (kt0 == kt1) return true;
+    if (!chunk_wait_warp(bars.qfull, u & 1, p)) return false;
+    const int n = kt1 - kt0;
+    const int e0 = two ? min(kt1, n0) - kt0 : n;  // tiles of warpgroup 0 (two row tiles)
+    // Ring entries are K(0), V(0), K(1), V(1) ...: waits for the entry at
+    // stage st (V tiles that are checked: until they are clean).
+    auto k_ready = [&](uint32_t st) {
+      const uint32_t par = (full >> st) & 1;
+      full ^= 1u << st;
+      return chunk_wait_warp(&bars.full[st], par, p);
     };
-    auto k_ready = [&](int j) { return ready(2 * (tiles + j), bars.full, full); };
-    auto v_ready = [&](int j) {
-      return checked_tile(un, un.kt0 + j) ? ready(2 * (tiles + j) + 1, bars.clean, clean)
-                                          : ready(2 * (tiles + j) + 1, bars.full, full);
+    auto v_ready = [&](uint32_t st, int j) {
+      if (!checked_tile(pos0, kt0 + j)) return k_ready(st);
+      const uint32_t par = (clean >> st) & 1;
+      clean ^= 1u << st;
+      return chunk_wait_warp(&bars.clean[st], par, p);
     };
-    auto p_ready = [&](int wg) { return chunk_wait(&bars.pfull[wg], pc[wg]++ & 1, p); };
-    if (un.two) {
-      int st = k_ready(0);
-      if (st < 0) return false;
+    auto after = [](uint32_t st, uint32_t by) { return st + by >= NST ? st + by - NST : st + by; };
+    uint32_t st = at;  // K(j)'s stage
+    if (two) {
+      if (!k_ready(st)) return false;
       tc_fence_after();
       if (e0 > 0) mma.qk(0, 0, st);
       mma.qk(1, 1, st);
-      umma_commit(&bars.empty[st]);
-      if (n == 1) umma_commit(bars.qempty);
+      umma_commit_elect(&bars.empty[st]);
+      if (n == 1) umma_commit_elect(bars.qempty);
       for (int j = 0; j < n; ++j) {
-        int sv = -1, sk = -1;
-#pragma unroll
-        for (int wg = 0; wg < 2; ++wg) {
-          const int e = wg == 0 ? e0 : n;
-          if (j < e) {
-            if (!p_ready(wg)) return false;
-            if (sv < 0 && (sv = v_ready(j)) < 0) return false;
+        const uint32_t sv = after(st, 1), sk = after(st, 2);
+        const bool more = j + 1 < n;
+        bool v_in = false, k_in = false;
+        if (j < e0) {
+          if (!chunk_wait_warp(&bars.pfull[0], pc0++ & 1, p) || !v_ready(sv, j)) return false;
+          v_in = true;
+          tc_fence_after();
+          mma.pv(0, sv, j > 0);
+          if (j == e0 - 1) umma_commit_elect(&bars.ofull[0]);
+          if (j + 1 < e0) {
+            if (!k_ready(sk)) return false;
+            k_in = true;
             tc_fence_after();
-            mma.pv(wg, sv, j > 0);
-            if (j == e - 1) umma_commit(&bars.ofull[wg]);
-          }
-          if (j + 1 < e) {
-            if (sk < 0 && (sk = k_ready(j + 1)) < 0) return false;
-            tc_fence_after();
-            mma.qk(wg, wg, sk);
+            mma.qk(0, 0, sk);
           }
         }
-        umma_commit(&bars.empty[sv]);
-        if (j + 1 < n) umma_commit(&bars.empty[sk]);
-        if (j + 2 == n) umma_commit(bars.qempty);
+        if (!chunk_wait_warp(&bars.pfull[1], pc1++ & 1, p)) return false;
+        if (!v_in && !v_ready(sv, j)) return false;
+        tc_fence_after();
+        mma.pv(1, sv, j > 0);
+        umma_commit_elect(&bars.empty[sv]);
+        if (!more) umma_commit_elect(&bars.ofull[1]);
+        if (more) {
+          if (!k_in && !k_ready(sk)) return false;
+          tc_fence_after();
+          mma.qk(1, 1, sk);
+          umma_commit_elect(&bars.empty[sk]);
+          if (j + 2 == n) umma_commit_elect(bars.qempty);
+        }
+        st = sk;
       }
     } else {
       for (int j = 0; j < min(n, 2); ++j) {
-        const int st = k_ready(j);
-        if (st < 0) return false;
+        const uint32_t sk = after(st, 2 * j);
+        if (!k_ready(sk)) return false;
         tc_fence_after();
-        mma.qk(j, 0, st);
-        umma_commit(&bars.empty[st]);
+        mma.qk(j, 0, sk);
+        umma_commit_elect(&bars.empty[sk]);
       }
-      if (n <= 2) umma_commit(bars.qempty);
+      if (n <= 2) umma_commit_elect(bars.qempty);
       for (int j = 0; j < n; ++j) {
         const int wg = j & 1;
-        if (!p_ready(wg)) return false;
-        const int sv = v_ready(j);
-        if (sv < 0) return false;
+        const uint32_t sv = after(st, 1);
+        if (!chunk_wait_warp(&bars.pfull[wg], (wg ? pc1++ : pc0++) & 1, p) || !v_ready(sv, j)) return false;
         tc_fence_after();
         mma.pv(wg, sv, j > 1);
-        if (j >= n - 2) umma_commit(&bars.ofull[wg]);
-        umma_commit(&bars.empty[sv]);
+        if (j >= n - 2) umma_commit_elect(&bars.ofull[wg]);
+        umma_commit_elect(&bars.empty[sv]);
         if (j + 2 < n) {
-          const int sk = k_ready(j + 2);
-          if (sk < 0) return false;
+          const uint32_t sk = after(st, 4);
+          if (!k_ready(sk)) return false;
           tc_fence_after();
           mma.qk(wg, 0, sk);
-          umma_commit(&bars.empty[sk]);
-          if (j + 3 == n) umma_commit(bars.qempty);
+          umma_commit_elect(&bars.empty[sk]);
+          if (j + 3 == n) umma_commit_elect(bars.qempty);
         }
+        st = after(st, 2);
       }
     }
-    tiles += n;
+    at = st;
   }
 }
 
@@ -785,7 +803,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
           live = false;
           break;
         }
-        uint64_t* bar = &(v && checked_tile(un, kt) ? bars.landed : bars.full)[st];
+        uint64_t* bar = &(v && checked_tile(un.pos0, kt) ? bars.landed : bars.full)[st];
         if (lane == 0) mbar_arrive_expect_tx(bar, Lay::kStageBytes);
         __syncwarp();
         if (lane < kBoxes)
@@ -885,13 +903,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp == kProducer) {
     producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, smem, lane);
   } else if (warp == kMma) {
-    if (lane == 0) {
-      const uint32_t base = smem_u32(smem);
-      if (!mma_role<HD>(p, bars, units, tmem, base + Lay::kRing, base)) {
-        // abandoned: wait (bounded) for every tensor-core operation issued
-        umma_commit(bars.drain);
-        mbar_wait(bars.drain, 0);
-      }
+    const uint32_t base = smem_u32(smem);
+    if (!mma_role<HD>(p, bars, units, tmem, base + Lay::kRing, base, lane)) {
+      // abandoned: wait (bounded) for every tensor-core operation issued
+      umma_commit_elect(bars.drain);
+      if (lane == 0) mbar_wait(bars.drain, 0);
     }
     __syncwarp();
   } else {
