@@ -97,7 +97,7 @@ struct ChunkLayout {
   static constexpr int kSmall = kRing + kStages * kStageBytes;
   // small area: barriers, units, (m, l) exchange, non-finite notes
   static constexpr int kBars = kSmall;
-  static constexpr int kBarCount = 4 * kStages + 15;
+  static constexpr int kBarCount = 4 * kStages + 17;
   static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
   static constexpr int kFlags = kUnits + 2 * 48;
   static constexpr int kNotes = kFlags + 32;
@@ -115,7 +115,8 @@ struct ChunkBars {
   // only, so their parities are counted per stage (a bit mask), and whoever
   // waits on one of them waits for every phase of it.
   uint64_t *full, *landed, *clean, *empty;  // [stages]
-  uint64_t *sfull, *pfull, *ofull;         // [2]
+  uint64_t *sfull, *ofull;                 // [2]: S, all of O of a warpgroup
+  uint64_t *pfull;                         // [4]: halves of P of a warpgroup
   uint64_t *qfull, *qempty, *ufull, *uempty, *xfull, *xdone, *drain;
 };
 
@@ -128,14 +129,14 @@ __device__ __forceinline__ ChunkBars chunk_bars(uint64_t* b, int stages) {
   b += 4 * stages;
   r.sfull = b;
   r.pfull = b + 2;
-  r.ofull = b + 4;
-  r.ufull = b + 6;
-  r.uempty = b + 8;
-  r.qfull = b + 10;
-  r.qempty = b + 11;
-  r.xfull = b + 12;
-  r.xdone = b + 13;
-  r.drain = b + 14;
+  r.ofull = b + 6;
+  r.ufull = b + 8;
+  r.uempty = b + 10;
+  r.qfull = b + 12;
+  r.qempty = b + 13;
+  r.xfull = b + 14;
+  r.xdone = b + 15;
+  r.drain = b + 16;
   return r;
 }
 
@@ -184,6 +185,33 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       : "memory");
 }
 
+// Two floats in one 64-bit register, and operations on both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A V entry with its non-finite value given back: rel = the row's token within
 // the unit, notes = first token distance of a NaN, +inf, -inf in dimension c.
 template <int HD>
@@ -226,33 +254,23 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
       ++sc;
       tc_fence_after();
       if (rows) {
-        uint32_t a[64], b[64];
-        tmem_ld64(scol, a);
-        tmem_ld64(scol + 64, b);
+        uint32_t s[2][64];
+        tmem_ld64(scol, s[0]);
+        tmem_ld64(scol + 64, s[1]);
         const int rem = lim - kt * kTile;  // last attended column
-        const bool whole = __all_sync(0xffffffffu, rem >= kTile - 1 || !valid);
-        if (!whole) {
+        if (!__all_sync(0xffffffffu, rem >= kTile - 1 || !valid)) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j > rem) a[j] = 0xff800000u;
+          for (int j = 0; j < kTile; ++j)
+            if (j > rem) s[j >> 6][j & 63] = 0xff800000u;  // -inf
         }
-        float mx[8];
+        float mx[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(a[j]);
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
 #pragma unroll
-        for (int j = 8; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(a[j]));
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j + 64 > rem) b[j] = 0xff800000u;
-        }
-#pragma unroll
-        for (int j = 0; j < 64; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(b[j]));
-#pragma unroll
-        for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-          for (int j = 0; j < w; ++j) mx[j] = fmaxf(mx[j], mx[j + w]);
-        const float m_tile = mx[0] * p.scale_log2;  // scale > 0: the maximum commutes with it
+        for (int j = 4; j < 64; ++j)
+          mx[j & 3] = max3(mx[j & 3], __uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
+        // scale > 0: the maximum commutes with it
+        const float m_tile = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
         const bool need = m_tile > m_used + kRescale;
         if (__any_sync(0xffffffffu, need)) {
           const float mn = need ? m_tile : m_used;
@@ -271,30 +289,41 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
           }
           m_used = mn;
         }
+        // P = 2^(s scale - m), handed over in two halves so that the product
+        // with V starts while the second half is computed
         const float nref = -safe_ref(m_used);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nref2 = pair(nref, nref);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int e = (q & 1) * 32 + 2 * j;
-            const float s0 = __uint_as_float(q < 2 ? a[e] : b[e]);
-            const float s1 = __uint_as_float(q < 2 ? a[e + 1] : b[e + 1]);
-            const float p0 = ex2(fmaf(s0, p.scale_log2, nref));
-            const float p1 = ex2(fmaf(s1, p.scale_log2, nref));
-            acc[(j & 1) * 2] += p0;
-            acc[(j & 1) * 2 + 1] += p1;
-            pk[j] = pack_bf16(p0, p1);
+          for (int j = 0; j < 32; ++j) {
+            float2 x = unpair(fma2(pair(__uint_as_float(s[h][2 * j]), __uint_as_float(s[h][2 * j + 1])), scale2, nref2));
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            pk[j] = pack_bf16(x.x, x.y);
+            s[h][2 * j] = __float_as_uint(x.x);
+            s[h][2 * j + 1] = __float_as_uint(x.y);
           }
-          tmem_st16u(scol + q * 16, pk);
+          tmem_st32u(scol + h * 32, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.pfull[2 * wg + h]);
         }
-        lsum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        tmem_st_wait();
+        // the row sum, off the tensor cores' path
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          const uint32_t* x = &s[j >> 5][(j & 31) * 2];
+          acc[j & 3] = add2(acc[j & 3], pair(__uint_as_float(x[0]), __uint_as_float(x[1])));
+        }
+        const float2 sum = unpair(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+        lsum += sum.x + sum.y;
+      } else {
+        __syncwarp();
+        if (lane < 2) mbar_arrive(&bars.pfull[2 * wg + lane]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.pfull[wg]);
     }
     // -------- epilogue
     const bool has = end > first;
@@ -407,11 +436,11 @@ struct MmaIssuer {
     }
     umma_commit_elect(&bars.sfull[wg]);
   }
-  // O of warpgroup `wg` (+)= P V of the stage
-  __device__ __forceinline__ void pv(int wg, uint32_t stage, bool accumulate) {
+  // O of warpgroup `wg` (+)= P V of the stage, over half `half` of its positions
+  __device__ __forceinline__ void pv(int wg, uint32_t stage, int half, bool accumulate) {
     const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4);
 #pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks)
+    for (int ks = half * (kTile / 32); ks < (half + 1) * (kTile / 32); ++ks)
       umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
                          v + ks * (16 * 128 >> 4), kHi, kIdPv, accumulate || ks > 0);
   }
@@ -453,6 +482,18 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
       return chunk_wait_warp(&bars.clean[st], par, p);
     };
     auto after = [](uint32_t st, uint32_t by) { return st + by >= NST ? st + by - NST : st + by; };
+    // O(wg) (+)= P V: the first half of the positions while the warpgroup is
+    // still at the second
+    auto pv = [&](int wg, uint32_t sv, bool accumulate) {
+      const uint32_t par = (wg ? pc1++ : pc0++) & 1;
+      if (!chunk_wait_warp(&bars.pfull[2 * wg], par, p)) return false;
+      tc_fence_after();
+      mma.pv(wg, sv, 0, accumulate);
+      if (!chunk_wait_warp(&bars.pfull[2 * wg + 1], par, p)) return false;
+      tc_fence_after();
+      mma.pv(wg, sv, 1, true);
+      return true;
+    };
     uint32_t st = at;  // K(j)'s stage
     if (two) {
       if (!k_ready(st)) return false;
@@ -464,32 +505,24 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
       for (int j = 0; j < n; ++j) {
         const uint32_t sv = after(st, 1), sk = after(st, 2);
         const bool more = j + 1 < n;
-        bool v_in = false, k_in = false;
+        // the tiles are waited for first, while the warpgroups are at P(j)
+        if (!v_ready(sv, j) || (more && !k_ready(sk))) return false;
         if (j < e0) {
-          if (!chunk_wait_warp(&bars.pfull[0], pc0++ & 1, p) || !v_ready(sv, j)) return false;
-          v_in = true;
-          tc_fence_after();
-          mma.pv(0, sv, j > 0);
-          if (j == e0 - 1) umma_commit_elect(&bars.ofull[0]);
-          if (j + 1 < e0) {
-            if (!k_ready(sk)) return false;
-            k_in = true;
-            tc_fence_after();
+          if (!pv(0, sv, j > 0)) return false;
+          if (j + 1 < e0)
             mma.qk(0, 0, sk);
-          }
+          else
+            umma_commit_elect(&bars.ofull[0]);
         }
-        if (!chunk_wait_warp(&bars.pfull[1], pc1++ & 1, p)) return false;
-        if (!v_in && !v_ready(sv, j)) return false;
-        tc_fence_after();
-        mma.pv(1, sv, j > 0);
-        umma_commit_elect(&bars.empty[sv]);
-        if (!more) umma_commit_elect(&bars.ofull[1]);
+        if (!pv(1, sv, j > 0)) return false;
         if (more) {
-          if (!k_in && !k_ready(sk)) return false;
-          tc_fence_after();
           mma.qk(1, 1, sk);
+          umma_commit_elect(&bars.empty[sv]);
           umma_commit_elect(&bars.empty[sk]);
           if (j + 2 == n) umma_commit_elect(bars.qempty);
+        } else {
+          umma_commit_elect(&bars.ofull[1]);
+          umma_commit_elect(&bars.empty[sv]);
         }
         st = sk;
       }
@@ -504,14 +537,11 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
       if (n <= 2) umma_commit_elect(bars.qempty);
       for (int j = 0; j < n; ++j) {
         const int wg = j & 1;
-        const uint32_t sv = after(st, 1);
-        if (!chunk_wait_warp(&bars.pfull[wg], (wg ? pc1++ : pc0++) & 1, p) || !v_ready(sv, j)) return false;
-        tc_fence_after();
-        mma.pv(wg, sv, j > 1);
+        const uint32_t sv = after(st, 1), sk = after(st, 4);
+        if (!v_ready(sv, j) || !pv(wg, sv, j > 1)) return false;
         if (j >= n - 2) umma_commit_elect(&bars.ofull[wg]);
         umma_commit_elect(&bars.empty[sv]);
         if (j + 2 < n) {
-          const uint32_t sk = after(st, 4);
           if (!k_ready(sk)) return false;
           tc_fence_after();
           mma.qk(wg, 0, sk);
@@ -880,7 +910,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.sfull[i], 1);
-      mbar_init(&bars.pfull[i], 4);
+      mbar_init(&bars.pfull[2 * i], 4);
+      mbar_init(&bars.pfull[2 * i + 1], 4);
       mbar_init(&bars.ofull[i], 1);
       mbar_init(&bars.ufull[i], 1);
       mbar_init(&bars.uempty[i], 8 + 1 + 2);
@@ -898,6 +929,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  // The softmax warpgroups hold a row of S in registers: 208 for their threads,
+  // 80 for the others (256 * 208 + 128 * 80 of the launch's 384 * 168).
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
   if (warp < 8) {
     softmax_role<HD>(p, bars, units, note_flags, notes, ml, tmem, warp >> 2, warp, lane);
   } else if (warp == kProducer) {
