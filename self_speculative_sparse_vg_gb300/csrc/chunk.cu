@@ -9,7 +9,8 @@
 //    floor(128 / g) tokens of a tile times their g query heads, packed token
 //    by token, so K and V are read once for all heads of the group.  Its work
 //    is the 128-position tiles up to its last row's position.
-//  * All units' tiles form one line (sequence, KV head, row tiles), cut into
+//  * All units' tiles form one line (sequence, KV head, row tiles; a unit counts
+//    two tiles more, for its Q, its first scores and its epilogue), cut into
 //    equal shares, one per CTA: any mix of long prompts and single tokens is
 //    balanced to a tile.  KV heads outrank row tiles on the line so that the
 //    CTAs of a long prompt stream the same few heads, which L2 holds.  A unit
@@ -51,6 +52,7 @@ constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax)
 constexpr int kMaxBatch = 4096;
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that moves the reference
 constexpr int kRowsMax = 2 * kTile;    // rows of a unit
+constexpr int kUnitCost = 2;           // what a unit costs beside its position tiles, in tiles
 
 struct ChunkParams {
   const int32_t* page_table;
@@ -154,9 +156,10 @@ __device__ __forceinline__ bool sequence_of(const ChunkParams& p, int b, int& q0
   return ok;
 }
 
-// Position tiles of row-tile pair `rt` (tu tokens each) of a sequence.
-__device__ __forceinline__ int unit_tiles(int n, int len, int tu, int rt) {
-  return tiles_to(len - n + min((rt + 1) * tu, n) - 1);
+// Length on the line of row-tile pair `rt` (tu tokens each) of a sequence: its
+// overhead, then its position tiles.
+__device__ __forceinline__ int unit_length(int n, int len, int tu, int rt) {
+  return kUnitCost + tiles_to(len - n + min((rt + 1) * tu, n) - 1);
 }
 
 // Whether some row of the unit does not attend all of tile kt (its first row
@@ -352,7 +355,6 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
       }
     }
     if (rows && (un.two || wg == 0)) {
-      const bool noted_half[2] = {note_flags[slot * 2] != 0, note_flags[slot * 2 + 1] != 0};
       const uint16_t* notes = notes_s + slot * 3 * HD;
       const bool direct = un.part < 0;
       const int t = un.tok0 + tok, qh = un.h * g + head_r;
@@ -361,34 +363,43 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
       const float f_own = has ? w_own * inv : 0.f, f_other = w_other * inv;
       float* po = direct ? nullptr : p.part_o + ((size_t)un.part * p.rows + prow) * HD;
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 16) {
-        float o[16];
+      for (int c = 0; c < HD; c += 64) {
+        uint32_t o[64];
         if (has) {
-          tmem_ld16(ocol + c, o);
+          tmem_ld64(ocol + c, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= f_own;
+          for (int j = 0; j < 64; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own);
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0.f;
+          for (int j = 0; j < 64; ++j) o[j] = 0u;
         }
         if (other) {
-          float x[16];
-          tmem_ld16(ocol + HD + c, x);
+          uint32_t x[64];
+          tmem_ld64(ocol + HD + c, x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = fmaf(x[j], f_other, o[j]);
+          for (int j = 0; j < 64; ++j)
+            o[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f_other, __uint_as_float(o[j])));
         }
-        if (noted_half[c >= HD / 2]) {
+        if (note_flags[slot * 2] | note_flags[slot * 2 + 1]) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = noted<HD>(o[j], notes, c + j, tok);
+          for (int j = 0; j < 64; ++j)
+            if (note_flags[slot * 2 + (c + j >= HD / 2)])
+              o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
         }
         if (valid && direct) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + t * p.out_stride + (int64_t)qh * HD + c);
-          dst[0] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-          dst[1] = make_uint4(pack_bf16(o[8], o[9]), pack_bf16(o[10], o[11]), pack_bf16(o[12], o[13]), pack_bf16(o[14], o[15]));
-        } else if (valid) {
-          float4* dst = reinterpret_cast<float4*>(po + c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16(__uint_as_float(o[8 * j + 2 * i]), __uint_as_float(o[8 * j + 2 * i + 1]));
+            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(po + c);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
         __syncwarp();
       }
@@ -633,14 +644,14 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
 
 // -------------------------------------------------------------- the CTA's share
 struct Share {
-  long long unit_at;  // line position where the first unit begins
+  long long unit_at;  // line position where the first unit begins (perhaps before the share)
   long long x1;       // end of the share on the line
   int share, b, h, rt, kt0;
 };
 
 // Every CTA finds where its share of the line begins.  `cost` is scratch for
-// the batch (position tiles of one KV head of each sequence, then their
-// running sums over the line).
+// the batch (length of one KV head of each sequence, then the running sums over
+// the line).
 __device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost, Share* out) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int tu = 2 * (kTile / p.group);
@@ -652,7 +663,7 @@ __device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost
     const int nrt = (int)(((long long)n + tu - 1) / tu);
     long long c = 0;
     if (nrt <= 4)
-      for (int rt = 0; rt < nrt; ++rt) c += unit_tiles(n, len, tu, rt);
+      for (int rt = 0; rt < nrt; ++rt) c += unit_length(n, len, tu, rt);
     uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4);
     while (todo) {
       const int src = __ffs(todo) - 1;
@@ -660,7 +671,7 @@ __device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost
       const int sn = __shfl_sync(0xffffffffu, n, src), sl = __shfl_sync(0xffffffffu, len, src);
       const int sr = __shfl_sync(0xffffffffu, nrt, src);
       long long s = 0;
-      for (int rt = lane; rt < sr; rt += 32) s += unit_tiles(sn, sl, tu, rt);
+      for (int rt = lane; rt < sr; rt += 32) s += unit_length(sn, sl, tu, rt);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == src) c = s;
@@ -705,10 +716,10 @@ __device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost
       int q0, n, len;
       sequence_of(p, b, q0, n, len);
       const int nrt = (int)(((long long)n + tu - 1) / tu);
-      long long before = 0;  // tiles of the row tiles before rt0
+      long long before = 0;  // length of the row tiles before rt0
       int rt = 0;
       for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
-        const long long own = rt0 + lane < nrt ? unit_tiles(n, len, tu, rt0 + lane) : 0;
+        const long long own = rt0 + lane < nrt ? unit_length(n, len, tu, rt0 + lane) : 0;
         long long v = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -727,8 +738,8 @@ __device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost
       s.b = b;
       s.h = h;
       s.rt = rt;
-      s.kt0 = (int)(y - before);
-      s.unit_at = x0 - s.kt0;
+      s.kt0 = max((int)(y - before) - kUnitCost, 0);
+      s.unit_at = x0 - (y - before);
     }
     if (lane == 0) *out = s;
   }
@@ -747,7 +758,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   constexpr int NST = Lay::kStages;
   constexpr int kBoxes = Lay::kHalves * kPagesPerTile;  // TMA boxes of a tile
   const int g = p.group, tt = kTile / g, tu = 2 * tt;
-  const uint64_t keep = l2_policy_evict_first();
+  const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
   uint8_t* ring = smem + Lay::kRing;
   const int pi = lane & 7, dh = lane >> 3;
   int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
@@ -755,7 +766,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   int q0, n, len;
   sequence_of(p, b, q0, n, len);
   uint32_t ri = 0, u = 0, full = 0, landed = 0;
-  bool live = true;
+  bool live = true, q_armed = false;
   MergeUnit cut = {};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     int go = 1;
@@ -763,7 +774,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     return __shfl_sync(0xffffffffu, go, 0) != 0;
   };
   while (live) {
-    const bool more = at + kt0 < s.x1;
+    const bool more = at + kUnitCost + kt0 < s.x1;  // its next position tile is in the share
     const int slot = u & 1;
     if (u >= 2 && !wait(&bars.uempty[slot], ((u >> 1) - 1) & 1)) {
       live = false;
@@ -780,22 +791,25 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
       un.n0 = tiles_to(un.pos0 + min(tt, un.ntok) - 1);
       const int tiles = tiles_to(un.pos0 + un.ntok - 1);
       un.kt0 = kt0;
-      un.kt1 = (int)min((long long)tiles, s.x1 - at);
+      un.kt1 = (int)min((long long)tiles, s.x1 - at - kUnitCost);
       un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
+      at += kUnitCost + tiles;  // the next unit's
       if (kt0 == 0 && un.kt1 < tiles) {
-        cut.parts = (int)((at + tiles - 1) / s.share) - (int)blockIdx.x + 1;
+        cut.parts = (int)((at - 1) / s.share) - (int)blockIdx.x + 1;
         cut.tok0 = un.tok0;
         cut.ntok = un.ntok;
         cut.h = h;
       }
-      at += tiles;  // the next unit's
     }
+    q_armed = false;
     if (lane == 0) {
       units[slot] = un;
       mbar_arrive(&bars.ufull[slot]);
     }
     __syncwarp();
     if (!more) break;
+    // K and V of a sequence with several row tiles are read again by other CTAs
+    const uint64_t policy = n > tu ? again : once;
     // page ids of four tiles at a time, one per lane
     const int npages = (len + kPageSize - 1) / kPageSize;
     auto fetch = [&](int kt) -> int {
@@ -807,18 +821,6 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
       return p.num_pages;
     };
     int ids = fetch(un.kt0), ids_next = fetch(un.kt0 + 4);
-    if (u >= 1 && !wait(bars.qempty, (u - 1) & 1)) {
-      live = false;
-      break;
-    }
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kHalves * tt * g * 128);
-      for (int t = 0; t < (un.two ? 2 : 1); ++t)
-        for (int x = 0; x < Lay::kHalves; ++x)
-          tma_load_3d(smem + t * Lay::kQBytes + x * Lay::kHalfBytes, &tmq, bars.qfull, x * 64, h * g,
-                      un.tok0 + t * tt);
-    }
-    __syncwarp();
     for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
       const int w = (kt - un.kt0) & 3;
       if (w == 0 && kt > un.kt0) {
@@ -828,6 +830,21 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
       const int id = __shfl_sync(0xffffffffu, ids, w * 8 + pi);
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
+        if (v == 1 && kt == un.kt0) {  // Q, once the unit before has made its scores
+          if (u >= 1 && !wait(bars.qempty, (u - 1) & 1)) {
+            live = false;
+            break;
+          }
+          q_armed = true;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kHalves * tt * g * 128);
+            for (int t = 0; t < (un.two ? 2 : 1); ++t)
+              for (int x = 0; x < Lay::kHalves; ++x)
+                tma_load_3d(smem + t * Lay::kQBytes + x * Lay::kHalfBytes, &tmq, bars.qfull, x * 64,
+                            h * g, un.tok0 + t * tt);
+          }
+          __syncwarp();
+        }
         const uint32_t st = ri % NST;
         if (ri >= NST && !wait(&bars.empty[st], ((ri / NST) - 1) & 1)) {
           live = false;
@@ -838,7 +855,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
         __syncwarp();
         if (lane < kBoxes)
           tma_load_4d(ring + st * Lay::kStageBytes + dh * Lay::kHalfBytes + pi * kPageSize * 128,
-                      v ? &tmv : &tmk, bar, dh * 64, 0, h, id, keep);
+                      v ? &tmv : &tmk, bar, dh * 64, 0, h, id, policy);
         __syncwarp();
         if (bar == &bars.full[st])
           full ^= 1u << st;
@@ -867,7 +884,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
         mbar_wait(&bars.full[st], ((full >> st) & 1) ^ 1);
         mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
       }
-      if (u > 0) mbar_wait(bars.qfull, (u - 1) & 1);
+      if (u > 0 && q_armed) mbar_wait(bars.qfull, (u - 1) & 1);
     }
   }
   __syncwarp();
