@@ -646,104 +646,141 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
 struct Share {
   long long unit_at;  // line position where the first unit begins (perhaps before the share)
   long long x1;       // end of the share on the line
-  int share, b, h, rt, kt0;
+  long long share;    // its length
+  int b, h, rt, kt0;
+  int q0, n, len;     // the first unit's sequence
 };
 
-// Every CTA finds where its share of the line begins.  `cost` is scratch for
-// the batch (length of one KV head of each sequence, then the running sums over
-// the line).
-__device__ __forceinline__ void find_share(const ChunkParams& p, long long* cost, Share* out) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int tu = 2 * (kTile / p.group);
-  for (int b0 = tid - lane; b0 < p.batch; b0 += kChunkThreads) {
-    const int b = b0 + lane;
-    int q0 = 0, n = 0, len = 0;
-    if (b < p.batch && !sequence_of(p, b, q0, n, len) && blockIdx.x == 0)
-      flag_error(p.error_flag, VG_DEVERR_LENGTH);
-    const int nrt = (int)(((long long)n + tu - 1) / tu);
-    long long c = 0;
-    if (nrt <= 4)
-      for (int rt = 0; rt < nrt; ++rt) c += unit_length(n, len, tu, rt);
-    uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int sn = __shfl_sync(0xffffffffu, n, src), sl = __shfl_sync(0xffffffffu, len, src);
-      const int sr = __shfl_sync(0xffffffffu, nrt, src);
-      long long s = 0;
-      for (int rt = lane; rt < sr; rt += 32) s += unit_length(sn, sl, tu, rt);
+// a / b of non-negative numbers that mostly fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+__device__ __forceinline__ long long warp_inclusive_sum(long long v, int lane) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == src) c = s;
-    }
-    if (b < p.batch) cost[b] = c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
   }
-  __syncthreads();
-  if (tid < 32) {
-    long long total = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      long long v = b < p.batch ? cost[b] * p.num_kv_heads : 0;
+  return v;
+}
+
+__device__ __forceinline__ int row_tiles(int n, int tu) {
+  return (int)(((unsigned)n + (unsigned)tu - 1u) / (unsigned)tu);
+}
+
+// Length on the line of one KV head of the 32 sequences b0 .. b0 + 31, one per
+// lane of a warp; seq = their first row, tokens and length.
+__device__ __forceinline__ long long sequence_lengths(const ChunkParams& p, int b0, int tu, int lane,
+                                                      int4& seq) {
+  const int b = b0 + lane;
+  int q0 = 0, n = 0, len = 0;
+  if (b < p.batch && !sequence_of(p, b, q0, n, len) && blockIdx.x == 0)
+    flag_error(p.error_flag, VG_DEVERR_LENGTH);
+  seq = make_int4(q0, n, len, 0);
+  const int nrt = row_tiles(n, tu);
+  long long c = 0;
+  if (nrt <= 4)
+    for (int rt = 0; rt < nrt; ++rt) c += unit_length(n, len, tu, rt);
+  uint32_t todo = __ballot_sync(0xffffffffu, nrt > 4);
+  while (todo) {  // long sequences: a lane per row tile
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int sn = __shfl_sync(0xffffffffu, n, src), sl = __shfl_sync(0xffffffffu, len, src);
+    const int sr = __shfl_sync(0xffffffffu, nrt, src);
+    long long s = 0;
+    for (int rt = lane; rt < sr; rt += 32) s += unit_length(sn, sl, tu, rt);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long w = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += w;
-      }
-      v += total;
-      if (b < p.batch) cost[b] = v;
-      total = __shfl_sync(0xffffffffu, v, 31);
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == src) c = s;
+  }
+  return c;
+}
+
+// Batches of more than 32 sequences: the CTA's warps put every sequence's
+// length into shared memory first.
+struct SequenceTable {
+  long long* length;
+  int4* seq;
+};
+
+__device__ __forceinline__ void fill_sequence_table(const ChunkParams& p, const SequenceTable& tab) {
+  const int lane = threadIdx.x & 31, tu = 2 * (kTile / p.group);
+  for (int b0 = threadIdx.x - lane; b0 < p.batch; b0 += kChunkThreads) {
+    int4 seq;
+    const long long c = sequence_lengths(p, b0, tu, lane, seq);
+    if (b0 + lane < p.batch) {
+      tab.length[b0 + lane] = c;
+      tab.seq[b0 + lane] = seq;
+    }
+  }
+}
+
+// Where the CTA's share of the line begins; found by one warp.  b < 0: no work.
+__device__ __forceinline__ Share find_share(const ChunkParams& p, const SequenceTable& tab, int lane) {
+  const int tu = 2 * (kTile / p.group);
+  const bool small = p.batch <= 32;
+  int4 seq = make_int4(0, 0, 0, 0);
+  long long sum = 0, total = 0;  // running sum over the line, this lane's sequence included
+  if (small) {
+    sum = warp_inclusive_sum(sequence_lengths(p, 0, tu, lane, seq) * p.num_kv_heads, lane);
+    total = __shfl_sync(0xffffffffu, sum, 31);
+  } else {
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const bool in = b0 + lane < p.batch;
+      sum = total + warp_inclusive_sum(in ? tab.length[b0 + lane] * p.num_kv_heads : 0, lane);
+      if (in) tab.length[b0 + lane] = sum;
+      total = __shfl_sync(0xffffffffu, sum, 31);
     }
     __syncwarp();
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
-    const long long x0 = share * blockIdx.x;
-    Share s = {};
-    s.share = (int)share;
-    s.x1 = min(total, x0 + share);
-    s.b = -1;
-    if (x0 < total) {
-      int b = 0;
-      for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const uint32_t past = __ballot_sync(0xffffffffu, b0 + lane < p.batch && cost[b0 + lane] > x0);
-        if (past) {
-          b = b0 + __ffs(past) - 1;
-          break;
-        }
-      }
-      const long long base = b > 0 ? cost[b - 1] : 0;
-      const long long per_head = (cost[b] - base) / p.num_kv_heads;
-      const int h = (int)((x0 - base) / per_head);
-      const long long y = x0 - base - h * per_head;
-      int q0, n, len;
-      sequence_of(p, b, q0, n, len);
-      const int nrt = (int)(((long long)n + tu - 1) / tu);
-      long long before = 0;  // length of the row tiles before rt0
-      int rt = 0;
-      for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
-        const long long own = rt0 + lane < nrt ? unit_length(n, len, tu, rt0 + lane) : 0;
-        long long v = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long w = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += w;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + v > y);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          rt = rt0 + l;
-          before += __shfl_sync(0xffffffffu, v - own, l);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, v, 31);
-      }
-      s.b = b;
-      s.h = h;
-      s.rt = rt;
-      s.kt0 = max((int)(y - before) - kUnitCost, 0);
-      s.unit_at = x0 - (y - before);
-    }
-    if (lane == 0) *out = s;
   }
-  __syncthreads();
+  const long long share = quotient(total + gridDim.x - 1, gridDim.x);
+  const long long x0 = share * blockIdx.x;
+  Share s = {};
+  s.share = share;
+  s.x1 = min(total, x0 + share);
+  s.b = -1;
+  if (x0 >= total) return s;
+  long long base = 0, end = 0;  // the sequence's part of the line
+  if (small) {
+    s.b = __ffs(__ballot_sync(0xffffffffu, sum > x0)) - 1;
+    end = __shfl_sync(0xffffffffu, sum, s.b);
+    base = __shfl_sync(0xffffffffu, sum, max(s.b - 1, 0));
+    if (s.b == 0) base = 0;
+    s.q0 = __shfl_sync(0xffffffffu, seq.x, s.b);
+    s.n = __shfl_sync(0xffffffffu, seq.y, s.b);
+    s.len = __shfl_sync(0xffffffffu, seq.z, s.b);
+  } else {
+    for (int b0 = 0; b0 < p.batch && s.b < 0; b0 += 32) {
+      const uint32_t past = __ballot_sync(0xffffffffu, b0 + lane < p.batch && tab.length[b0 + lane] > x0);
+      if (past) s.b = b0 + __ffs(past) - 1;
+    }
+    end = tab.length[s.b];
+    base = s.b > 0 ? tab.length[s.b - 1] : 0;
+    s.q0 = tab.seq[s.b].x;
+    s.n = tab.seq[s.b].y;
+    s.len = tab.seq[s.b].z;
+  }
+  const long long per_head = quotient(end - base, p.num_kv_heads);
+  s.h = (int)quotient(x0 - base, per_head);
+  const long long y = x0 - base - s.h * per_head;
+  const int nrt = row_tiles(s.n, tu);
+  long long before = 0;  // length of the row tiles before rt
+  for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
+    const long long own = rt0 + lane < nrt ? unit_length(s.n, s.len, tu, rt0 + lane) : 0;
+    const long long v = warp_inclusive_sum(own, lane);
+    const uint32_t past = __ballot_sync(0xffffffffu, before + v > y);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      s.rt = rt0 + l;
+      before += __shfl_sync(0xffffffffu, v - own, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, v, 31);
+  }
+  s.kt0 = max((int)(y - before) - kUnitCost, 0);
+  s.unit_at = x0 - (y - before);
+  return s;
 }
 
 // ----------------------------------------------------------------- producer
@@ -763,8 +800,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   const int pi = lane & 7, dh = lane >> 3;
   int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
   long long at = s.unit_at;  // line position of the current unit's first tile
-  int q0, n, len;
-  sequence_of(p, b, q0, n, len);
+  int q0 = s.q0, n = s.n, len = s.len;
   uint32_t ri = 0, u = 0, full = 0, landed = 0;
   bool live = true, q_armed = false;
   MergeUnit cut = {};
@@ -774,7 +810,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     return __shfl_sync(0xffffffffu, go, 0) != 0;
   };
   while (live) {
-    const bool more = at + kUnitCost + kt0 < s.x1;  // its next position tile is in the share
+    const bool more = b >= 0 && at + kUnitCost + kt0 < s.x1;  // its next position tile is in the share
     const int slot = u & 1;
     if (u >= 2 && !wait(&bars.uempty[slot], ((u >> 1) - 1) & 1)) {
       live = false;
@@ -795,7 +831,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
       un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
       at += kUnitCost + tiles;  // the next unit's
       if (kt0 == 0 && un.kt1 < tiles) {
-        cut.parts = (int)((at - 1) / s.share) - (int)blockIdx.x + 1;
+        cut.parts = (int)quotient(at - 1, s.share) - (int)blockIdx.x + 1;
         cut.tok0 = un.tok0;
         cut.ntok = un.ntok;
         cut.h = h;
@@ -903,22 +939,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + Lay::kFlags + 16);
   uint16_t* notes = reinterpret_cast<uint16_t*>(smem + Lay::kNotes);
   float2* ml = reinterpret_cast<float2*>(smem + Lay::kMl);
+  // what needs no input comes before the wait for the previous kernel
   if (warp == kProducer && lane == 0) {
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  // the share is found in memory that the ring takes over afterwards
-  Share* share_s = reinterpret_cast<Share*>(smem + Lay::kMl);
-  find_share(p, reinterpret_cast<long long*>(smem), share_s);
-  const Share share = *share_s;
-  if (share.b < 0) {  // no work for this CTA
-    if (tid == 0) p.merge[blockIdx.x] = MergeUnit{};
-    return;
-  }
-  if (tid == 0) {
     for (int i = 0; i < Lay::kStages; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 1);
@@ -941,7 +966,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     fence_barrier_init();
   }
   if (warp == kMma) tmem_alloc(tmem_at, 512);
-  fence_proxy_async_smem();  // the scratch was written by ordinary stores, the ring is not
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  // in memory that the ring takes over afterwards
+  const SequenceTable tab = {reinterpret_cast<long long*>(smem),
+                             reinterpret_cast<int4*>(smem + kMaxBatch * sizeof(long long))};
+  if (p.batch > 32) fill_sequence_table(p, tab);
+  fence_proxy_async_smem();  // the table was written by ordinary stores, the ring is not
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -956,6 +987,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp < 8) {
     softmax_role<HD>(p, bars, units, note_flags, notes, ml, tmem, warp >> 2, warp, lane);
   } else if (warp == kProducer) {
+    const Share share = find_share(p, tab, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
     producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, smem, lane);
   } else if (warp == kMma) {
     const uint32_t base = smem_u32(smem);
@@ -977,68 +1011,162 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
 }
 
-// Merge of the units that several CTAs share: a warp per row, weights
-// 2^(m - max m) of the parts, which sit in slot 1 of the CTA where the unit
-// begins and in slot 0 of the following ones.
-constexpr int kMergeWarps = 8;
+// Merge of the units that several CTAs share, weights 2^(m - max m) of the
+// parts, which sit in slot 1 of the CTA where the unit begins and in slot 0 of
+// the following ones.  A warp takes four rows at once: their (m, l) of eight
+// parts are one load, and their O of a part four loads in flight; the whole
+// merge is one wave of CTAs.
+constexpr int kMergeWarps = 8, kMergeRows = 4;
 
 template <int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32;
+  constexpr int E = HD / 32, R = kMergeRows, P = 32 / R;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row of the partial
+  const int row0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * R;  // rows of the partial
   const MergeUnit mu = p.merge[c];
   const int g = p.group, tt = kTile / g;
-  const int tile = row / kTile, r = row - tile * kTile, tok_r = r / g;
-  const int tok = mu.ntok > tt ? tile * tt + tok_r : tok_r;
-  if (mu.parts == 0 || tok_r >= tt || tok >= mu.ntok || (tile && mu.ntok <= tt)) return;
-  auto at = [&](int i) { return (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.rows + row; };
+  const bool two = mu.ntok > tt;
+  const int rows = two ? kTile + (mu.ntok - tt) * g : mu.ntok * g;
+  if (mu.parts == 0 || row0 >= rows) return;
+  auto at = [&](int part, int row) {
+    return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)) * p.rows + row;
+  };
+  // lane's (row, part) among the four rows and each eight parts
+  const int lr = row0 + lane / P, lp = lane % P;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  const bool mine = lr < rows;  // rows between the tiles' ends hold nothing: not used below
   float m = -INFINITY;
-  for (int i = lane; i < mu.parts; i += 32) m = fmaxf(m, __ldcg(&ml[at(i)]).x);
+  for (int i = lp; i < mu.parts; i += P) m = fmaxf(m, mine ? __ldcg(&ml[at(i, lr)]).x : -INFINITY);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = P / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = safe_ref(m);
-  float l = 0.f, acc[E];
+  float l = 0.f, acc[R][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i0 = 0; i0 < mu.parts; i0 += 32) {
-    float w_l = 0.f, l_l = 0.f;
-    if (i0 + lane < mu.parts) {
-      const float2 x = __ldcg(&ml[at(i0 + lane)]);
-      w_l = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
-      l_l = w_l * x.y;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+  for (int i0 = 0; i0 < mu.parts; i0 += P) {
+    float w = 0.f;
+    if (mine && i0 + lp < mu.parts) {
+      const float2 x = __ldcg(&ml[at(i0 + lp, lr)]);
+      w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
+      if (w != 0.f) l += w * x.y;
     }
-    if (w_l != 0.f) l += l_l;
-    const int n = min(32, mu.parts - i0);
-#pragma unroll 4
+    const int n = min(P, mu.parts - i0);
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(0xffffffffu, w_l, i);
-      const float* src = p.part_o + at(i0 + i) * HD + lane * E;
-      float v[E];
-      if (E == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        v[0] = x.x, v[1] = x.y;
+      float v[R][E];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float* src = p.part_o + at(i0 + i, min(row0 + r, rows - 1)) * HD + lane * E;
+        if (E == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[r][0] = x.x, v[r][1] = x.y, v[r][E - 2] = x.z, v[r][E - 1] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[r][0] = x.x, v[r][1] = x.y;
+        }
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = w != 0.f ? fmaf(w, v[e], acc[e]) : acc[e];
+      for (int r = 0; r < R; ++r) {
+        const float wr = __shfl_sync(0xffffffffu, w, r * P + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = wr != 0.f ? fmaf(wr, v[r][e], acc[r][e]) : acc[r][e];
+      }
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
-  const int t = mu.tok0 + tok, qh = mu.h * g + r - tok_r * g;
-  __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + lane * E;
+  for (int o = P / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)t * p.num_q_heads + qh] = (m + log2f(l)) * 0.6931471805599453f;
+  for (int r = 0; r < R; ++r) {
+    const float lr_ = __shfl_sync(0xffffffffu, l, r * P), mr = __shfl_sync(0xffffffffu, m, r * P);
+    const int row = row0 + r, tile = row / kTile, tr = row % kTile;
+    const int tok = tile * tt + tr / g;
+    if (tr >= tt * g || tok >= mu.ntok) continue;  // no token's row
+    const float inv = lr_ > 0.f ? 1.f / lr_ : lr_ == lr_ ? 0.f : NAN;
+    const int t = mu.tok0 + tok, qh = mu.h * g + tr % g;
+    __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[r][e] * inv, acc[r][e + 1] * inv);
+    if (p.lse && lane == 0)
+      p.lse[(int64_t)t * p.num_q_heads + qh] = (mr + log2f(lr_)) * 0.6931471805599453f;
+  }
+}
+
+// The same for calls of few rows (single tokens), whose units have many parts:
+// a CTA per row, its warps over the parts, every load in flight at once.
+template <int HD>
+__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_row_kernel(const ChunkParams p) {
+  constexpr int E = HD / 32;
+  __shared__ float acc_s[kMergeWarps][HD], l_s[kMergeWarps], m_s[kMergeWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const MergeUnit mu = p.merge[c];
+  const int g = p.group;
+  if (mu.parts == 0 || row >= mu.ntok * g) return;
+  auto at = [&](int part) {
+    return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)) * p.rows + row;
+  };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < mu.parts; i += kMergeWarps) {
+    const float2 x = __ldcg(&ml[at(i)]);
+    const float* src = p.part_o + at(i) * HD + lane * E;
+    float v[E];
+    if (E == 4) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+      v[0] = y.x, v[1] = y.y, v[E - 2] = y.z, v[E - 1] = y.w;
+    } else {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+      v[0] = y.x, v[1] = y.y;
+    }
+    const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
+    const float f = ex2(m - ref), w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+    if (w != 0.f) {
+      l += w * x.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+    m = mn;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
+  if (lane == 0) {
+    l_s[warp] = l;
+    m_s[warp] = m;
+  }
+  __syncthreads();
+  if (threadIdx.x >= HD / 2) return;
+  float m_all = m_s[0];
+#pragma unroll
+  for (int i = 1; i < kMergeWarps; ++i) m_all = fmaxf(m_all, m_s[i]);
+  const float ref = safe_ref(m_all);
+  float l_all = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) {
+    const float li = l_s[i], w = li == li ? ex2(m_s[i] - ref) : NAN;
+    if (w != 0.f) {
+      l_all += w * li;
+      o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
+      o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
+    }
+  }
+  const float inv = l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN;
+  const int t = mu.tok0 + row / g, qh = mu.h * g + row % g;
+  *reinterpret_cast<uint32_t*>(p.out + t * p.out_stride + (int64_t)qh * HD + 2 * threadIdx.x) =
+      pack_bf16(o0 * inv, o1 * inv);
+  if (p.lse && threadIdx.x == 0)
+    p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
 }
 
 struct ChunkPlan {
@@ -1082,9 +1210,15 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<HD>, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.num_tokens * p.group;  // no unit has more
-  cfg.gridDim = dim3(pl.grid, ceil_div((int)(rows < pl.rows && pl.rows == kTile ? rows : pl.rows), kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
+  // Up to 32 rows: a CTA per row (one token of 8 heads over 2K: MERGE_SMALL);
+  // more rows mean fewer parts, and a CTA takes 32 rows.
+  if (rows <= 32) {
+    cfg.gridDim = dim3(pl.grid, (int)rows);
+    return cudaLaunchKernelEx(&cfg, chunk_merge_row_kernel<HD>, p);
+  }
+  cfg.gridDim = dim3(pl.grid, ceil_div(pl.rows == kTile ? (int)rows : pl.rows, kMergeWarps * kMergeRows));
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<HD>, p);
 }
 
