@@ -28,9 +28,11 @@
 //    says that O may be rescaled.  The exponent reference moves only when a
 //    row maximum grows by more than 2^8: P stays below 2^8 times a weight of
 //    one, exact range in bf16 and far from the fp32 range in l and O.
-//  * A producer warp streams K and V tiles (page by page, TMA, 128-byte
-//    swizzle) through a ring of stages and publishes the CTA's units; one
-//    thread issues every tensor-core operation.
+//  * A producer warp streams K and V tiles (TMA, 128-byte swizzle) through a
+//    ring of stages and publishes the CTA's units; one warp issues every
+//    tensor-core operation.  A page of a head is one TMA box: at about 100
+//    cycles a box, two boxes a page (one per 64-dim block) held a CTA to one
+//    64 KB tile of K and V in 3300 cycles.
 //  * Position tiles that some row of the unit does not attend in full (the
 //    diagonal and the end of the cache) pass through two checking warps
 //    first: a weight of zero times a NaN or an infinity in V would still
@@ -90,9 +92,13 @@ struct Unit {
 
 template <int HD>
 struct ChunkLayout {
-  static constexpr int kHalves = HD / 64;
-  static constexpr int kHalfBytes = kTile * 128;
-  static constexpr int kStageBytes = kHalves * kHalfBytes;
+  static constexpr int kBlocks = HD / 64;              // 64-dim blocks of a row
+  // Q: [block][row][128 bytes].  K and V: [8-position group][block][8][128
+  // bytes], the order in which one TMA box brings a page.
+  static constexpr int kQBlockBytes = kTile * 128;
+  static constexpr int kGroupBytes = kBlocks * 1024;
+  static constexpr int kPageBytes = 2 * kGroupBytes;
+  static constexpr int kStageBytes = kPagesPerTile * kPageBytes;
   static constexpr int kStages = HD == 128 ? 5 : 10;
   static constexpr int kQBytes = kStageBytes;          // one row tile
   static constexpr int kRing = 2 * kQBytes;
@@ -106,6 +112,11 @@ struct ChunkLayout {
   static constexpr int kMl = kNotes + 2 * 3 * HD * 2;
   static constexpr int kBytes = kMl + kTile * 8;
   static constexpr int kSCol = 0, kOCol = 2 * kTile;
+
+  // Byte offset of 16-byte piece `ch` of position `row` in a K or V tile.
+  static __device__ __forceinline__ uint32_t kv_offset(int row, int ch) {
+    return (row >> 3) * kGroupBytes + (ch >> 3) * 1024 + (row & 7) * 128 + (((ch & 7) ^ (row & 7)) << 4);
+  }
 };
 static_assert(ChunkLayout<128>::kBytes <= 227 * 1024 && ChunkLayout<64>::kBytes <= 227 * 1024, "");
 static_assert(sizeof(Unit) <= 48, "");
@@ -434,7 +445,7 @@ struct MmaIssuer {
   uint32_t tmem, ring_lo, q_lo, v_lo;  // low descriptor words of stage 0 and of Q
   static constexpr uint32_t kIdQk = umma_idesc_bf16(kTile, kTile, 0, 0);
   static constexpr uint32_t kIdPv = umma_idesc_bf16(kTile, HD, 0, 1);
-  static constexpr uint32_t kHi = umma_desc_hi(1024);
+  static constexpr uint32_t kHiQ = umma_desc_hi(1024), kHiKv = umma_desc_hi(Lay::kGroupBytes);
 
   // S of warpgroup `wg` = Q (row tile qt) K^T of the stage
   __device__ __forceinline__ void qk(int wg, int qt, uint32_t stage) {
@@ -442,8 +453,9 @@ struct MmaIssuer {
     const uint32_t q = q_lo + qt * (Lay::kQBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
-      const uint32_t off = ((ks >> 2) * Lay::kHalfBytes + (ks & 3) * 32) >> 4;
-      umma_bf16_elect(tmem + Lay::kSCol + wg * kTile, q + off, kHi, k + off, kHi, kIdQk, ks > 0);
+      const int block = ks >> 2, in = (ks & 3) * 32;
+      umma_bf16_elect(tmem + Lay::kSCol + wg * kTile, q + ((block * Lay::kQBlockBytes + in) >> 4), kHiQ,
+                      k + ((block * 1024 + in) >> 4), kHiKv, kIdQk, ks > 0);
     }
     umma_commit_elect(&bars.sfull[wg]);
   }
@@ -453,7 +465,7 @@ struct MmaIssuer {
 #pragma unroll
     for (int ks = half * (kTile / 32); ks < (half + 1) * (kTile / 32); ++ks)
       umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
-                         v + ks * (16 * 128 >> 4), kHi, kIdPv, accumulate || ks > 0);
+                         v + ks * (Lay::kPageBytes >> 4), kHiKv, kIdPv, accumulate || ks > 0);
   }
 };
 
@@ -464,7 +476,7 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   using Lay = ChunkLayout<HD>;
   constexpr uint32_t NST = Lay::kStages;
   MmaIssuer<HD> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
-                    umma_desc_lo(ring, Lay::kHalfBytes)};
+                    umma_desc_lo(ring, 1024)};
   uint32_t pc0 = 0, pc1 = 0, full = 0, clean = 0;  // parities
   uint32_t at = 0;                                 // stage of the unit's first K tile
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
@@ -598,7 +610,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
 #pragma unroll 4
       for (int r0 = 0; r0 < kTile; r0 += RPI) {
         const int row = r0 + lane / CPW, pos = kt * kTile + row;
-        uint4* at = reinterpret_cast<uint4*>(tile + sw128_offset(row, ch, kTile));
+        uint4* at = reinterpret_cast<uint4*>(tile + Lay::kv_offset(row, ch));
         if (pos >= un.len) {
           *at = make_uint4(0u, 0u, 0u, 0u);
         } else if (pos > un.pos0) {
@@ -622,7 +634,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
           for (int row = 0; row < kTile; ++row) {
             const int pos = kt * kTile + row;
             if (pos <= un.pos0 || pos >= un.len) continue;
-            uint16_t* e = reinterpret_cast<uint16_t*>(tile + sw128_offset(row, c >> 3, kTile)) + (c & 7);
+            uint16_t* e = reinterpret_cast<uint16_t*>(tile + Lay::kv_offset(row, c >> 3)) + (c & 7);
             const uint16_t x = *e;
             if ((x & 0x7f80) != 0x7f80) continue;
             const int kind = (x & 0x7f) ? 0 : x & 0x8000 ? 2 : 1;
@@ -793,11 +805,10 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
                                               Unit* units, uint8_t* smem, int lane) {
   using Lay = ChunkLayout<HD>;
   constexpr int NST = Lay::kStages;
-  constexpr int kBoxes = Lay::kHalves * kPagesPerTile;  // TMA boxes of a tile
   const int g = p.group, tt = kTile / g, tu = 2 * tt;
   const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
   uint8_t* ring = smem + Lay::kRing;
-  const int pi = lane & 7, dh = lane >> 3;
+  const int pi = lane & 7;
   int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
   long long at = s.unit_at;  // line position of the current unit's first tile
   int q0 = s.q0, n = s.n, len = s.len;
@@ -873,10 +884,10 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
           }
           q_armed = true;
           if (lane == 0) {
-            mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kHalves * tt * g * 128);
+            mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kBlocks * tt * g * 128);
             for (int t = 0; t < (un.two ? 2 : 1); ++t)
-              for (int x = 0; x < Lay::kHalves; ++x)
-                tma_load_3d(smem + t * Lay::kQBytes + x * Lay::kHalfBytes, &tmq, bars.qfull, x * 64,
+              for (int x = 0; x < Lay::kBlocks; ++x)
+                tma_load_3d(smem + t * Lay::kQBytes + x * Lay::kQBlockBytes, &tmq, bars.qfull, x * 64,
                             h * g, un.tok0 + t * tt);
           }
           __syncwarp();
@@ -889,9 +900,9 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
         uint64_t* bar = &(v && checked_tile(un.pos0, kt) ? bars.landed : bars.full)[st];
         if (lane == 0) mbar_arrive_expect_tx(bar, Lay::kStageBytes);
         __syncwarp();
-        if (lane < kBoxes)
-          tma_load_4d(ring + st * Lay::kStageBytes + dh * Lay::kHalfBytes + pi * kPageSize * 128,
-                      v ? &tmv : &tmk, bar, dh * 64, 0, h, id, policy);
+        if (lane < kPagesPerTile)
+          tma_load_4d(ring + st * Lay::kStageBytes + pi * Lay::kPageBytes, v ? &tmv : &tmk, bar, 0, 0,
+                      0, (id * p.num_kv_heads + h) * 2, policy);
         __syncwarp();
         if (bar == &bars.full[st])
           full ^= 1u << st;
@@ -1254,12 +1265,14 @@ extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, in
       q_stride < row || out_stride < row || q_stride % 8 || out_stride % 8)
     return VG_ERR_INVALID_ARGUMENT;
   const int g = num_q_heads / kv->num_kv_heads;
-  if (g > 16 || batch > kMaxBatch || kv->max_pages_per_seq > (1 << 26)) return VG_ERR_UNSUPPORTED;
+  if (g > 16 || batch > kMaxBatch || kv->max_pages_per_seq > (1 << 26) ||
+      (int64_t)kv->num_pages * kv->num_kv_heads >= (1 << 29))
+    return VG_ERR_UNSUPPORTED;
   const ChunkPlan pl = make_chunk_plan(num_tokens, g, kv->head_dim);
   if (!workspace || workspace_bytes < pl.bytes) return VG_ERR_WORKSPACE_TOO_SMALL;
   CUtensorMap tq, tk, tv;
-  if (!page_pool_tensor_map(kv->k_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tk) ||
-      !page_pool_tensor_map(kv->v_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tv) ||
+  if (!page_chunk_tensor_map(kv->k_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tk) ||
+      !page_chunk_tensor_map(kv->v_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tv) ||
       !token_rows_tensor_map(q, num_tokens, num_q_heads, kv->head_dim, q_stride, g, kTile / g, &tq))
     return VG_ERR_LAUNCH;
   ChunkParams p = {};

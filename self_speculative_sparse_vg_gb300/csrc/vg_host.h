@@ -35,6 +35,14 @@ bool page_pool_tensor_map(const void* base, int num_pages, int num_kv_heads, int
 bool token_rows_tensor_map(const void* base, int num_tokens, int num_heads, int head_dim,
                            int64_t token_stride, int box_heads, int box_tokens, CUtensorMap* out);
 
+// 4-D tiled TMA descriptor over a page pool viewed as [num_pages * num_kv_heads
+// * 2][head_dim / 64][8][64] bf16: index ((page * num_kv_heads + head) * 2 + i)
+// is the i-th 8-position group of a page, so that one box of 64 x 8 x head_dim
+// / 64 x 2 is a whole (page, head) chunk, laid down group by group, 64-dim
+// block by block, with the 128-byte swizzle.  Made anew on every call.
+bool page_chunk_tensor_map(const void* base, int num_pages, int num_kv_heads, int head_dim,
+                           CUtensorMap* out);
+
 // Basic checks of a vg_paged_kv; VG_OK or an error status.
 vg_status check_paged_kv(const vg_paged_kv* kv);
 
