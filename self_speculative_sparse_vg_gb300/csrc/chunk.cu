@@ -62,7 +62,7 @@ struct ChunkParams {
   const int32_t* kv_lens;
   __nv_bfloat16* out;
   float* lse;
-  float* part_o;      // [grid][2][rows][HD]
+  float* part_o;      // [grid][2][HD / 4][rows][4]
   float* part_ml;     // [grid][2][rows][2]
   struct MergeUnit* merge;  // [grid]
   int32_t* error_flag;
@@ -226,6 +226,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 32-byte store (a whole sector of a row per lane).
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // A V entry with its non-finite value given back: rel = the row's token within
 // the unit, notes = first token distance of a NaN, +inf, -inf in dimension c.
 template <int HD>
@@ -372,7 +379,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
       const int prow = (un.two ? wg * kTile : 0) + r;       // row of the partial
       const float inv = direct ? (l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN) : 1.f;
       const float f_own = has ? w_own * inv : 0.f, f_other = w_other * inv;
-      float* po = direct ? nullptr : p.part_o + ((size_t)un.part * p.rows + prow) * HD;
+      const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
 #pragma unroll 1
       for (int c = 0; c < HD; c += 64) {
         uint32_t o[64];
@@ -398,19 +405,26 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
               o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
         }
         if (valid && direct) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + t * p.out_stride + (int64_t)qh * HD + c);
+          __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + c;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t w[4];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16(__uint_as_float(o[8 * j + 2 * i]), __uint_as_float(o[8 * j + 2 * i + 1]));
-            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 8; ++i)
+              w[i] = pack_bf16(__uint_as_float(o[16 * j + 2 * i]), __uint_as_float(o[16 * j + 2 * i + 1]));
+            if (wide) {
+              store32(dst + 16 * j, w);
+            } else {
+              *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + 16 * j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(po + c);
+          // [4-dim piece][row][4]: a warp's rows are neighbours
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o) + ((size_t)un.part * (HD / 4) + c / 4) * p.rows + prow;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 16; ++j)
+            dst[(size_t)j * p.rows] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
         __syncwarp();
       }
@@ -1024,86 +1038,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
 // Merge of the units that several CTAs share, weights 2^(m - max m) of the
 // parts, which sit in slot 1 of the CTA where the unit begins and in slot 0 of
-// the following ones.  A warp takes four rows at once: their (m, l) of eight
-// parts are one load, and their O of a part four loads in flight; the whole
-// merge is one wave of CTAs.
-constexpr int kMergeWarps = 8, kMergeRows = 4;
+// the following ones.  A CTA takes 32 rows, a lane each (the parts' layout);
+// a warp takes an eighth of the dimensions, and the rows leave through shared
+// memory in whole lines.
+constexpr int kMergeWarps = 8, kMergeRows = 32;
 
 template <int HD>
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32, R = kMergeRows, P = 32 / R;
+  constexpr int NP = HD / 4 / kMergeWarps;   // 4-dim pieces of a warp
+  constexpr int kRow = HD / 2 + 4;           // words of a staged row (spread over the banks)
+  __shared__ __align__(16) uint32_t out_s[kMergeRows][kRow];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int row0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * R;  // rows of the partial
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = blockIdx.y * kMergeRows, row = row0 + lane;  // row of the partial
   const MergeUnit mu = p.merge[c];
   const int g = p.group, tt = kTile / g;
-  const bool two = mu.ntok > tt;
-  const int rows = two ? kTile + (mu.ntok - tt) * g : mu.ntok * g;
+  const int rows = mu.ntok > tt ? kTile + (mu.ntok - tt) * g : mu.ntok * g;
   if (mu.parts == 0 || row0 >= rows) return;
-  auto at = [&](int part, int row) {
-    return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)) * p.rows + row;
-  };
-  // lane's (row, part) among the four rows and each eight parts
-  const int lr = row0 + lane / P, lp = lane % P;
+  const int tr = row % kTile, tok = row / kTile * tt + tr / g;
+  const bool mine = tr < tt * g && tok < mu.ntok;  // else no token's row
+  auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  const bool mine = lr < rows;  // rows between the tiles' ends hold nothing: not used below
-  float m = -INFINITY;
-  for (int i = lp; i < mu.parts; i += P) m = fmaxf(m, mine ? __ldcg(&ml[at(i, lr)]).x : -INFINITY);
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)(warp * NP) * p.rows + row;
+  float m = -INFINITY, l = 0.f, acc[NP][4];
 #pragma unroll
-  for (int o = P / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = safe_ref(m);
-  float l = 0.f, acc[R][E];
+  for (int k = 0; k < NP; ++k)
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+  if (mine) {
+#pragma unroll 4
+    for (int i = 0; i < mu.parts; ++i) {
+      const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
+      float4 v[NP];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
-  for (int i0 = 0; i0 < mu.parts; i0 += P) {
-    float w = 0.f;
-    if (mine && i0 + lp < mu.parts) {
-      const float2 x = __ldcg(&ml[at(i0 + lp, lr)]);
-      w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
+      for (int k = 0; k < NP; ++k) v[k] = __ldcg(po + (slot(i) * (HD / 4) + k) * p.rows);
+      const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
+      const float f = ex2(m - ref), w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
+      l *= f;
       if (w != 0.f) l += w * x.y;
-    }
-    const int n = min(P, mu.parts - i0);
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-      float v[R][E];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float* src = p.part_o + at(i0 + i, min(row0 + r, rows - 1)) * HD + lane * E;
-        if (E == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          v[r][0] = x.x, v[r][1] = x.y, v[r][E - 2] = x.z, v[r][E - 1] = x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          v[r][0] = x.x, v[r][1] = x.y;
+      for (int k = 0; k < NP; ++k) {
+        const float y[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[k][e] *= f;
+          if (w != 0.f) acc[k][e] = fmaf(w, y[e], acc[k][e]);
         }
       }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float wr = __shfl_sync(0xffffffffu, w, r * P + i);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] = wr != 0.f ? fmaf(wr, v[r][e], acc[r][e]) : acc[r][e];
-      }
+      m = mn;
     }
   }
+  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
 #pragma unroll
-  for (int o = P / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float lr_ = __shfl_sync(0xffffffffu, l, r * P), mr = __shfl_sync(0xffffffffu, m, r * P);
-    const int row = row0 + r, tile = row / kTile, tr = row % kTile;
-    const int tok = tile * tt + tr / g;
-    if (tr >= tt * g || tok >= mu.ntok) continue;  // no token's row
-    const float inv = lr_ > 0.f ? 1.f / lr_ : lr_ == lr_ ? 0.f : NAN;
-    const int t = mu.tok0 + tok, qh = mu.h * g + tr % g;
-    __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[r][e] * inv, acc[r][e + 1] * inv);
-    if (p.lse && lane == 0)
-      p.lse[(int64_t)t * p.num_q_heads + qh] = (mr + log2f(lr_)) * 0.6931471805599453f;
+  for (int k = 0; k < NP; ++k) {
+    out_s[lane][(warp * NP + k) * 2] = pack_bf16(acc[k][0] * inv, acc[k][1] * inv);
+    out_s[lane][(warp * NP + k) * 2 + 1] = pack_bf16(acc[k][2] * inv, acc[k][3] * inv);
+  }
+  if (mine && warp == 0 && p.lse)
+    p.lse[(int64_t)(mu.tok0 + tok) * p.num_q_heads + mu.h * g + tr % g] =
+        (m + log2f(l)) * 0.6931471805599453f;
+  __syncthreads();
+  constexpr int kPieces = HD / 8;  // 16-byte pieces of a row
+  for (int i = threadIdx.x; i < kMergeRows * kPieces; i += kMergeWarps * 32) {
+    const int r = row0 + i / kPieces, rr = r % kTile, tk = r / kTile * tt + rr / g;
+    if (rr >= tt * g || tk >= mu.ntok) continue;
+    *reinterpret_cast<uint4*>(p.out + (int64_t)(mu.tok0 + tk) * p.out_stride +
+                              (int64_t)(mu.h * g + rr % g) * HD + (i % kPieces) * 8) =
+        *reinterpret_cast<const uint4*>(&out_s[i / kPieces][(i % kPieces) * 4]);
   }
 }
 
@@ -1119,17 +1121,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_row_kernel(const
   const MergeUnit mu = p.merge[c];
   const int g = p.group;
   if (mu.parts == 0 || row >= mu.ntok * g) return;
-  auto at = [&](int part) {
-    return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)) * p.rows + row;
-  };
+  auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int i = warp; i < mu.parts; i += kMergeWarps) {
-    const float2 x = __ldcg(&ml[at(i)]);
-    const float* src = p.part_o + at(i) * HD + lane * E;
+    const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
+    const float* src = p.part_o + ((slot(i) * (HD / 4) + lane * E / 4) * p.rows + row) * 4 + lane * E % 4;
     float v[E];
     if (E == 4) {
       const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
@@ -1229,7 +1229,7 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
     cfg.gridDim = dim3(pl.grid, (int)rows);
     return cudaLaunchKernelEx(&cfg, chunk_merge_row_kernel<HD>, p);
   }
-  cfg.gridDim = dim3(pl.grid, ceil_div(pl.rows == kTile ? (int)rows : pl.rows, kMergeWarps * kMergeRows));
+  cfg.gridDim = dim3(pl.grid, ceil_div(pl.rows == kTile ? (int)rows : pl.rows, kMergeRows));
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<HD>, p);
 }
 
