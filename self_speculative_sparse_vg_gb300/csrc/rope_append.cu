@@ -80,61 +80,46 @@ __device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float2* cs
 
 template <int HD, bool NEAR>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
-  extern __shared__ float2 cs_s[];  // [tokens of the CTA][half]
+  extern __shared__ float2 cs_s[];  // [tokens of the CTA][half], then their slots
   constexpr int IPH = HD / 16;      // items of a head
   const int t0 = blockIdx.x * p.tokens_per_cta;
   const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  const int per_token = heads * IPH;
-  const int items = nt * per_token;
+  int32_t* slot_s = reinterpret_cast<int32_t*>(cs_s + p.tokens_per_cta * p.half);
+  const int heads = p.num_q_heads + 2 * p.num_kv_heads, qk = p.num_q_heads + p.num_kv_heads;
+  const int items = nt * heads * IPH;
   const int turning = p.half / 8;   // items of a head that turn; the others pass
+  // element offsets of an item's two pieces within its head
+  auto pieces = [&](int c, int& off0, int& off1) {
+    if (c < turning) {
+      off0 = NEAR ? c * 16 : c * 8;
+      off1 = NEAR ? off0 + 8 : p.half + off0;
+    } else {  // passing items follow the turning dims two pieces at a time
+      off0 = 2 * p.half + (c - turning) * 16;
+      off1 = off0 + 8;
+    }
+  };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  bool have_angles = false;
+  bool ready = false;
   for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += kRopeThreads * kUnroll) {
     uint4 x0[kUnroll], x1[kUnroll];
-    __nv_bfloat16* dst[kUnroll];
-    int off0[kUnroll], off1[kUnroll], cs_at[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kRopeThreads;
-      dst[u] = nullptr;
-      cs_at[u] = -1;
       if (i >= items) continue;
-      const int c = i % IPH, hi = i / IPH, tl = hi / heads, hh = hi - tl * heads;
+      const int hi = i / IPH, tl = hi / heads, hh = hi - tl * heads;
       const int64_t t = t0 + tl;
-      // element offsets of the item's two pieces within the head
-      const bool turns = c < turning;
-      off0[u] = turns && !NEAR ? c * 8 : c * 16;
-      off1[u] = turns && !NEAR ? p.half + c * 8 : c * 16 + 8;
-      if (turns && hh < p.num_q_heads + p.num_kv_heads) {
-        cs_at[u] = tl * p.half + c * 8;
-      } else if (!turns) {
-        // passing items follow the turning dims two pieces at a time
-        off0[u] = 2 * p.half + (c - turning) * 16;
-        off1[u] = off0[u] + 8;
-      }
-      const __nv_bfloat16* src;
-      if (hh < p.num_q_heads) {
-        src = p.q + t * p.q_stride + (int64_t)hh * HD;
-        dst[u] = p.q_out + t * p.q_out_stride + (int64_t)hh * HD;
-      } else {
-        const bool is_k = hh < p.num_q_heads + p.num_kv_heads;
-        const int h = hh - p.num_q_heads - (is_k ? 0 : p.num_kv_heads);
-        const int slot = p.slots[t];
-        if (slot < 0) continue;
-        if (slot >= p.num_slots) {
-          flag_error(p.error_flag, VG_DEVERR_INDEX);
-          continue;
-        }
-        src = is_k ? p.k + t * p.k_stride + (int64_t)h * HD : p.v + t * p.v_stride + (int64_t)h * HD;
-        dst[u] = (is_k ? p.k_pages : p.v_pages) +
-                 (((int64_t)(slot / kPageSize) * p.num_kv_heads + h) * kPageSize + slot % kPageSize) * HD;
-      }
-      x0[u] = *reinterpret_cast<const uint4*>(src + off0[u]);
-      x1[u] = *reinterpret_cast<const uint4*>(src + off1[u]);
+      const __nv_bfloat16* src =
+          hh < p.num_q_heads ? p.q + t * p.q_stride + hh * HD
+          : hh < qk          ? p.k + t * p.k_stride + (hh - p.num_q_heads) * HD
+                             : p.v + t * p.v_stride + (hh - qk) * HD;
+      int off0, off1;
+      pieces(i % IPH, off0, off1);
+      x0[u] = __ldcs(reinterpret_cast<const uint4*>(src + off0));
+      x1[u] = __ldcs(reinterpret_cast<const uint4*>(src + off1));
     }
-    if (!have_angles) {
+    if (!ready) {
+      for (int i = threadIdx.x; i < nt; i += kRopeThreads) slot_s[i] = p.slots[t0 + i];
       for (int i = threadIdx.x; i < nt * p.half; i += kRopeThreads) {
         const int tl = i / p.half, f = i - tl * p.half;
         int axis = p.freq_axis ? p.freq_axis[f] : 0;
@@ -145,14 +130,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
         cs_s[i] = turn_of(p.positions[axis * p.pos_stride + t0 + tl], p.inv_freq[f]);
       }
       __syncthreads();
-      have_angles = true;
+      ready = true;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (!dst[u]) continue;
-      if (cs_at[u] >= 0) turn_item<NEAR>(x0[u], x1[u], cs_s + cs_at[u]);
-      *reinterpret_cast<uint4*>(dst[u] + off0[u]) = x0[u];
-      *reinterpret_cast<uint4*>(dst[u] + off1[u]) = x1[u];
+      const int i = i0 + u * kRopeThreads;
+      if (i >= items) continue;
+      const int c = i % IPH, hi = i / IPH, tl = hi / heads, hh = hi - tl * heads;
+      if (c < turning && hh < qk) turn_item<NEAR>(x0[u], x1[u], cs_s + tl * p.half + c * 8);
+      __nv_bfloat16* dst;
+      if (hh < p.num_q_heads) {
+        dst = p.q_out + (int64_t)(t0 + tl) * p.q_out_stride + hh * HD;
+      } else {
+        const int slot = slot_s[tl];
+        if (slot < 0) continue;
+        if (slot >= p.num_slots) {
+          flag_error(p.error_flag, VG_DEVERR_INDEX);
+          continue;
+        }
+        const int h = hh < qk ? hh - p.num_q_heads : hh - qk;
+        dst = (hh < qk ? p.k_pages : p.v_pages) +
+              (((int64_t)(slot / kPageSize) * p.num_kv_heads + h) * kPageSize + slot % kPageSize) * HD;
+      }
+      int off0, off1;
+      pieces(c, off0, off1);
+      *reinterpret_cast<uint4*>(dst + off0) = x0[u];
+      *reinterpret_cast<uint4*>(dst + off1) = x1[u];
     }
   }
 }
@@ -165,7 +168,7 @@ cudaError_t launch_rope(const RopeParams& p, bool near, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ceil_div(p.num_tokens, p.tokens_per_cta));
   cfg.blockDim = dim3(kRopeThreads);
-  cfg.dynamicSmemBytes = (size_t)p.tokens_per_cta * p.half * sizeof(float2);
+  cfg.dynamicSmemBytes = (size_t)p.tokens_per_cta * (p.half * sizeof(float2) + sizeof(int32_t));
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
