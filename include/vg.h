@@ -422,8 +422,8 @@ vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, in
  *                cache (padding; the query is still turned), one past the pool
  *                is flagged VG_DEVERR_INDEX and skipped.  Of two tokens with
  *                the same slot either may be the one that stays.
- * Angles are formed in double and reduced to a turn; the rotation is float32,
- * rounded once.
+ * Angles are exact up to the reduction to a turn, whatever the position; the
+ * rotation is float32, rounded once.
  * ------------------------------------------------------------------------- */
 vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
                          int64_t k_stride, const void* v, int64_t v_stride, void* q_out,

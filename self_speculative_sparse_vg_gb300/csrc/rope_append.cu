@@ -10,13 +10,15 @@
 // The call moves 2 (Hq + 2 Hkv) d bf16 per token and is bound by HBM; for a
 // few tokens by latency.  An item is two 16-byte pieces of one head that hold
 // eight pairs (pieces c and c + rot / 16, or 2c and 2c + 1), so a thread turns
-// its item without shuffles.  A CTA takes as many tokens as give every thread
-// several items; a thread loads up to kUnroll items before it waits, and the
-// CTA computes each of its angles once while those loads are in flight.
+// its item without shuffles.  A thread keeps one (head, c) of kUnroll tokens:
+// its pointers move by a stride and nothing is divided per item (with a
+// division and 64-bit offsets for each item the call was bound by the
+// instructions, 43 us for 8192 tokens of 32 + 2 * 8 heads).  It loads all its
+// items before it waits; meanwhile the CTA makes its tokens' angles, each once.
 //
-// Angles: position * frequency is formed in double (a far position times a
-// frequency has more than 24 significant bits) and reduced there to half a
-// turn either way; only the sine and cosine are single precision.
+// Angles: a far position times a frequency has more than 24 significant bits,
+// so the product is kept exactly until whole turns are taken off; only the
+// sine and cosine are single precision.
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -25,8 +27,11 @@
 namespace vg {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kUnroll = 4;
+// Most threads of a CTA, tokens of a thread.  8192 tokens of 32 + 2 * 8 heads:
+// 35.5 us (5.7 TB/s) as set, 36.1 with 256 threads, 37.2 with 512, 37.8 with
+// four tokens of a thread.
+constexpr int kRopeThreads = 128;
+constexpr int kUnroll = 2;
 constexpr int kAxesMax = 8;
 
 struct RopeParams {
@@ -42,16 +47,30 @@ struct RopeParams {
   const int32_t* freq_axis;
   int32_t* error_flag;
   int64_t q_stride, k_stride, v_stride, q_out_stride, pos_stride;  // elements between tokens / axes
-  int num_tokens, num_q_heads, num_kv_heads, head_dim, num_slots, n_axes, half;
-  int tokens_per_cta;
+  int num_tokens, num_q_heads, num_kv_heads, num_slots, n_axes, half;
+  int per_cta;  // (head, c) columns of a CTA; its threads are some tokens' columns
+  int side;     // tokens side by side
 };
 
-// (cos a, sin a) of a = pos * f, reduced to a fraction of a turn in double.
+// (cos a, sin a) of a = pos * f, as a fraction of a turn.  A position below
+// 2^24 is exact in single precision, so an fma gives the rest of its product
+// with f, and another the rest of the product with 1 / (2 pi) (Dekker's exact
+// product): the fraction is good to 1e-8 of a turn, in six operations of the
+// full-rate pipe.  Farther positions go through double precision.
 __device__ __forceinline__ float2 turn_of(int pos, float f) {
-  constexpr double kInvTwoPi = 0.15915494309189533577;
-  const double turns = (double)pos * (double)f * kInvTwoPi;
+  float frac;
+  if (pos > -(1 << 24) && pos < (1 << 24)) {
+    constexpr double kInvTwoPi = 0.15915494309189533577;
+    constexpr float kHi = (float)kInvTwoPi, kLo = (float)(kInvTwoPi - (double)kHi);
+    const float x = (float)pos, hi = x * f, lo = fmaf(x, f, -hi);
+    const float turns = hi * kHi;
+    frac = (turns - rintf(turns)) + fmaf(lo, kHi, fmaf(hi, kLo, fmaf(hi, kHi, -turns)));
+  } else {
+    const double turns = (double)pos * (double)f * 0.15915494309189533577;
+    frac = (float)(turns - rint(turns));
+  }
   float s, c;
-  sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+  sincospif(2.f * frac, &s, &c);
   return make_float2(c, s);
 }
 
@@ -59,19 +78,27 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t v) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
+// cs[j * stride] holds cosine and sine of the item's frequencies 2j and 2j + 1.
 template <bool NEAR>
-__device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float2* cs) {
+__device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float4* cs, int stride) {
   uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, b[4] = {x1.x, x1.y, x1.z, x1.w};
+  if (NEAR) {  // a word is a pair; frequencies 0 .. 3 in the first piece
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (NEAR) {  // a word is a pair; frequencies i (first piece) and 4 + i
-      const float2 u = unpack_bf16(a[i]), w = unpack_bf16(b[i]), c0 = cs[i], c1 = cs[4 + i];
-      a[i] = pack_bf16(u.x * c0.x - u.y * c0.y, u.y * c0.x + u.x * c0.y);
-      b[i] = pack_bf16(w.x * c1.x - w.y * c1.y, w.y * c1.x + w.x * c1.y);
-    } else {     // pairs run across the two pieces; frequencies 2i, 2i + 1
-      const float2 u = unpack_bf16(a[i]), w = unpack_bf16(b[i]), c0 = cs[2 * i], c1 = cs[2 * i + 1];
-      a[i] = pack_bf16(u.x * c0.x - w.x * c0.y, u.y * c1.x - w.y * c1.y);
-      b[i] = pack_bf16(w.x * c0.x + u.x * c0.y, w.y * c1.x + u.y * c1.y);
+    for (int j = 0; j < 4; ++j) {
+      const float4 w = cs[j * stride];
+      uint32_t& p0 = j < 2 ? a[2 * j] : b[2 * j - 4];
+      uint32_t& p1 = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+      const float2 u = unpack_bf16(p0), v = unpack_bf16(p1);
+      p0 = pack_bf16(u.x * w.x - u.y * w.y, u.y * w.x + u.x * w.y);
+      p1 = pack_bf16(v.x * w.z - v.y * w.w, v.y * w.z + v.x * w.w);
+    }
+  } else {     // pairs run across the two pieces
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 w = cs[j * stride];
+      const float2 u = unpack_bf16(a[j]), v = unpack_bf16(b[j]);
+      a[j] = pack_bf16(u.x * w.x - v.x * w.y, u.y * w.z - v.y * w.w);
+      b[j] = pack_bf16(v.x * w.x + u.x * w.y, v.y * w.z + u.y * w.w);
     }
   }
   x0 = make_uint4(a[0], a[1], a[2], a[3]);
@@ -80,95 +107,86 @@ __device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float2* cs
 
 template <int HD, bool NEAR>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
-  extern __shared__ float2 cs_s[];  // [tokens of the CTA][half], then their slots
+  extern __shared__ float4 cs_s[];  // [token of the CTA][4][half / 8]
   constexpr int IPH = HD / 16;      // items of a head
-  const int t0 = blockIdx.x * p.tokens_per_cta;
-  const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
-  int32_t* slot_s = reinterpret_cast<int32_t*>(cs_s + p.tokens_per_cta * p.half);
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads, qk = p.num_q_heads + p.num_kv_heads;
-  const int items = nt * heads * IPH;
+  const int tokens = p.side * kUnroll, t0 = blockIdx.x * tokens;
+  const int nt = min(tokens, p.num_tokens - t0);
+  int32_t* slot_s = reinterpret_cast<int32_t*>(cs_s + tokens * (p.half / 2));  // [token of the CTA]
+  const int qk = p.num_q_heads + p.num_kv_heads;
   const int turning = p.half / 8;   // items of a head that turn; the others pass
-  // element offsets of an item's two pieces within its head
-  auto pieces = [&](int c, int& off0, int& off1) {
-    if (c < turning) {
-      off0 = NEAR ? c * 16 : c * 8;
-      off1 = NEAR ? off0 + 8 : p.half + off0;
-    } else {  // passing items follow the turning dims two pieces at a time
-      off0 = 2 * p.half + (c - turning) * 16;
-      off1 = off0 + 8;
-    }
-  };
+  // this thread's column and first token
+  const int tl0 = threadIdx.x / p.per_cta;
+  const int col = blockIdx.y * p.per_cta + threadIdx.x - tl0 * p.per_cta;
+  const int c = col % IPH, hh = col / IPH;
+  const bool is_q = hh < p.num_q_heads, is_k = !is_q && hh < qk;
+  const bool on = tl0 < p.side && hh < qk + p.num_kv_heads;
+  // element offsets of the item's two pieces within its head; passing items
+  // follow the turning dims two pieces at a time
+  const bool turns = c < turning;
+  const int off0 = !turns ? 2 * p.half + (c - turning) * 16 : NEAR ? c * 16 : c * 8;
+  const int off1 = turns && !NEAR ? p.half + off0 : off0 + 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  bool ready = false;
-  for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < items; i0 += kRopeThreads * kUnroll) {
-    uint4 x0[kUnroll], x1[kUnroll];
+  uint4 x0[kUnroll], x1[kUnroll];
+  if (on) {
+    const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+    const __nv_bfloat16* src = (is_q   ? p.q + hh * HD
+                                : is_k ? p.k + (hh - p.num_q_heads) * HD
+                                       : p.v + (hh - qk) * HD) +
+                               (t0 + tl0) * stride;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kRopeThreads;
-      if (i >= items) continue;
-      const int hi = i / IPH, tl = hi / heads, hh = hi - tl * heads;
-      const int64_t t = t0 + tl;
-      const __nv_bfloat16* src =
-          hh < p.num_q_heads ? p.q + t * p.q_stride + hh * HD
-          : hh < qk          ? p.k + t * p.k_stride + (hh - p.num_q_heads) * HD
-                             : p.v + t * p.v_stride + (hh - qk) * HD;
-      int off0, off1;
-      pieces(i % IPH, off0, off1);
-      x0[u] = __ldcs(reinterpret_cast<const uint4*>(src + off0));
-      x1[u] = __ldcs(reinterpret_cast<const uint4*>(src + off1));
-    }
-    if (!ready) {
-      for (int i = threadIdx.x; i < nt; i += kRopeThreads) slot_s[i] = p.slots[t0 + i];
-      for (int i = threadIdx.x; i < nt * p.half; i += kRopeThreads) {
-        const int tl = i / p.half, f = i - tl * p.half;
-        int axis = p.freq_axis ? p.freq_axis[f] : 0;
-        if (axis < 0 || axis >= p.n_axes) {
-          flag_error(p.error_flag, VG_DEVERR_INDEX);
-          axis = 0;
-        }
-        cs_s[i] = turn_of(p.positions[axis * p.pos_stride + t0 + tl], p.inv_freq[f]);
+    for (int u = 0; u < kUnroll; ++u)
+      if (tl0 + u * p.side < nt) {
+        x0[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * p.side * stride + off0));
+        x1[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * p.side * stride + off1));
       }
-      __syncthreads();
-      ready = true;
+  }
+  for (int i = threadIdx.x; i < nt; i += blockDim.x) slot_s[i] = p.slots[t0 + i];
+  for (int i = threadIdx.x; i < nt * p.half; i += blockDim.x) {
+    const int tl = i / p.half, f = i - tl * p.half;
+    int axis = p.freq_axis ? p.freq_axis[f] : 0;
+    if (axis < 0 || axis >= p.n_axes) {
+      flag_error(p.error_flag, VG_DEVERR_INDEX);
+      axis = 0;
     }
+    float2* at = reinterpret_cast<float2*>(cs_s + tl * (p.half / 2) + (f % 8 / 2) * turning + f / 8) + f % 2;
+    *at = turn_of(p.positions[axis * p.pos_stride + t0 + tl], p.inv_freq[f]);
+  }
+  __syncthreads();
+  if (!on) return;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kRopeThreads;
-      if (i >= items) continue;
-      const int c = i % IPH, hi = i / IPH, tl = hi / heads, hh = hi - tl * heads;
-      if (c < turning && hh < qk) turn_item<NEAR>(x0[u], x1[u], cs_s + tl * p.half + c * 8);
-      __nv_bfloat16* dst;
-      if (hh < p.num_q_heads) {
-        dst = p.q_out + (int64_t)(t0 + tl) * p.q_out_stride + hh * HD;
-      } else {
-        const int slot = slot_s[tl];
-        if (slot < 0) continue;
-        if (slot >= p.num_slots) {
-          flag_error(p.error_flag, VG_DEVERR_INDEX);
-          continue;
-        }
-        const int h = hh < qk ? hh - p.num_q_heads : hh - qk;
-        dst = (hh < qk ? p.k_pages : p.v_pages) +
-              (((int64_t)(slot / kPageSize) * p.num_kv_heads + h) * kPageSize + slot % kPageSize) * HD;
+  for (int u = 0; u < kUnroll; ++u) {
+    const int tl = tl0 + u * p.side;
+    if (tl >= nt) break;
+    if (turns && hh < qk) turn_item<NEAR>(x0[u], x1[u], cs_s + tl * (p.half / 2) + c, turning);
+    __nv_bfloat16* dst;
+    if (is_q) {
+      dst = p.q_out + (t0 + tl) * p.q_out_stride + hh * HD;
+    } else {
+      const int slot = slot_s[tl];
+      if (slot < 0) continue;
+      if (slot >= p.num_slots) {
+        flag_error(p.error_flag, VG_DEVERR_INDEX);
+        continue;
       }
-      int off0, off1;
-      pieces(c, off0, off1);
-      *reinterpret_cast<uint4*>(dst + off0) = x0[u];
-      *reinterpret_cast<uint4*>(dst + off1) = x1[u];
+      const int h = is_k ? hh - p.num_q_heads : hh - qk;
+      dst = (is_k ? p.k_pages : p.v_pages) +
+            (((int64_t)(slot / kPageSize) * p.num_kv_heads + h) * kPageSize + slot % kPageSize) * HD;
     }
+    *reinterpret_cast<uint4*>(dst + off0) = x0[u];
+    *reinterpret_cast<uint4*>(dst + off1) = x1[u];
   }
 }
 
 template <int HD>
-cudaError_t launch_rope(const RopeParams& p, bool near, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeParams& p, dim3 grid, int threads, bool near, cudaStream_t stream) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ceil_div(p.num_tokens, p.tokens_per_cta));
-  cfg.blockDim = dim3(kRopeThreads);
-  cfg.dynamicSmemBytes = (size_t)p.tokens_per_cta * (p.half * sizeof(float2) + sizeof(int32_t));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)p.side * kUnroll * (p.half * sizeof(float2) + sizeof(int32_t));
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
@@ -228,16 +246,19 @@ extern "C" vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_
   p.num_tokens = num_tokens;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = kv->num_kv_heads;
-  p.head_dim = d;
   p.num_slots = kv->num_pages * kPageSize;
   p.n_axes = n_axes;
   p.half = rot_dim / 2;
-  // as many tokens as give every thread kUnroll items, at most 64 (their
-  // angles then fit 32 KB), at least one
-  const int items = (num_q_heads + 2 * kv->num_kv_heads) * (d / 16);
-  int tpc = kRopeThreads * kUnroll / items;
-  p.tokens_per_cta = tpc < 1 ? 1 : tpc > 64 ? 64 : tpc;
-  const cudaError_t e = d == 128 ? launch_rope<128>(p, interleaved != 0, stream)
-                                 : launch_rope<64>(p, interleaved != 0, stream);
+  // Threads: as many tokens' columns side by side as fit kRopeThreads (at most
+  // 32 tokens, whose angles fit 48 KB); a token of more columns than that is
+  // cut over grid.y into equal parts of whole warps.
+  const int columns = (num_q_heads + 2 * kv->num_kv_heads) * (d / 16);
+  const int parts = ceil_div(columns, kRopeThreads);
+  p.per_cta = parts == 1 ? columns : ceil_div(ceil_div(columns, parts), 32) * 32;
+  p.side = kRopeThreads / p.per_cta < 32 ? kRopeThreads / p.per_cta : 32;
+  const int threads = ceil_div(p.side * p.per_cta, 32) * 32;
+  const dim3 grid(ceil_div(num_tokens, p.side * kUnroll), parts);
+  const cudaError_t e = d == 128 ? launch_rope<128>(p, grid, threads, interleaved != 0, stream)
+                                 : launch_rope<64>(p, grid, threads, interleaved != 0, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }
