@@ -157,8 +157,16 @@ class PagedKV:
                              self.page_table.data_ptr(), P, S, self.page_table.shape[1], H, D)
 
     def pointer(self):
-        """struct() by reference, for a call that is made at once."""
-        return ctypes.byref(self.struct())
+        """struct() by reference for a call.  The struct is made again when the
+        tensors are not what it says."""
+        k, v, t = self.k_pages, self.v_pages, self.page_table
+        now = (k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, t.shape)
+        kept = self.__dict__.get("_kept")
+        if kept is None or kept[0] != now:
+            if not (k.is_cuda and v.is_cuda and t.is_cuda):
+                raise ValueError("the paged cache has to be on a GPU")
+            kept = self.__dict__["_kept"] = (now, self.struct())
+        return ctypes.byref(kept[1])
 
 
 # --------------------------------------------------------------------- verify
@@ -325,42 +333,42 @@ def _expect(ok, what):
 
 
 def _int32(t, n, name):
-    """Device pointer of a contiguous int32 tensor of n elements (n None: any)."""
-    if not (t.dtype is torch.int32 and t.is_cuda and t.is_contiguous()
-            and (n is None or t.numel() == n)):
+    """Device pointer of a contiguous int32 tensor of n elements."""
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} elements is needed")
     return t.data_ptr()
 
 
-def _opt(t, n, name):
-    return None if t is None else _int32(t, n, name)
+def _flag(t):
+    """Device pointer of an error flag (or None)."""
+    return None if t is None else _int32(t, t.numel(), "error_flag")
 
 
 def _heads(t, name):
     """(pointer, tokens, heads, head_dim, elements between tokens) of bf16 rows
     [T][H][d] whose heads are contiguous within a token."""
-    if t.dim() != 3 or t.dtype is not torch.bfloat16 or not t.is_cuda:
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name}: a bfloat16 GPU tensor [tokens][heads][head_dim] is needed")
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if n > 0 and (s2 != 1 or (s1 != d and h > 1)):
+    if (s2 != 1 or (s1 != d and h > 1)) and n > 0:
         raise ValueError(f"{name}: the heads of a token have to be contiguous")
     return t.data_ptr(), n, h, d, s0 if n > 1 else h * d
 
 
-def _device_stream(t, stream):
-    """Raw stream for a call on tensor t's device: the given one, or that
-    device's current stream."""
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device, without a Stream object
 
 
-def _call(fn, t, *args):
-    """Call an entry point with t's device current."""
-    if t.device.index == torch.cuda.current_device():
-        status = fn(*args)
+def _call(fn, t, stream, *args):
+    """Call an entry point on the given stream (None: the current stream of t's
+    device) with t's device current."""
+    dev = t.get_device()
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
     else:
-        with torch.cuda.device(t.device):
-            status = fn(*args)
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
     if status != 0:
         raise VGError(fn.__name__, status)
 
@@ -375,14 +383,19 @@ def step_tables(page_table, num_pages, cached_lens, new_lens, cu_tokens, kv_lens
     Outputs: cu_tokens [B + 1], kv_lens [B], positions and slots [max_tokens]."""
     _expect(page_table.dim() == 2, "page_table: [batch][max_pages] is needed")
     B, width = page_table.shape
-    _expect(slots.numel() == positions.numel(), "positions and slots differ in length")
-    _call(_lib.vg_step_tables, page_table, _int32(cached_lens, B, "cached_lens"),
-          _int32(new_lens, B, "new_lens"), B, _int32(page_table, None, "page_table"), width,
-          int(num_pages), _opt(owned, B, "owned"), _opt(free_pages, None, "free_pages"),
-          0 if free_pages is None else free_pages.numel(), _opt(free_count, 1, "free_count"),
-          positions.numel(), _int32(cu_tokens, B + 1, "cu_tokens"), _int32(kv_lens, B, "kv_lens"),
-          _int32(positions, None, "positions"), _int32(slots, None, "slots"),
-          _opt(error_flag, None, "error_flag"), _device_stream(page_table, stream))
+    T = positions.numel()
+    pool = (None, None, 0, None)
+    if owned is not None or free_pages is not None or free_count is not None:
+        _expect(owned is not None and free_pages is not None and free_count is not None,
+                "owned, free_pages and free_count are given together")
+        n = free_pages.numel()
+        pool = (_int32(owned, B, "owned"), _int32(free_pages, n, "free_pages"), n,
+                _int32(free_count, 1, "free_count"))
+    _call(_lib.vg_step_tables, page_table, stream, _int32(cached_lens, B, "cached_lens"),
+          _int32(new_lens, B, "new_lens"), B, _int32(page_table, B * width, "page_table"), width,
+          num_pages, *pool, T, _int32(cu_tokens, B + 1, "cu_tokens"),
+          _int32(kv_lens, B, "kv_lens"), _int32(positions, T, "positions"),
+          _int32(slots, T, "slots"), _flag(error_flag))
     return cu_tokens, kv_lens, positions, slots
 
 
@@ -396,30 +409,34 @@ def rope_append(kv: PagedKV, q, k, v, slots, q_out=None, positions=None, inv_fre
     inv_freq float32 [rot / 2] (None: nothing turns); freq_axis int32 [rot / 2]."""
     kp, T, H, d, ks = _heads(k, "k")
     vp, Tv, Hv, dv, vs = _heads(v, "v")
-    _expect(T == Tv and H == Hv == kv.num_kv_heads and d == dv == kv.head_dim,
-            "k and v do not match each other or the cache")
+    _, Hc, _, dc = kv.k_pages.shape
+    if not (T == Tv and H == Hv == Hc and d == dv == dc):
+        raise ValueError("k and v do not match each other or the cache")
     qp = op = None
     Hq = qs = os_ = 0
     if q is not None:
         qp, Tq, Hq, dq, qs = _heads(q, "q")
         op, To, Ho, do, os_ = (qp, Tq, Hq, dq, qs) if q_out is None else _heads(q_out, "q_out")
-        _expect(Tq == To == T and Ho == Hq and dq == do == d, "q or q_out does not match k")
-    pos = freq = None
+        if not (Tq == To == T and Ho == Hq and dq == do == d):
+            raise ValueError("q or q_out does not match k")
+    pos = freq = axis = None
     axes, ps, rot = 0, 0, 0
     if inv_freq is not None:
-        _expect(inv_freq.dtype is torch.float32 and inv_freq.is_cuda and inv_freq.is_contiguous(),
-                "inv_freq: a contiguous float32 GPU tensor is needed")
+        if inv_freq.dtype is not torch.float32 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq: a contiguous float32 GPU tensor is needed")
         _expect(positions is not None, "positions are needed with inv_freq")
-        _expect(positions.dtype is torch.int32 and positions.is_cuda and positions.dim() <= 2
-                and positions.shape[-1] == T and (T < 2 or positions.stride(-1) == 1),
-                "positions: int32 [tokens] or [axes][tokens] on the GPU is needed")
+        if (positions.dtype is not torch.int32 or not positions.is_cuda or positions.dim() > 2
+                or positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1)):
+            raise ValueError("positions: int32 [tokens] or [axes][tokens] on the GPU is needed")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
         ps = T if axes == 1 else positions.stride(0)
-        pos, freq, rot = positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel()
-    _call(_lib.vg_rope_append, k, kv.pointer(), qp, qs, kp, ks, vp, vs, op, os_, T, Hq, pos, ps,
-          axes, freq, _opt(freq_axis, rot // 2, "freq_axis"), rot, 1 if interleaved else 0,
-          _int32(slots, T, "slots"), _opt(error_flag, None, "error_flag"),
-          _device_stream(k, stream))
+        half = inv_freq.numel()
+        pos, freq, rot = positions.data_ptr(), inv_freq.data_ptr(), 2 * half
+        if freq_axis is not None:
+            axis = _int32(freq_axis, half, "freq_axis")
+    _call(_lib.vg_rope_append, k, stream, kv.pointer(), qp, qs, kp, ks, vp, vs, op, os_, T, Hq, pos,
+          ps, axes, freq, axis, rot, 1 if interleaved else 0, _int32(slots, T, "slots"),
+          _flag(error_flag))
     return q if q_out is None else q_out
 
 
@@ -436,20 +453,21 @@ def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None,
     given)."""
     qp, T, Hq, d, qs = _heads(q, "q")
     op, To, Ho, do, os_ = _heads(out, "out")
-    _expect(T == To and Hq == Ho and d == do == kv.head_dim, "out or the cache does not match q")
+    if not (T == To and Hq == Ho and d == do == kv.head_dim):
+        raise ValueError("out or the cache does not match q")
     B = kv_lens.numel()
     _expect(kv.page_table.shape[0] == B, "the cache's page table has another batch size")
     if lse is not None:
         _expect(lse.dtype is torch.float32 and lse.is_cuda and lse.is_contiguous()
                 and lse.numel() == T * Hq, "lse: a contiguous float32 GPU tensor [T][Hq] is needed")
     if workspace is None:
-        workspace = torch.empty(max(chunk_workspace_bytes(B, T, Hq, kv.num_kv_heads, d), 1),
-                                dtype=torch.uint8, device=q.device)
-    _call(_lib.vg_chunk_attention, q, kv.pointer(), qp, qs, _int32(cu_q, B + 1, "cu_q"),
+        with torch.cuda.device(q.device):   # its size goes by the device
+            n = chunk_workspace_bytes(B, T, Hq, kv.num_kv_heads, d)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    _call(_lib.vg_chunk_attention, q, stream, kv.pointer(), qp, qs, _int32(cu_q, B + 1, "cu_q"),
           _int32(kv_lens, B, "kv_lens"), B, T, Hq, softmax_scale, op, os_,
-          None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _opt(error_flag, None, "error_flag"),
-          _device_stream(q, stream))
+          None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+          _flag(error_flag))
     return out
 
 
