@@ -30,13 +30,13 @@
 //    one, exact range in bf16 and far from the fp32 range in l and O.
 //  * A producer warp streams K and V tiles (TMA, 128-byte swizzle) through a
 //    ring of stages and publishes the CTA's units; one warp issues every
-//    tensor-core operation.  A page of a head is one TMA box: at about 100
+//    tensor-core operation (a warp for each warpgroup was slower: the two
+//    streams of products then mix on the tensor cores and finish together).  A page of a head is one TMA box: at about 100
 //    cycles a box, two boxes a page (one per 64-dim block) held a CTA to one
 //    64 KB tile of K and V in 3300 cycles.
 //  * Position tiles that some row of the unit does not attend in full (the
-//    diagonal and the end of the cache) pass through two checking warps
-//    first: a weight of zero times a NaN or an infinity in V would still
-//    spoil the row, so they zero V past the length and take non-finite values
+//    diagonal and the end of the cache) pass through a checking warp first: a weight of zero times a NaN or an infinity in V would still
+//    spoil the row, so it zeroes V past the length and takes non-finite values
 //    out of the tile, noting per dimension the first position of each kind;
 //    rows that attend it get it back at the end.
 #include <math.h>
@@ -50,7 +50,7 @@ namespace {
 constexpr int kTile = 128;             // positions of a KV tile, rows of a row tile
 constexpr int kPagesPerTile = kTile / kPageSize;
 constexpr int kChunkThreads = 384;
-constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax)
+constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax, 11: idle)
 constexpr int kMaxBatch = 4096;
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that moves the reference
 constexpr int kRowsMax = 2 * kTile;    // rows of a unit
@@ -105,7 +105,7 @@ struct ChunkLayout {
   static constexpr int kSmall = kRing + kStages * kStageBytes;
   // small area: barriers, units, (m, l) exchange, non-finite notes
   static constexpr int kBars = kSmall;
-  static constexpr int kBarCount = 4 * kStages + 17;
+  static constexpr int kBarCount = 3 * kStages + 17;
   static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
   static constexpr int kFlags = kUnits + 2 * 48;
   static constexpr int kNotes = kFlags + 32;
@@ -122,12 +122,11 @@ static_assert(ChunkLayout<128>::kBytes <= 227 * 1024 && ChunkLayout<64>::kBytes 
 static_assert(sizeof(Unit) <= 48, "");
 
 struct ChunkBars {
-  // Ring stages: `full` (a K tile, or a V tile that needs no check, has
-  // landed), `landed` (a V tile to check has), `clean` (it was checked),
-  // `empty`.  Each use of a stage completes a phase of one of the first two
-  // only, so their parities are counted per stage (a bit mask), and whoever
-  // waits on one of them waits for every phase of it.
-  uint64_t *full, *landed, *clean, *empty;  // [stages]
+  // Ring stages.  `landed`: a V tile that is to be checked has landed; `full`:
+  // a tile may be read (it has landed, or it was checked); `empty`: its
+  // products are done.  Whoever waits on `full` or `landed`
+  // waits for every phase of it, so that a parity names one phase.
+  uint64_t *full, *landed, *empty;         // [stages]
   uint64_t *sfull, *ofull;                 // [2]: S, all of O of a warpgroup
   uint64_t *pfull;                         // [4]: halves of P of a warpgroup
   uint64_t *qfull, *qempty, *ufull, *uempty, *xfull, *xdone, *drain;
@@ -137,9 +136,8 @@ __device__ __forceinline__ ChunkBars chunk_bars(uint64_t* b, int stages) {
   ChunkBars r;
   r.full = b;
   r.landed = b + stages;
-  r.clean = b + 2 * stages;
-  r.empty = b + 3 * stages;
-  b += 4 * stages;
+  r.empty = b + 2 * stages;
+  b += 3 * stages;
   r.sfull = b;
   r.pfull = b + 2;
   r.ofull = b + 6;
@@ -231,6 +229,12 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// Non-zero when one of two packed bf16 is an infinity or a NaN (an exponent of
+// ones: adding the exponent's lowest bit carries out of it).
+__device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+  return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
 // A V entry with its non-finite value given back: rel = the row's token within
@@ -398,11 +402,10 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
           for (int j = 0; j < 64; ++j)
             o[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f_other, __uint_as_float(o[j])));
         }
-        if (note_flags[slot * 2] | note_flags[slot * 2 + 1]) {
+        if (note_flags[slot]) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            if (note_flags[slot * 2 + (c + j >= HD / 2)])
-              o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
+            o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
         }
         if (valid && direct) {
           __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + c;
@@ -491,117 +494,114 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   constexpr uint32_t NST = Lay::kStages;
   MmaIssuer<HD> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
                     umma_desc_lo(ring, 1024)};
-  uint32_t pc0 = 0, pc1 = 0, full = 0, clean = 0;  // parities
-  uint32_t at = 0;                                 // stage of the unit's first K tile
+  uint32_t pc0 = 0, pc1 = 0;  // tiles of the warpgroups so far
+  // next K's and V's ring stage and parity; entries are K(0), V(0), K(1) ...
+  uint32_t sk = 0, pk = 0, sv = 1, pv = 0;
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return chunk_wait_warp(bar, parity, p);
+  };
+  auto next = [](uint32_t& st, uint32_t& par) {
+    st += 2;
+    if (st >= NST) {
+      st -= NST;
+      par ^= 1;
+    }
+  };
+  // O(wg) (+)= P V: the first half of the positions while the warpgroup is
+  // still at the second
+  auto pv_product = [&](int wg, uint32_t st, bool accumulate) {
+    const uint32_t par = (wg ? pc1++ : pc0++) & 1;
+    if (!wait(&bars.pfull[2 * wg], par)) return false;
+    tc_fence_after();
+    mma.pv(wg, st, 0, accumulate);
+    if (!wait(&bars.pfull[2 * wg + 1], par)) return false;
+    tc_fence_after();
+    mma.pv(wg, st, 1, true);
+    return true;
+  };
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
     if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
     const int kt0 = same(units[slot].kt0), kt1 = same(units[slot].kt1), n0 = same(units[slot].n0);
-    const int pos0 = same(units[slot].pos0), two = same(units[slot].two);
+    const int two = same(units[slot].two);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.uempty[slot]);
     if (kt0 == kt1) return true;
     if (!chunk_wait_warp(bars.qfull, u & 1, p)) return false;
     const int n = kt1 - kt0;
-    const int e0 = two ? min(kt1, n0) - kt0 : n;  // tiles of warpgroup 0 (two row tiles)
-    // Ring entries are K(0), V(0), K(1), V(1) ...: waits for the entry at
-    // stage st (V tiles that are checked: until they are clean).
-    auto k_ready = [&](uint32_t st) {
-      const uint32_t par = (full >> st) & 1;
-      full ^= 1u << st;
-      return chunk_wait_warp(&bars.full[st], par, p);
-    };
-    auto v_ready = [&](uint32_t st, int j) {
-      if (!checked_tile(pos0, kt0 + j)) return k_ready(st);
-      const uint32_t par = (clean >> st) & 1;
-      clean ^= 1u << st;
-      return chunk_wait_warp(&bars.clean[st], par, p);
-    };
-    auto after = [](uint32_t st, uint32_t by) { return st + by >= NST ? st + by - NST : st + by; };
-    // O(wg) (+)= P V: the first half of the positions while the warpgroup is
-    // still at the second
-    auto pv = [&](int wg, uint32_t sv, bool accumulate) {
-      const uint32_t par = (wg ? pc1++ : pc0++) & 1;
-      if (!chunk_wait_warp(&bars.pfull[2 * wg], par, p)) return false;
-      tc_fence_after();
-      mma.pv(wg, sv, 0, accumulate);
-      if (!chunk_wait_warp(&bars.pfull[2 * wg + 1], par, p)) return false;
-      tc_fence_after();
-      mma.pv(wg, sv, 1, true);
-      return true;
-    };
-    uint32_t st = at;  // K(j)'s stage
     if (two) {
-      if (!k_ready(st)) return false;
+      const int e0 = min(kt1, n0) - kt0;  // tiles of the first row tile
+      if (!wait(&bars.full[sk], pk)) return false;
       tc_fence_after();
-      if (e0 > 0) mma.qk(0, 0, st);
-      mma.qk(1, 1, st);
-      umma_commit_elect(&bars.empty[st]);
+      if (e0 > 0) mma.qk(0, 0, sk);
+      mma.qk(1, 1, sk);
+      umma_commit_elect(&bars.empty[sk]);
       if (n == 1) umma_commit_elect(bars.qempty);
+      next(sk, pk);
       for (int j = 0; j < n; ++j) {
-        const uint32_t sv = after(st, 1), sk = after(st, 2);
         const bool more = j + 1 < n;
         // the tiles are waited for first, while the warpgroups are at P(j)
-        if (!v_ready(sv, j) || (more && !k_ready(sk))) return false;
+        if (!wait(&bars.full[sv], pv) || (more && !wait(&bars.full[sk], pk))) return false;
         if (j < e0) {
-          if (!pv(0, sv, j > 0)) return false;
+          if (!pv_product(0, sv, j > 0)) return false;
           if (j + 1 < e0)
             mma.qk(0, 0, sk);
           else
             umma_commit_elect(&bars.ofull[0]);
         }
-        if (!pv(1, sv, j > 0)) return false;
+        if (!pv_product(1, sv, j > 0)) return false;
         if (more) {
           mma.qk(1, 1, sk);
           umma_commit_elect(&bars.empty[sv]);
           umma_commit_elect(&bars.empty[sk]);
           if (j + 2 == n) umma_commit_elect(bars.qempty);
+          next(sk, pk);
         } else {
           umma_commit_elect(&bars.ofull[1]);
           umma_commit_elect(&bars.empty[sv]);
         }
-        st = sk;
+        next(sv, pv);
       }
     } else {
       for (int j = 0; j < min(n, 2); ++j) {
-        const uint32_t sk = after(st, 2 * j);
-        if (!k_ready(sk)) return false;
+        if (!wait(&bars.full[sk], pk)) return false;
         tc_fence_after();
         mma.qk(j, 0, sk);
         umma_commit_elect(&bars.empty[sk]);
+        next(sk, pk);
       }
       if (n <= 2) umma_commit_elect(bars.qempty);
       for (int j = 0; j < n; ++j) {
         const int wg = j & 1;
-        const uint32_t sv = after(st, 1), sk = after(st, 4);
-        if (!v_ready(sv, j) || !pv(wg, sv, j > 1)) return false;
+        if (!wait(&bars.full[sv], pv) || !pv_product(wg, sv, j > 1)) return false;
         if (j >= n - 2) umma_commit_elect(&bars.ofull[wg]);
         umma_commit_elect(&bars.empty[sv]);
+        next(sv, pv);
         if (j + 2 < n) {
-          if (!k_ready(sk)) return false;
+          // only now: a stream from HBM is behind, and V(j)'s stage is wanted
+          if (!wait(&bars.full[sk], pk)) return false;
           tc_fence_after();
           mma.qk(wg, 0, sk);
           umma_commit_elect(&bars.empty[sk]);
           if (j + 3 == n) umma_commit_elect(bars.qempty);
+          next(sk, pk);
         }
-        st = after(st, 2);
       }
     }
-    at = st;
   }
 }
 
 // ------------------------------------------------------------ V checks
-// Warp `half` of two owns half of the dimensions of every checked V tile.
 template <int HD>
 __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars& bars,
                                            const Unit* units, int* note_flags, uint16_t* notes_s,
-                                           uint8_t* ring, int half, int lane) {
+                                           uint8_t* ring, int lane) {
   using Lay = ChunkLayout<HD>;
   constexpr int NST = Lay::kStages;
-  constexpr int CPW = HD / 16;       // 16-byte pieces of a row per warp
-  constexpr int RPI = 32 / CPW;      // rows per pass
+  constexpr int CPR = HD / 8;        // 16-byte pieces of a row
+  constexpr int RPI = 32 / CPR;      // rows per pass
   uint32_t tiles = 0, landed = 0;
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
@@ -610,7 +610,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
     if (un.kt0 == un.kt1) return;
     uint16_t* notes = notes_s + slot * 3 * HD;
     bool noting = false;
-    if (lane == 0) note_flags[slot * 2 + half] = 0;
+    if (lane == 0) note_flags[slot] = 0;
     // the checked tiles are the last ones, from the first that has a position
     // past the first row's
     const int from = max(un.kt0, un.pos0 < 0 ? 0 : (un.pos0 + 1) / kTile);
@@ -619,40 +619,38 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
       if (!chunk_wait_warp(&bars.landed[st], (landed >> st) & 1, p)) return;
       landed ^= 1u << st;
       uint8_t* tile = ring + st * Lay::kStageBytes;
-      const int ch = half * CPW + lane % CPW;  // piece of the row
-      bool bad = false;
-#pragma unroll 4
+      // rows past the length are zeroed, those past the first row's position
+      // looked at (earlier ones are attended by every row)
+      const int last = min(un.len - kt * kTile, kTile);
+      const int begin = max(un.pos0 + 1 - kt * kTile, 0);
+      const int ch = lane % CPR;  // piece of the row
+      uint32_t bad = 0;
+#pragma unroll 8
       for (int r0 = 0; r0 < kTile; r0 += RPI) {
-        const int row = r0 + lane / CPW, pos = kt * kTile + row;
+        const int row = r0 + lane / CPR;
         uint4* at = reinterpret_cast<uint4*>(tile + Lay::kv_offset(row, ch));
-        if (pos >= un.len) {
+        if (row >= last) {
           *at = make_uint4(0u, 0u, 0u, 0u);
-        } else if (pos > un.pos0) {
+        } else if (row >= begin) {
           const uint4 v = *at;
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            bad |= (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
+          bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
         }
       }
-      if (__any_sync(0xffffffffu, bad)) {
-        if (!noting) {  // clear this warp's notes: no position sees them
-          for (int c = lane; c < 3 * HD / 2; c += 32)
-            notes[c / (HD / 2) * HD + half * (HD / 2) + c % (HD / 2)] = 0xffff;
+      if (__any_sync(0xffffffffu, bad != 0)) {
+        if (!noting) {  // clear the notes: no position sees them
+          for (int c = lane; c < 3 * HD; c += 32) notes[c] = 0xffff;
           noting = true;
-          if (lane == 0) note_flags[slot * 2 + half] = 1;
+          if (lane == 0) note_flags[slot] = 1;
         }
         __syncwarp();
         // a lane per dimension, rows in order
-        for (int c = half * (HD / 2) + lane; c < (half + 1) * (HD / 2); c += 32) {
-          for (int row = 0; row < kTile; ++row) {
-            const int pos = kt * kTile + row;
-            if (pos <= un.pos0 || pos >= un.len) continue;
+        for (int c = lane; c < HD; c += 32) {
+          for (int row = begin; row < last; ++row) {
             uint16_t* e = reinterpret_cast<uint16_t*>(tile + Lay::kv_offset(row, c >> 3)) + (c & 7);
             const uint16_t x = *e;
             if ((x & 0x7f80) != 0x7f80) continue;
             const int kind = (x & 0x7f) ? 0 : x & 0x8000 ? 2 : 1;
-            const int rel = min(pos - un.pos0, 0xfffe);
+            const int rel = min(kt * kTile + row - un.pos0, 0xfffe);
             if (rel < notes[kind * HD + c]) notes[kind * HD + c] = (uint16_t)rel;
             *e = 0;
           }
@@ -660,7 +658,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.clean[st]);
+      if (lane == 0) mbar_arrive(&bars.full[st]);
     }
     tiles += un.kt1 - un.kt0;
     __syncwarp();
@@ -826,7 +824,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
   long long at = s.unit_at;  // line position of the current unit's first tile
   int q0 = s.q0, n = s.n, len = s.len;
-  uint32_t ri = 0, u = 0, full = 0, landed = 0;
+  uint32_t ri = 0, u = 0, on_landed = 0, landed = 0;  // bits: last load of a stage, its parity
   bool live = true, q_armed = false;
   MergeUnit cut = {};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -918,10 +916,11 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
           tma_load_4d(ring + st * Lay::kStageBytes + pi * Lay::kPageBytes, v ? &tmv : &tmk, bar, 0, 0,
                       0, (id * p.num_kv_heads + h) * 2, policy);
         __syncwarp();
-        if (bar == &bars.full[st])
-          full ^= 1u << st;
-        else
+        on_landed &= ~(1u << st);
+        if (bar == &bars.landed[st]) {
+          on_landed |= 1u << st;
           landed ^= 1u << st;
+        }
         ++ri;
       }
     }
@@ -941,9 +940,12 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   if (lane == 0) {
     p.merge[blockIdx.x] = cut;
     if (!live) {
-      for (int st = 0; st < NST; ++st) {
-        mbar_wait(&bars.full[st], ((full >> st) & 1) ^ 1);
-        mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
+      for (uint32_t i = ri > NST ? ri - NST : 0; i < ri; ++i) {
+        const uint32_t st = i % NST;
+        if ((on_landed >> st) & 1)
+          mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
+        else
+          mbar_wait(&bars.full[st], (i / NST) & 1);
       }
       if (u > 0 && q_armed) mbar_wait(bars.qfull, (u - 1) & 1);
     }
@@ -973,7 +975,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 1);
       mbar_init(&bars.landed[i], 1);
-      mbar_init(&bars.clean[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.sfull[i], 1);
@@ -981,13 +982,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&bars.pfull[2 * i + 1], 4);
       mbar_init(&bars.ofull[i], 1);
       mbar_init(&bars.ufull[i], 1);
-      mbar_init(&bars.uempty[i], 8 + 1 + 2);
+      mbar_init(&bars.uempty[i], 8 + 1 + 1);
     }
     mbar_init(bars.qfull, 1);
     mbar_init(bars.qempty, 1);
+    mbar_init(bars.drain, 1);
     mbar_init(bars.xfull, 4);
     mbar_init(bars.xdone, 4);
-    mbar_init(bars.drain, 1);
     fence_barrier_init();
   }
   if (warp == kMma) tmem_alloc(tmem_at, 512);
@@ -1023,9 +1024,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       umma_commit_elect(bars.drain);
       if (lane == 0) mbar_wait(bars.drain, 0);
     }
-    __syncwarp();
-  } else {
-    check_role<HD>(p, bars, units, note_flags, notes, smem + Lay::kRing, warp - kChecker, lane);
+  } else if (warp == kChecker) {
+    check_role<HD>(p, bars, units, note_flags, notes, smem + Lay::kRing, lane);
   }
   __syncwarp();
   tc_fence_before();
