@@ -9,10 +9,10 @@
 //    floor(128 / g) tokens of a tile times their g query heads, packed token
 //    by token, so K and V are read once for all heads of the group.  Its work
 //    is the 128-position tiles up to its last row's position.
-//  * All units' tiles form one line (sequence, KV head, row tiles; a unit counts
-//    two tiles more, for its Q, its first scores and its epilogue), cut into
-//    equal shares, one per CTA: any mix of long prompts and single tokens is
-//    balanced to a tile.  KV heads outrank row tiles on the line so that the
+//  * All units' tiles form one line (sequence, KV head, row tiles; weighted by
+//    what they cost), cut into equal shares, one per CTA: any mix of long
+//    prompts and single tokens is balanced to a tile.  KV heads outrank row
+//    tiles on the line so that the
 //    CTAs of a long prompt stream the same few heads, which L2 holds.  A unit
 //    that a cut divides leaves fp32 partials (m, l, O) in the workspace; a
 //    small chained kernel merges them.  Every CTA finds its own share from
@@ -35,8 +35,9 @@
 //    cycles a box, two boxes a page (one per 64-dim block) held a CTA to one
 //    64 KB tile of K and V in 3300 cycles.
 //  * Position tiles that some row of the unit does not attend in full (the
-//    diagonal and the end of the cache) pass through a checking warp first: a weight of zero times a NaN or an infinity in V would still
-//    spoil the row, so it zeroes V past the length and takes non-finite values
+//    diagonal and the end of the cache) pass through two checking warps
+//    first: a weight of zero times a NaN or an infinity in V would still
+//    spoil the row, so they zero V past the length and take non-finite values
 //    out of the tile, noting per dimension the first position of each kind;
 //    rows that attend it get it back at the end.
 #include <math.h>
@@ -50,11 +51,14 @@ namespace {
 constexpr int kTile = 128;             // positions of a KV tile, rows of a row tile
 constexpr int kPagesPerTile = kTile / kPageSize;
 constexpr int kChunkThreads = 384;
-constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax, 11: idle)
+constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax; two checkers)
 constexpr int kMaxBatch = 4096;
 constexpr float kRescale = 8.f;        // log2 growth of a row maximum that moves the reference
 constexpr int kRowsMax = 2 * kTile;    // rows of a unit
-constexpr int kUnitCost = 2;           // what a unit costs beside its position tiles, in tiles
+// Costs on the line that the CTAs share: a position tile of a unit with two row
+// tiles or with one, and what a unit costs beside its tiles (Q, first scores,
+// epilogue).  Measured: 2900, 2400 and 7000 - 10000 cycles.
+constexpr int kTwoCost = 5, kOneCost = 4, kUnitCost = 15;
 
 struct ChunkParams {
   const int32_t* page_table;
@@ -165,10 +169,19 @@ __device__ __forceinline__ bool sequence_of(const ChunkParams& p, int b, int& q0
   return ok;
 }
 
+__device__ __forceinline__ int tile_cost(int ntok, int tu) { return 2 * ntok > tu ? kTwoCost : kOneCost; }
+
 // Length on the line of row-tile pair `rt` (tu tokens each) of a sequence: its
 // overhead, then its position tiles.
-__device__ __forceinline__ int unit_length(int n, int len, int tu, int rt) {
-  return kUnitCost + tiles_to(len - n + min((rt + 1) * tu, n) - 1);
+__device__ __forceinline__ long long unit_length(int n, int len, int tu, int rt) {
+  const int ntok = min(tu, n - rt * tu);
+  return kUnitCost + (long long)tile_cost(ntok, tu) * tiles_to(len - n + rt * tu + ntok - 1);
+}
+
+// A unit's position tiles that end before offset y of its length; a CTA whose
+// share holds [y0, y1) of it takes tiles [tiles_before(y0), tiles_before(y1)).
+__device__ __forceinline__ int tiles_before(long long y, int cost) {
+  return y <= kUnitCost ? 0 : (int)((y - kUnitCost) / cost);
 }
 
 // Whether some row of the unit does not attend all of tile kt (its first row
@@ -402,10 +415,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
           for (int j = 0; j < 64; ++j)
             o[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f_other, __uint_as_float(o[j])));
         }
-        if (note_flags[slot]) {
+        if (note_flags[slot * 2] | note_flags[slot * 2 + 1]) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
-            o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
+            if (note_flags[slot * 2 + (c + j >= HD / 2)])
+              o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
         }
         if (valid && direct) {
           __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + c;
@@ -594,14 +608,15 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
 }
 
 // ------------------------------------------------------------ V checks
+// Warp `half` of two owns half of the dimensions of every checked V tile.
 template <int HD>
 __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars& bars,
                                            const Unit* units, int* note_flags, uint16_t* notes_s,
-                                           uint8_t* ring, int lane) {
+                                           uint8_t* ring, int half, int lane) {
   using Lay = ChunkLayout<HD>;
   constexpr int NST = Lay::kStages;
-  constexpr int CPR = HD / 8;        // 16-byte pieces of a row
-  constexpr int RPI = 32 / CPR;      // rows per pass
+  constexpr int CPW = HD / 16;       // 16-byte pieces of a row per warp
+  constexpr int RPI = 32 / CPW;      // rows per pass
   uint32_t tiles = 0, landed = 0;
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
@@ -610,7 +625,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
     if (un.kt0 == un.kt1) return;
     uint16_t* notes = notes_s + slot * 3 * HD;
     bool noting = false;
-    if (lane == 0) note_flags[slot] = 0;
+    if (lane == 0) note_flags[slot * 2 + half] = 0;
     // the checked tiles are the last ones, from the first that has a position
     // past the first row's
     const int from = max(un.kt0, un.pos0 < 0 ? 0 : (un.pos0 + 1) / kTile);
@@ -623,28 +638,27 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
       // looked at (earlier ones are attended by every row)
       const int last = min(un.len - kt * kTile, kTile);
       const int begin = max(un.pos0 + 1 - kt * kTile, 0);
-      const int ch = lane % CPR;  // piece of the row
+      const int ch = half * CPW + lane % CPW, r = lane / CPW;  // piece of the row, row of the pass
       uint32_t bad = 0;
 #pragma unroll 8
-      for (int r0 = 0; r0 < kTile; r0 += RPI) {
-        const int row = r0 + lane / CPR;
-        uint4* at = reinterpret_cast<uint4*>(tile + Lay::kv_offset(row, ch));
-        if (row >= last) {
-          *at = make_uint4(0u, 0u, 0u, 0u);
-        } else if (row >= begin) {
-          const uint4 v = *at;
-          bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-        }
+      for (int r0 = begin; r0 < last; r0 += RPI) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + Lay::kv_offset(min(r0 + r, last - 1), ch));
+        bad |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
       }
+#pragma unroll 4
+      for (int r0 = max(last, 0); r0 < kTile; r0 += RPI)
+        if (r0 + r < kTile)
+          *reinterpret_cast<uint4*>(tile + Lay::kv_offset(r0 + r, ch)) = make_uint4(0u, 0u, 0u, 0u);
       if (__any_sync(0xffffffffu, bad != 0)) {
-        if (!noting) {  // clear the notes: no position sees them
-          for (int c = lane; c < 3 * HD; c += 32) notes[c] = 0xffff;
+        if (!noting) {  // clear this warp's notes: no position sees them
+          for (int c = lane; c < 3 * HD / 2; c += 32)
+            notes[c / (HD / 2) * HD + half * (HD / 2) + c % (HD / 2)] = 0xffff;
           noting = true;
-          if (lane == 0) note_flags[slot] = 1;
+          if (lane == 0) note_flags[slot * 2 + half] = 1;
         }
         __syncwarp();
         // a lane per dimension, rows in order
-        for (int c = lane; c < HD; c += 32) {
+        for (int c = half * (HD / 2) + lane; c < (half + 1) * (HD / 2); c += 32) {
           for (int row = begin; row < last; ++row) {
             uint16_t* e = reinterpret_cast<uint16_t*>(tile + Lay::kv_offset(row, c >> 3)) + (c & 7);
             const uint16_t x = *e;
@@ -758,7 +772,9 @@ __device__ __forceinline__ Share find_share(const ChunkParams& p, const Sequence
     }
     __syncwarp();
   }
-  const long long share = quotient(total + gridDim.x - 1, gridDim.x);
+  // at least one tile, so that every CTA inside a divided unit has a part of it
+  const long long share = max(quotient(total + gridDim.x - 1, gridDim.x),
+                              (long long)(p.rows == kTile ? kOneCost : kTwoCost));
   const long long x0 = share * blockIdx.x;
   Share s = {};
   s.share = share;
@@ -802,7 +818,7 @@ __device__ __forceinline__ Share find_share(const ChunkParams& p, const Sequence
     }
     before += __shfl_sync(0xffffffffu, v, 31);
   }
-  s.kt0 = max((int)(y - before) - kUnitCost, 0);
+  s.kt0 = tiles_before(y - before, tile_cost(min(tu, s.n - s.rt * tu), tu));
   s.unit_at = x0 - (y - before);
   return s;
 }
@@ -833,7 +849,9 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     return __shfl_sync(0xffffffffu, go, 0) != 0;
   };
   while (live) {
-    const bool more = b >= 0 && at + kUnitCost + kt0 < s.x1;  // its next position tile is in the share
+    const int ntok = min(tu, n - rt * tu), cost = tile_cost(ntok, tu);
+    // its next position tile ends in the share
+    const bool more = b >= 0 && at + kUnitCost + (long long)cost * (kt0 + 1) <= s.x1;
     const int slot = u & 1;
     if (u >= 2 && !wait(&bars.uempty[slot], ((u >> 1) - 1) & 1)) {
       live = false;
@@ -842,7 +860,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     Unit un = {};
     if (more) {
       un.tok0 = q0 + rt * tu;
-      un.ntok = min(tu, n - rt * tu);
+      un.ntok = ntok;
       un.pos0 = len - n + rt * tu;
       un.len = len;
       un.h = h;
@@ -850,9 +868,9 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
       un.n0 = tiles_to(un.pos0 + min(tt, un.ntok) - 1);
       const int tiles = tiles_to(un.pos0 + un.ntok - 1);
       un.kt0 = kt0;
-      un.kt1 = (int)min((long long)tiles, s.x1 - at - kUnitCost);
+      un.kt1 = min(tiles, tiles_before(s.x1 - at, cost));
       un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
-      at += kUnitCost + tiles;  // the next unit's
+      at += kUnitCost + (long long)cost * tiles;  // the next unit's
       if (kt0 == 0 && un.kt1 < tiles) {
         cut.parts = (int)quotient(at - 1, s.share) - (int)blockIdx.x + 1;
         cut.tok0 = un.tok0;
@@ -910,7 +928,10 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
           break;
         }
         uint64_t* bar = &(v && checked_tile(un.pos0, kt) ? bars.landed : bars.full)[st];
-        if (lane == 0) mbar_arrive_expect_tx(bar, Lay::kStageBytes);
+        if (lane == 0) {
+          if (bar == &bars.full[st]) mbar_arrive(bar);  // for the second checker
+          mbar_arrive_expect_tx(bar, Lay::kStageBytes);
+        }
         __syncwarp();
         if (lane < kPagesPerTile)
           tma_load_4d(ring + st * Lay::kStageBytes + pi * Lay::kPageBytes, v ? &tmv : &tmk, bar, 0, 0,
@@ -972,7 +993,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
     for (int i = 0; i < Lay::kStages; ++i) {
-      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.full[i], 2);
       mbar_init(&bars.empty[i], 1);
       mbar_init(&bars.landed[i], 1);
     }
@@ -982,7 +1003,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&bars.pfull[2 * i + 1], 4);
       mbar_init(&bars.ofull[i], 1);
       mbar_init(&bars.ufull[i], 1);
-      mbar_init(&bars.uempty[i], 8 + 1 + 1);
+      mbar_init(&bars.uempty[i], 8 + 1 + 2);
     }
     mbar_init(bars.qfull, 1);
     mbar_init(bars.qempty, 1);
@@ -1024,8 +1045,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       umma_commit_elect(bars.drain);
       if (lane == 0) mbar_wait(bars.drain, 0);
     }
-  } else if (warp == kChecker) {
-    check_role<HD>(p, bars, units, note_flags, notes, smem + Lay::kRing, lane);
+  } else {
+    check_role<HD>(p, bars, units, note_flags, notes, smem + Lay::kRing, warp - kChecker, lane);
   }
   __syncwarp();
   tc_fence_before();
