@@ -14,7 +14,8 @@ What stands in for the parts of a model outside the attention path:
   * projections      q, k, v = bf16(h W_q), bf16(h W_k), bf16(h W_v), computed
                      in float64 so that the bf16 values do not depend on the
                      summation order
-  * residual         x <- x + o   (no output projection, RoPE or MLP)
+  * residual         x <- x + o   (no output projection or MLP; rotary
+                     positions only when the spec sets rope_theta)
   * next token       the input vector of the token after position p is the
                      RMS-normalised final residual of position p (stands in
                      for LM head, sampling and embedding lookup)
@@ -31,8 +32,13 @@ n + a + 1 tokens, the next input comes from verify row a, and the next drafts'
 tail starts at n.  A first one-row verify of the first token seeds the
 selection.
 
-The projections, norms and K/V writes are PyTorch plumbing; every attention
-step runs in libvg's kernels through the C ABI.
+A prompt enters through prefill(), in one piece or in chunks, before the seed
+verify: its rows attend the cache and themselves causally.
+
+The projections and norms are PyTorch plumbing; positions and cache slots
+(vg_step_tables, once per step), K/V writes with rotary positions
+(vg_rope_append) and every attention step run in libvg's kernels through the C
+ABI.
 """
 from __future__ import annotations
 
@@ -136,6 +142,11 @@ class DecodeStack:
         self.ws_draft = vg.zero_workspace(
             vg.sparse_draft_workspace_bytes(B, Hq, Hkv, d, self.cap, self.max_tail), dev)
         self.flag = torch.zeros(1, dtype=torch.int32, device=dev)
+        # rotary frequencies (None: no rotary positions)
+        self.inv_freq = None if not s.rope_theta else (
+            s.rope_theta ** (-torch.arange(d // 2, dtype=torch.float64) * 2 / d)).float().to(dev)
+        self.placed = [int(L) for L in s.prefix_lens]   # tokens cached by prefill, on the host
+        self._places = {}
         self.draws = make_acceptance(s)
         self.iteration = 0
         self.accepted: List[torch.Tensor] = []
@@ -155,14 +166,40 @@ class DecodeStack:
         v = y[..., self.nq + self.nk:].reshape(*shp, s.num_kv_heads, s.head_dim)
         return q.contiguous(), k, v
 
+    def _place(self, pos, n):
+        """Rows, lengths, positions and cache slots of a step that adds n tokens
+        (an int, or an int32 tensor of as many per sequence as `total` rows hold)
+        to every sequence from position pos[b]; the layers' writes use them."""
+        B = self.spec.batch
+        new, total = (n, int(n.sum())) if isinstance(n, torch.Tensor) else (n, n * B)
+        key = n if isinstance(n, int) else -total
+        if key not in self._places:
+            i32 = lambda m: torch.empty(m, dtype=torch.int32, device=self.device)  # noqa: E731
+            self._places[key] = dict(new=i32(B), cu=i32(B + 1), lens=i32(B), positions=i32(total),
+                                     slots=i32(total))
+            if isinstance(n, int):
+                self._places[key]["new"].fill_(n)
+        self.at = at = self._places[key]
+        if isinstance(n, torch.Tensor):
+            at["new"].copy_(new)
+        vg.step_tables(self.page_table, self.num_pages, pos, at["new"], at["cu"], at["lens"],
+                       at["positions"], at["slots"], error_flag=self.flag)
+
     def _write_kv(self, l, k, v, pos):
-        """k, v [B][n][Hkv][d] to positions pos[b] + 0..n-1."""
-        n = k.shape[1]
-        p = pos[:, None].long() + torch.arange(n, device=self.device)[None, :]
-        phys = torch.gather(self.page_table.long(), 1, p // PAGE_SIZE)
-        slot = p % PAGE_SIZE
-        self.kp[l][phys, :, slot] = k
-        self.vp[l][phys, :, slot] = v
+        """k, v [B][n][Hkv][d] to positions pos[b] + 0..n-1, where _place put
+        them."""
+        vg.rope_append(self.kv[l], None, k.flatten(0, 1), v.flatten(0, 1), self.at["slots"],
+                       error_flag=self.flag)
+
+    def _append(self, l, q, k, v, pos):
+        """Write the step's K/V rows; with rotary positions, turn q (in place)
+        and the written keys."""
+        if self.inv_freq is None:
+            self._write_kv(l, k, v, pos)
+            return
+        vg.rope_append(self.kv[l], q.flatten(0, -3), k.flatten(0, -3), v.flatten(0, -3),
+                       self.at["slots"], positions=self.at["positions"], inv_freq=self.inv_freq,
+                       error_flag=self.flag)
 
     def _timed(self, kind, fn, *args, **kw):
         if self.timing is None:
@@ -196,14 +233,55 @@ class DecodeStack:
             self.indices[l].copy_(r[0])
             self.counts[l].copy_(r[1])
 
+    def prefill(self, inputs: torch.Tensor, new_lens) -> torch.Tensor:
+        """Add a chunk of prompt tokens to every sequence, before the seed
+        verify: inputs float64 [T][hidden], the sequences' input vectors one
+        after another, new_lens the number of each (0 allowed).  Their rows
+        attend everything cached and themselves causally.  The next token's
+        input becomes the normalised residual of each sequence's last row.
+        Returns the final residuals [T][hidden]."""
+        s = self.spec
+        new = [int(n) for n in new_lens]
+        if len(new) != s.batch or min(new) < 0 or sum(new) != inputs.shape[0]:
+            raise ValueError("prefill: new_lens does not match the batch or the input rows")
+        after = [a + n for a, n in zip(self.placed, new)]
+        if any(m > L + s.prompt for m, L in zip(after, s.prefix_lens)):
+            raise ValueError(f"prefill: more than the spec's {s.prompt} prompt tokens")
+        if sum(new) == 0:
+            return inputs
+        T = inputs.shape[0]
+        pos = torch.tensor(self.placed, dtype=torch.int32, device=self.device)
+        self._place(pos, torch.tensor(new, dtype=torch.int32))
+        ws = vg.zero_workspace(vg.chunk_workspace_bytes(
+            s.batch, T, s.num_q_heads, s.num_kv_heads, s.head_dim), self.device)
+        x = inputs
+        for l in range(s.layers):
+            q, k, v = self._qkv(l, x[None])
+            self._append(l, q, k, v, pos)
+            out = torch.empty(T, s.num_q_heads, s.head_dim, dtype=torch.bfloat16,
+                              device=self.device)
+            self._timed("chunk", vg.chunk_attention, self.kv[l], q[0], self.at["cu"],
+                        self.at["lens"], s.softmax_scale, out, workspace=ws, error_flag=self.flag)
+            if self.record:
+                self.record("chunk", l, dict(out=out, q=q[0]))
+            x = x + out.double().reshape(T, -1)
+        self.placed = after
+        self.lens = torch.tensor(after, dtype=torch.int32, device=self.device)
+        self.tail_start = self.lens.clone()
+        last = torch.tensor(new, device=self.device).cumsum(0) - 1
+        has = torch.tensor([n > 0 for n in new], device=self.device)
+        self.e = torch.where(has[:, None], _rms(x[last.clamp(min=0)]), self.e)
+        return x
+
     def seed_selection(self):
         """A one-row verify of the first token over the initial context
         seeds every layer's selection; the token is committed."""
         s = self.spec
         x = self.e[:, None, :]                                   # [B][1][H]
+        self._place(self.lens, 1)
         for l in range(s.layers):
             q, k, v = self._qkv(l, x)
-            self._write_kv(l, k, v, self.lens)
+            self._append(l, q, k, v, self.lens)
             out = self._verify_select(l, q, 1)
             if self.record:
                 self.record("seed", l, dict(out=out, capture=self.capture,
@@ -223,9 +301,10 @@ class DecodeStack:
             pos = self.lens + (t - 1)
             cur = pos + 1
             x = block[-1]
+            self._place(pos, 1)
             for l in range(s.layers):
                 q, kk, vv = self._qkv(l, x)
-                self._write_kv(l, kk[:, None], vv[:, None], pos)
+                self._append(l, q[:, None], kk[:, None], vv[:, None], pos)
                 out = torch.empty(B, s.num_q_heads, s.head_dim, dtype=torch.bfloat16,
                                   device=self.device)
                 self._timed("draft", vg.sparse_draft_attention, self.kv[l], q, self.indices[l],
@@ -237,9 +316,10 @@ class DecodeStack:
                 x = x + out.double().reshape(B, -1)
             block.append(_rms(x))
         X = torch.stack(block, dim=1)                            # [B][k+1][H]
+        self._place(self.lens, k + 1)
         for l in range(s.layers):
             q, kk, vv = self._qkv(l, X)
-            self._write_kv(l, kk, vv, self.lens)
+            self._append(l, q, kk, vv, self.lens)
             out = self._verify_select(l, q, k + 1)
             if self.record:
                 self.record("verify", l, dict(out=out, capture=self.capture,
@@ -256,13 +336,15 @@ class DecodeStack:
 
     def launches_per_iteration(self) -> int:
         """Kernels per layer and draft/verify iteration: k drafts, the verify
-        (+ split merge) and the selection."""
+        (+ split merge), the selection and the k + 1 writes of new K/V (the
+        k + 1 block-table kernels of an iteration serve every layer and are
+        not counted)."""
         s = self.spec
         merge = 1 if self.ws_verify[self.R].numel() > 1 else 0
         with torch.cuda.device(self.device):
             sel = vg.select_launches(vg.CAPTURE_GROUP_SUM, s.batch, s.num_kv_heads, s.max_prefix,
                                      s.per_head)
-        return s.n_drafts + 1 + merge + sel
+        return s.n_drafts + 1 + merge + sel + s.n_drafts + 1
 
     def run(self, iterations: Optional[int] = None):
         self.seed_selection()

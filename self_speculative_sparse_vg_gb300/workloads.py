@@ -267,6 +267,8 @@ class StackSpec:
     accept_p: float = 0.7
     per_head: bool = False
     seed: int = 6
+    prompt: int = 0               # prompt tokens per sequence that prefill may add
+    rope_theta: float = 0.0       # base of the rotary frequencies; 0: no rotary positions
 
     @property
     def batch(self) -> int:
@@ -278,9 +280,10 @@ class StackSpec:
 
     @property
     def room(self) -> int:
-        """Cache positions written past L_b over a run: the first token, then
-        at most k + 1 committed per iteration, plus one block of k + 1 beyond."""
-        return 1 + (self.iterations + 1) * (self.n_drafts + 1)
+        """Cache positions written past L_b over a run: the prompt, the first
+        token, then at most k + 1 committed per iteration, plus one block of
+        k + 1 beyond."""
+        return self.prompt + 1 + (self.iterations + 1) * (self.n_drafts + 1)
 
     @property
     def max_prefix(self) -> int:
