@@ -40,6 +40,7 @@
 //    spoil the row, so they zero V past the length and take non-finite values
 //    out of the tile, noting per dimension the first position of each kind;
 //    rows that attend it get it back at the end.
+#include <limits.h>
 #include <math.h>
 
 #include "vg_device.cuh"
@@ -250,13 +251,13 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
   return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
-// A V entry with its non-finite value given back: rel = the row's token within
-// the unit, notes = first token distance of a NaN, +inf, -inf in dimension c.
+// The non-finite value that dimension c of a row attends, or 0: rel = the row's
+// token within the unit, notes = first token distance of a NaN, +inf and -inf.
 template <int HD>
-__device__ __forceinline__ float noted(float v, const uint16_t* notes, int c, int rel) {
+__device__ __forceinline__ float noted(const uint16_t* notes, int c, int rel) {
   const bool n = rel >= notes[c], pi = rel >= notes[HD + c], ni = rel >= notes[2 * HD + c];
   if (n || (pi && ni)) return NAN;
-  return pi ? INFINITY : ni ? -INFINITY : v;
+  return pi ? INFINITY : ni ? -INFINITY : 0.f;
 }
 
 // ---------------------------------------------------------------- softmax
@@ -298,8 +299,13 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
         const int rem = lim - kt * kTile;  // last attended column
         if (!__all_sync(0xffffffffu, rem >= kTile - 1 || !valid)) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (j > rem) s[j >> 6][j & 63] = 0xff800000u;  // -inf
+          for (int w = 0; w < kTile / 32; ++w) {
+            const int last = rem - 32 * w;  // last attended column of these 32
+            const uint32_t keep = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((keep >> j) & 1u)) s[w >> 1][(w & 1) * 32 + j] = 0xff800000u;  // -inf
+          }
         }
         float mx[4];
 #pragma unroll
@@ -415,12 +421,6 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
           for (int j = 0; j < 64; ++j)
             o[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f_other, __uint_as_float(o[j])));
         }
-        if (note_flags[slot * 2] | note_flags[slot * 2 + 1]) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (note_flags[slot * 2 + (c + j >= HD / 2)])
-              o[j] = __float_as_uint(noted<HD>(__uint_as_float(o[j]), notes, c + j, tok));
-        }
         if (valid && direct) {
           __nv_bfloat16* dst = p.out + t * p.out_stride + (int64_t)qh * HD + c;
 #pragma unroll
@@ -444,6 +444,19 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
             dst[(size_t)j * p.rows] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
         __syncwarp();
+      }
+      if (valid && (note_flags[slot * 2] | note_flags[slot * 2 + 1])) {
+        // rows that attend a non-finite value of a checked tile
+#pragma unroll 1
+        for (int c = 0; c < HD; ++c) {
+          if (!note_flags[slot * 2 + (c >= HD / 2)]) continue;
+          const float x = noted<HD>(notes, c, tok);
+          if (x == 0.f) continue;
+          if (direct)
+            p.out[t * p.out_stride + (int64_t)qh * HD + c] = __float2bfloat16(x);
+          else
+            p.part_o[(((size_t)un.part * (HD / 4) + c / 4) * p.rows + prow) * 4 + c % 4] = x;
+        }
       }
       if (valid && direct && p.lse)
         p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
@@ -728,9 +741,10 @@ __device__ __forceinline__ long long sequence_lengths(const ChunkParams& p, int 
     const int sr = __shfl_sync(0xffffffffu, nrt, src);
     long long s = 0;
     for (int rt = lane; rt < sr; rt += 32) s += unit_length(sn, sl, tu, rt);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == src) c = s;
+    // 64 bits in two reductions of 32
+    const long long lo = __reduce_add_sync(0xffffffffu, (uint32_t)s & 0x3ffffffu);
+    const long long hi = __reduce_add_sync(0xffffffffu, (uint32_t)(s >> 26));
+    if (lane == src) c = (hi << 26) + lo;
   }
   return c;
 }
@@ -878,6 +892,19 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
         cut.h = h;
       }
     }
+    // page ids of four tiles at a time, one per lane (read here, looked at
+    // where they are used)
+    const int npages = (len + kPageSize - 1) / kPageSize;
+    auto fetch = [&](int kt) -> int {
+      const int lp = kt * kPagesPerTile + lane;
+      return lp < npages && kt + (lane >> 3) < un.kt1 ? p.page_table[(size_t)b * p.width + lp] : INT_MIN;
+    };
+    auto page = [&](int id) -> int {
+      if (id >= 0 && id < p.num_pages) return id;
+      if (id != INT_MIN) flag_error(p.error_flag, VG_DEVERR_PAGE);
+      return p.num_pages;  // past the pool: zeros
+    };
+    int ids_next = more ? fetch(kt0) : 0, ids = 0;
     q_armed = false;
     if (lane == 0) {
       units[slot] = un;
@@ -887,25 +914,14 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     if (!more) break;
     // K and V of a sequence with several row tiles are read again by other CTAs
     const uint64_t policy = n > tu ? again : once;
-    // page ids of four tiles at a time, one per lane
-    const int npages = (len + kPageSize - 1) / kPageSize;
-    auto fetch = [&](int kt) -> int {
-      const int lp = kt * kPagesPerTile + lane;
-      if (lp >= npages || kt + (lane >> 3) >= un.kt1) return p.num_pages;  // zeros
-      const int id = p.page_table[(size_t)b * p.width + lp];
-      if (id >= 0 && id < p.num_pages) return id;
-      flag_error(p.error_flag, VG_DEVERR_PAGE);
-      return p.num_pages;
-    };
-    int ids = fetch(un.kt0), ids_next = fetch(un.kt0 + 4);
     for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
       const int w = (kt - un.kt0) & 3;
-      if (w == 0 && kt > un.kt0) {
-        ids = ids_next;
+      if (w == 0) {
+        ids = page(ids_next);
         ids_next = fetch(kt + 4);
       }
       const int id = __shfl_sync(0xffffffffu, ids, w * 8 + pi);
-#pragma unroll
+#pragma unroll 1
       for (int v = 0; v < 2; ++v) {
         if (v == 1 && kt == un.kt0) {  // Q, once the unit before has made its scores
           if (u >= 1 && !wait(bars.qempty, (u - 1) & 1)) {
