@@ -72,7 +72,8 @@ struct ChunkParams {
   struct MergeUnit* merge;  // [grid]
   int32_t* error_flag;
   int64_t out_stride;
-  uint64_t wait_ns;
+  uint64_t wait_ns;    // a longer wait is reported
+  int polls;           // polls of a wait between two looks at the timer
   float scale_log2;
   int batch, num_tokens, num_q_heads, num_kv_heads, group, num_pages, width, rows;
 };
@@ -191,11 +192,27 @@ __device__ __forceinline__ bool checked_tile(int pos0, int kt) {
   return kt * kTile + kTile - 1 > pos0;
 }
 
+// Waits for the phase with the given parity, as mbar_wait_checked does, in less
+// code.  Past the report bound the wait flags VG_DEVERR_TIMEOUT, past
+// kWaitLimitNs it gives up.  (The timer is slow to read: with a look at it after
+// every poll the whole kernel was 5 % slower.)
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
-  return mbar_wait_checked(bar, parity, p.wait_ns, p.error_flag);
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < p.polls; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > p.wait_ns) flag_error(p.error_flag, VG_DEVERR_TIMEOUT);
+    if (now - t0 > kWaitLimitNs) return false;
+  }
 }
-// The same for a whole warp, which stays together.
+// The same for a whole warp, which stays together: mostly one look and one vote
+// (a loop that the lanes leave one by one costs some 50 cycles more, and the
+// tensor-core warp waits eight times for a tile).
 __device__ __forceinline__ bool chunk_wait_warp(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, chunk_wait(bar, parity, p));
 }
 
@@ -526,7 +543,6 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   uint32_t sk = 0, pk = 0, sv = 1, pv = 0;
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return chunk_wait_warp(bar, parity, p);
   };
   auto next = [](uint32_t& st, uint32_t& par) {
@@ -1325,6 +1341,7 @@ extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, in
   p.error_flag = error_flag;
   p.out_stride = out_stride;
   p.wait_ns = wait_report_ns();
+  p.polls = p.wait_ns < kWaitLimitNs ? 1 : 64;
   p.scale_log2 = softmax_scale * kLog2e;
   p.batch = batch;
   p.num_tokens = num_tokens;
