@@ -587,23 +587,21 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
         const bool more = j + 1 < n;
         // the tiles are waited for first, while the warpgroups are at P(j)
         if (!wait(&bars.full[sv], pv) || (more && !wait(&bars.full[sk], pk))) return false;
-        if (j < e0) {
-          if (!pv_product(0, sv, j > 0)) return false;
-          if (j + 1 < e0)
-            mma.qk(0, 0, sk);
+#pragma unroll 1
+        for (int wg = 0; wg < 2; ++wg) {
+          const int e = wg ? n : e0;
+          if (j >= e) continue;
+          if (!pv_product(wg, sv, j > 0)) return false;
+          if (j + 1 < e)
+            mma.qk(wg, wg, sk);
           else
-            umma_commit_elect(&bars.ofull[0]);
+            umma_commit_elect(&bars.ofull[wg]);
         }
-        if (!pv_product(1, sv, j > 0)) return false;
+        umma_commit_elect(&bars.empty[sv]);
         if (more) {
-          mma.qk(1, 1, sk);
-          umma_commit_elect(&bars.empty[sv]);
           umma_commit_elect(&bars.empty[sk]);
           if (j + 2 == n) umma_commit_elect(bars.qempty);
           next(sk, pk);
-        } else {
-          umma_commit_elect(&bars.ofull[1]);
-          umma_commit_elect(&bars.empty[sv]);
         }
         next(sv, pv);
       }
