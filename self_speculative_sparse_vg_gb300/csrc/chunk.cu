@@ -111,7 +111,7 @@ struct ChunkLayout {
   static constexpr int kSmall = kRing + kStages * kStageBytes;
   // small area: barriers, units, (m, l) exchange, non-finite notes
   static constexpr int kBars = kSmall;
-  static constexpr int kBarCount = 3 * kStages + 17;
+  static constexpr int kBarCount = 3 * kStages + 15;
   static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
   static constexpr int kFlags = kUnits + 2 * 48;
   static constexpr int kNotes = kFlags + 32;
@@ -133,8 +133,7 @@ struct ChunkBars {
   // products are done.  Whoever waits on `full` or `landed`
   // waits for every phase of it, so that a parity names one phase.
   uint64_t *full, *landed, *empty;         // [stages]
-  uint64_t *sfull, *ofull;                 // [2]: S, all of O of a warpgroup
-  uint64_t *pfull;                         // [4]: halves of P of a warpgroup
+  uint64_t *sfull, *pfull, *ofull;         // [2]: S, P, all of O of a warpgroup
   uint64_t *qfull, *qempty, *ufull, *uempty, *xfull, *xdone, *drain;
 };
 
@@ -146,14 +145,14 @@ __device__ __forceinline__ ChunkBars chunk_bars(uint64_t* b, int stages) {
   b += 3 * stages;
   r.sfull = b;
   r.pfull = b + 2;
-  r.ofull = b + 6;
-  r.ufull = b + 8;
-  r.uempty = b + 10;
-  r.qfull = b + 12;
-  r.qempty = b + 13;
-  r.xfull = b + 14;
-  r.xdone = b + 15;
-  r.drain = b + 16;
+  r.ofull = b + 4;
+  r.ufull = b + 6;
+  r.uempty = b + 8;
+  r.qfull = b + 10;
+  r.qempty = b + 11;
+  r.xfull = b + 12;
+  r.xdone = b + 13;
+  r.drain = b + 14;
   return r;
 }
 
@@ -350,8 +349,8 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
           }
           m_used = mn;
         }
-        // P = 2^(s scale - m), handed over in two halves so that the product
-        // with V starts while the second half is computed
+        // P = 2^(s scale - m).  (Handing it over in two halves, so that the
+        // product with V starts earlier, changed nothing.)
         const float nref = -safe_ref(m_used);
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nref2 = pair(nref, nref);
 #pragma unroll
@@ -367,11 +366,11 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
             s[h][2 * j + 1] = __float_as_uint(x.y);
           }
           tmem_st32u(scol + h * 32, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.pfull[2 * wg + h]);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.pfull[wg]);
         // the row sum, off the tensor cores' path
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -383,7 +382,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
         lsum += sum.x + sum.y;
       } else {
         __syncwarp();
-        if (lane < 2) mbar_arrive(&bars.pfull[2 * wg + lane]);
+        if (lane == 0) mbar_arrive(&bars.pfull[wg]);
       }
     }
     // -------- epilogue
@@ -520,11 +519,11 @@ struct MmaIssuer {
     }
     umma_commit_elect(&bars.sfull[wg]);
   }
-  // O of warpgroup `wg` (+)= P V of the stage, over half `half` of its positions
-  __device__ __forceinline__ void pv(int wg, uint32_t stage, int half, bool accumulate) {
+  // O of warpgroup `wg` (+)= P V of the stage
+  __device__ __forceinline__ void pv(int wg, uint32_t stage, bool accumulate) {
     const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4);
 #pragma unroll
-    for (int ks = half * (kTile / 32); ks < (half + 1) * (kTile / 32); ++ks)
+    for (int ks = 0; ks < kTile / 16; ++ks)
       umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
                          v + ks * (Lay::kPageBytes >> 4), kHiKv, kIdPv, accumulate || ks > 0);
   }
@@ -538,13 +537,11 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   constexpr uint32_t NST = Lay::kStages;
   MmaIssuer<HD> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
                     umma_desc_lo(ring, 1024)};
-  uint32_t pc0 = 0, pc1 = 0;  // tiles of the warpgroups so far
+  uint32_t pc = 0;            // parities of the warpgroups' next P
   // next K's and V's ring stage and parity; entries are K(0), V(0), K(1) ...
   uint32_t sk = 0, pk = 0, sv = 1, pv = 0;
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return chunk_wait_warp(bar, parity, p);
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return chunk_wait_warp(bar, parity, p); };
   auto next = [](uint32_t& st, uint32_t& par) {
     st += 2;
     if (st >= NST) {
@@ -552,16 +549,13 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
       par ^= 1;
     }
   };
-  // O(wg) (+)= P V: the first half of the positions while the warpgroup is
-  // still at the second
+  // O(wg) (+)= P V
   auto pv_product = [&](int wg, uint32_t st, bool accumulate) {
-    const uint32_t par = (wg ? pc1++ : pc0++) & 1;
-    if (!wait(&bars.pfull[2 * wg], par)) return false;
+    const uint32_t par = (pc >> wg) & 1;
+    pc ^= 1u << wg;
+    if (!chunk_wait_warp(&bars.pfull[wg], par, p)) return false;
     tc_fence_after();
-    mma.pv(wg, st, 0, accumulate);
-    if (!wait(&bars.pfull[2 * wg + 1], par)) return false;
-    tc_fence_after();
-    mma.pv(wg, st, 1, true);
+    mma.pv(wg, st, accumulate);
     return true;
   };
   for (uint32_t u = 0;; ++u) {
@@ -587,6 +581,8 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
         const bool more = j + 1 < n;
         // the tiles are waited for first, while the warpgroups are at P(j)
         if (!wait(&bars.full[sv], pv) || (more && !wait(&bars.full[sk], pk))) return false;
+        // (one copy of this code for both warpgroups: with two the kernel was
+        // 6 % slower, its roles share the instruction cache)
 #pragma unroll 1
         for (int wg = 0; wg < 2; ++wg) {
           const int e = wg ? n : e0;
@@ -1029,8 +1025,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.sfull[i], 1);
-      mbar_init(&bars.pfull[2 * i], 4);
-      mbar_init(&bars.pfull[2 * i + 1], 4);
+      mbar_init(&bars.pfull[i], 4);
       mbar_init(&bars.ofull[i], 1);
       mbar_init(&bars.ufull[i], 1);
       mbar_init(&bars.uempty[i], 8 + 1 + 2);
