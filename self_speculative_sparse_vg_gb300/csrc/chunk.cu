@@ -194,13 +194,14 @@ __device__ __forceinline__ bool checked_tile(int pos0, int kt) {
 // Waits for the phase with the given parity, as mbar_wait_checked does, in less
 // code.  Past the report bound the wait flags VG_DEVERR_TIMEOUT, past
 // kWaitLimitNs it gives up.  (The timer is slow to read: with a look at it after
-// every poll the whole kernel was 5 % slower.)
+// every poll the whole kernel was 5 % slower; polls is 1 under a report bound
+// shorter than the limit, and the polls then do not sleep.)
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
   uint64_t t0 = 0;
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < p.polls; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+      if (p.polls > 1 ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
     const uint64_t now = global_timer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > p.wait_ns) flag_error(p.error_flag, VG_DEVERR_TIMEOUT);
@@ -209,9 +210,9 @@ __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const
 }
 // The same for a whole warp, which stays together: mostly one look and one vote
 // (a loop that the lanes leave one by one costs some 50 cycles more, and the
-// tensor-core warp waits eight times for a tile).
+// tensor-core warp waits six times for a tile).
 __device__ __forceinline__ bool chunk_wait_warp(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, chunk_wait(bar, parity, p));
 }
 

@@ -273,3 +273,111 @@ def test_long_shares(Hq, Hkv, d):
     lens = [29999, 30001, 23456, 30000, 27777, 31000, 12345, 30123]
     new = [1, 1, 70, 1, 33, 1, 6, 300 // Hq]
     check_chunk(Cache(lens, Hkv, d, seed=17), new, Hq)
+
+
+def test_short_wait_bound_reports_and_completes():
+    """A wait bound that every wait outlasts is reported; the call completes
+    with the same results, and the next call reports nothing."""
+    from self_speculative_sparse_vg_gb300 import vg
+    c = Cache([9000, 400], 2, 128, seed=18)
+    kv = c.gpu()
+    qd, want, lse = check_chunk(c, [1, 150], 8, kv=kv)
+    args = (kv, qd, i32([0, 1, 151]), i32([9000, 400]), 128 ** -0.5)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    l2 = torch.cuda.get_device_properties(0).L2_cache_size
+    cold = torch.ones(int(1.5 * l2) // 4, device="cuda")
+    vg.set_wait_limit_ns(1)
+    try:
+        out = torch.zeros_like(want)
+        cold.sum()
+        vg.chunk_attention(*args, out, error_flag=flag)
+        assert int(flag.item()) == vg.DEVERR_TIMEOUT
+        assert torch.equal(out, want)
+    finally:
+        vg.set_wait_limit_ns(0)
+    flag.zero_()
+    out = torch.zeros_like(want)
+    vg.chunk_attention(*args, out, error_flag=flag)
+    assert int(flag.item()) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_queries_and_keys_that_are_not_finite_stay_in_their_rows(bad):
+    """A bad value in one query row spoils that row alone; one in a key spoils
+    the rows that attend it (a key's +-infinity times the query's sign may also
+    just take the position out) and no earlier ones."""
+    from self_speculative_sparse_vg_gb300 import vg
+    c = Cache([180], 1, 64, seed=19)
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(120, 4, 64, generator=g).bfloat16()
+    _, want, _ = check_chunk(c, [120], 4, q=q)
+    q2 = q.clone()
+    q2[33, 2, 5] = bad
+    out = torch.zeros_like(want)
+    vg.chunk_attention(c.gpu(), q2.cuda(), i32([0, 120]), i32([180]), 0.125, out)
+    keep = torch.ones(120, 4, dtype=torch.bool, device="cuda")
+    keep[33, 2] = False
+    assert torch.equal(out[keep], want[keep]) and out[33, 2].isnan().all()
+    k = c.k[0].clone()
+    k[100, 0, 9] = bad                      # position 100: token 40
+    c.write(0, k, c.v[0])
+    out = torch.zeros_like(want)
+    vg.chunk_attention(c.gpu(), q.cuda(), i32([0, 120]), i32([180]), 0.125, out)
+    assert torch.equal(out[:40], want[:40])
+    s = q.double()[40:, :, 9] * bad         # the logit's sign at position 100
+    spoiled = ~(s == -float("inf"))
+    assert torch.equal(out[40:].isnan().all(-1).cpu(), spoiled)
+    assert torch.equal(out[40:].isnan().any(-1).cpu(), spoiled)
+
+
+def test_outputs_on_16_bytes():
+    """An output that starts on 16 bytes but not on 32, and odd row strides."""
+    from self_speculative_sparse_vg_gb300 import vg
+    c = Cache([140, 3], 2, 64, seed=20)
+    qd, want, _ = check_chunk(c, [70, 3], 8)
+    flat = torch.full((73 * 520 + 8,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:].view(73, 520)[:, :512].unflatten(1, (8, 64))
+    assert out.data_ptr() % 32 == 16
+    vg.chunk_attention(c.gpu(), qd, i32([0, 70, 73]), i32([140, 3]), 0.125, out)
+    assert torch.equal(out, want)
+    assert (flat[:8] == 9).all() and (flat[8:].view(73, 520)[:, 512:] == 9).all()
+
+
+def test_largest_batch():
+    """4096 sequences, one token each, a few positions; and one token more of
+    them is refused."""
+    from self_speculative_sparse_vg_gb300 import vg
+    rng = np.random.default_rng(1)
+    lens = rng.integers(1, 20, 4096)
+    check_chunk(Cache(lens.tolist(), 1, 64, seed=21), [1] * 4096, 2)
+    kv = Cache([1], 1, 64).gpu()
+    big = vg.PagedKV(kv.k_pages, kv.v_pages, kv.page_table.expand(4097, -1).contiguous())
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(vg.VGError) as e:
+        vg.chunk_attention(big, q, i32([0] * 4097 + [1]), i32([0] * 4096 + [1]), 0.125, torch.zeros_like(q),
+                           workspace=torch.zeros(1 << 26, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 2
+
+
+def test_two_graphs_with_their_own_workspaces():
+    """Two captured calls of different shapes replayed in turn and again."""
+    from self_speculative_sparse_vg_gb300 import vg
+    runs = []
+    for lens, new, seed in (([3000, 50], [3, 50], 22), ([777], [200], 23)):
+        c = Cache(lens, 2, 128, seed=seed)
+        qd, want, _ = check_chunk(c, new, 8)
+        kv, cu, ln = c.gpu(), i32(np.concatenate([[0], np.cumsum(new)])), i32(lens)
+        ws = torch.empty(vg.chunk_workspace_bytes(len(new), sum(new), 8, 2, 128), dtype=torch.uint8,
+                         device="cuda")
+        out = torch.zeros_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            vg.chunk_attention(kv, qd, cu, ln, 128 ** -0.5, out, workspace=ws)
+        runs.append((g, out, want, kv, cu, ln, ws, qd))
+    for _ in range(3):
+        for g, out, want, *_ in runs:
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for g, out, want, *_ in runs:
+            assert torch.equal(out, want)

@@ -21,7 +21,7 @@ def _pool(rng, B, cached, extra_owned, spare, width=None, new=None):
     return table, owned, free, spare, used + spare
 
 
-@pytest.mark.parametrize("B", [1, 2, 31, 33, 300, 1023, 1024, 1025, 2500])
+@pytest.mark.parametrize("B", [1, 2, 31, 33, 300, 1023, 1024, 1025, 2500, 8192])
 def test_mixed_steps(B):
     rng = np.random.default_rng(B)
     cached = rng.integers(0, 200, B)
