@@ -386,7 +386,7 @@ vg_status vg_verify_attention_noalloc(const vg_paged_kv* kv, const void* q,
  * count is out of range or the returned pages do not fit free_capacity.  Page
  * ids outside [0, num_pages) are flagged VG_DEVERR_PAGE: a request that would
  * return one is refused, a token on one has slot -1.
- * Outputs must not overlap inputs.  One kernel, or two past 4096 tokens.
+ * Outputs must not overlap inputs.  One kernel.
  * Supported: batch <= 8192.
  * ------------------------------------------------------------------------- */
 vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, int batch,

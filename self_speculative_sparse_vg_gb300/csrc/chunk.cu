@@ -859,7 +859,6 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   using Lay = ChunkLayout<HD>;
   constexpr int NST = Lay::kStages;
   const int g = p.group, tt = kTile / g, tu = 2 * tt;
-  const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
   uint8_t* ring = smem + Lay::kRing;
   const int pi = lane & 7;
   int b = s.b, h = s.h, rt = s.rt, kt0 = s.kt0;
@@ -923,8 +922,6 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     }
     __syncwarp();
     if (!more) break;
-    // K and V of a sequence with several row tiles are read again by other CTAs
-    const uint64_t policy = n > tu ? again : once;
     for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
       const int w = (kt - un.kt0) & 3;
       if (w == 0) {
@@ -962,7 +959,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
         __syncwarp();
         if (lane < kPagesPerTile)
           tma_load_4d(ring + st * Lay::kStageBytes + pi * Lay::kPageBytes, v ? &tmv : &tmk, bar, 0, 0,
-                      0, (id * p.num_kv_heads + h) * 2, policy);
+                      0, (id * p.num_kv_heads + h) * 2);
         __syncwarp();
         on_landed &= ~(1u << st);
         if (bar == &bars.landed[st]) {
@@ -1270,8 +1267,9 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   const long long rows = (long long)p.num_tokens * p.group;  // no unit has more
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  // Up to 32 rows: a CTA per row (one token of 8 heads over 2K: MERGE_SMALL);
-  // more rows mean fewer parts, and a CTA takes 32 rows.
+  // Up to 32 rows: a CTA per row, whose units have many parts (one token of 8
+  // heads over 2K: 10.0 us for the call, 12.7 with the other merge; eight tokens
+  // over 16K - 64K: the same).  More rows mean fewer parts, and a CTA takes 32.
   if (rows <= 32) {
     cfg.gridDim = dim3(pl.grid, (int)rows);
     return cudaLaunchKernelEx(&cfg, chunk_merge_row_kernel<HD>, p);

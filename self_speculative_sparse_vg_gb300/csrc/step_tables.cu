@@ -10,10 +10,12 @@
 // by latency: dependent memory round trips and launches, not bytes.  One CTA
 // resizes the tables (the free list is one stack, and three prefix sums over
 // the requests fix every request's place in it): a thread owns IPT
-// neighbouring requests, so one pass of warp shuffles makes each sum.  The
-// same CTA then writes the tokens' positions and slots when there are at most
-// kOneCtaTokens of them (their lookups cost less than a second launch);
-// beyond that a second kernel spreads the tokens over the GPU.
+// neighbouring requests, so one pass of warp shuffles makes each sum.  Then the
+// tokens' positions and slots are written, a token per thread; past 1024 tokens
+// the CTA is the first of a cluster whose others wait for it and share that
+// part.  64 tokens of 8 requests 4.2 us, 4096 tokens 5.4, 114K 9; a second
+// kernel for the tokens instead of the cluster took 4.7 - 5.6 us and 2 us more
+// of host time for its launch, one CTA alone 3.8 us for 64 and 6.5 for 4096.
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -23,9 +25,9 @@ namespace vg {
 namespace {
 
 constexpr int kTableThreads = 1024;
-constexpr int kFillThreads = 256;
+constexpr int kMaxTableCluster = 16;
 constexpr int kMaxTableBatch = 8192;   // requests: 8 per thread
-constexpr int kOneCtaTokens = 4096;
+constexpr int kFillBatch = 4;          // tokens of a thread whose loads are in flight together
 
 struct TableParams {
   const int32_t* cached;
@@ -69,36 +71,50 @@ __device__ __forceinline__ T cta_inclusive_sum(T v, T* part) {
   return v;
 }
 
-// Position and slot of token row t; ends[b] = clamped end row of request b.
-__device__ __forceinline__ void fill_token(const TableParams& p, const int32_t* ends, int t) {
-  int lo = 0, hi = p.batch;  // first request whose rows end past t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ends[mid] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+// Positions and slots of token rows first, first + stride, ...; ends[b] =
+// clamped end row of request b.
+__device__ __forceinline__ void fill_tokens(const TableParams& p, const int32_t* ends, int first,
+                                            int stride) {
+  for (int64_t t0 = first; t0 < p.max_tokens; t0 += (int64_t)kFillBatch * stride) {
+    int req[kFillBatch], pos[kFillBatch], page[kFillBatch];
+#pragma unroll
+    for (int k = 0; k < kFillBatch; ++k) {
+      const int64_t t = t0 + (int64_t)k * stride;
+      int lo = 0, hi = t < p.max_tokens ? p.batch : 0;  // first request whose rows end past t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ends[mid] > t)
+          hi = mid;
+        else
+          lo = mid + 1;
+      }
+      req[k] = t < p.max_tokens && lo < p.batch && __ldcg(p.kv_lens + lo) > 0 ? lo : -1;
+      pos[k] = req[k] >= 0 ? __ldcg(p.cached + lo) + (int)(t - (lo > 0 ? ends[lo - 1] : 0)) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kFillBatch; ++k)
+      page[k] = req[k] >= 0 ? __ldcg(p.page_table + (size_t)req[k] * p.width + pos[k] / kPageSize) : 0;
+#pragma unroll
+    for (int k = 0; k < kFillBatch; ++k) {
+      const int64_t t = t0 + (int64_t)k * stride;
+      if (t >= p.max_tokens) break;
+      int slot = -1;
+      if (req[k] >= 0) {
+        if (page[k] >= 0 && page[k] < p.num_pages)
+          slot = page[k] * kPageSize + pos[k] % kPageSize;
+        else
+          flag_error(p.error_flag, VG_DEVERR_PAGE);
+      }
+      p.positions[t] = pos[k];
+      p.slots[t] = slot;
+    }
   }
-  int pos = 0, slot = -1;
-  if (lo < p.batch && __ldcg(p.kv_lens + lo) > 0) {
-    pos = __ldcg(p.cached + lo) + t - (lo > 0 ? ends[lo - 1] : 0);
-    const int page = __ldcg(p.page_table + (size_t)lo * p.width + pos / kPageSize);
-    if (page >= 0 && page < p.num_pages)
-      slot = page * kPageSize + pos % kPageSize;
-    else
-      flag_error(p.error_flag, VG_DEVERR_PAGE);
-  }
-  p.positions[t] = pos;
-  p.slots[t] = slot;
 }
 
+// The tables, by one CTA; also leaves the requests' end rows in ends_s.
 template <int IPT>
-__global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const TableParams p) {
-  extern __shared__ int32_t ends_s[];  // [batch]
-  __shared__ long long part64[32];
+__device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* ends_s, long long* part64) {
   const int tid = threadIdx.x, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   const int b0 = tid * IPT;
   // a fixed table has no free list: every request keeps the pages it has
   const bool fixed = p.owned == nullptr;
@@ -231,36 +247,53 @@ __global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const TableP
 #pragma unroll
   for (int i = 0; i < IPT; ++i)
     if (b0 + i < p.batch) p.kv_lens[b0 + i] = ok[i] ? cached[i] + fresh[i] : 0;
-  if (p.max_tokens > kOneCtaTokens) return;  // the fill kernel follows
-  __syncthreads();
-  for (int t = tid; t < p.max_tokens; t += kTableThreads) fill_token(p, ends_s, t);
 }
 
-// Positions and slots of many tokens (chained to the kernel above).
-__global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableParams p) {
+template <int IPT>
+__global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const TableParams p) {
   extern __shared__ int32_t ends_s[];  // [batch]
+  __shared__ long long part64[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  for (int b = threadIdx.x; b < p.batch; b += kFillThreads) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
+  if (blockIdx.x == 0) resize_tables<IPT>(p, ends_s, part64);
+  if (gridDim.x > 1) {  // the grid is one cluster
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (blockIdx.x > 0)
+      for (int b = threadIdx.x; b < p.batch; b += kTableThreads) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
+  }
   __syncthreads();
-  const int t = blockIdx.x * kFillThreads + threadIdx.x;
-  if (t < p.max_tokens) fill_token(p, ends_s, t);
+  fill_tokens(p, ends_s, blockIdx.x * kTableThreads + threadIdx.x, gridDim.x * kTableThreads);
 }
 
-template <typename K>
-cudaError_t launch_chained(K kernel, int grid, int block, size_t smem, cudaStream_t stream,
-                           const TableParams& p) {
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+template <int IPT>
+cudaError_t launch_tables(const TableParams& p, int ctas, cudaStream_t stream) {
+  if (ctas > 8) {
+    static bool attr_set[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel<IPT>,
+                                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) attr_set[dev] = true;
+    }
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kTableThreads);
+  cfg.dynamicSmemBytes = (size_t)p.batch * sizeof(int32_t);  // at most 32 KB
   cfg.stream = stream;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, step_tables_kernel<IPT>, p);
 }
 
 }  // namespace
@@ -303,12 +336,9 @@ extern "C" vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* n
   p.num_pages = num_pages;
   p.free_capacity = free_capacity;
   p.max_tokens = max_tokens;
-  const size_t smem = (size_t)batch * sizeof(int32_t);  // at most 32 KB
-  cudaError_t e = batch <= kTableThreads
-                      ? launch_chained(step_tables_kernel<1>, 1, kTableThreads, smem, stream, p)
-                      : launch_chained(step_tables_kernel<8>, 1, kTableThreads, smem, stream, p);
-  if (e == cudaSuccess && max_tokens > kOneCtaTokens)
-    e = launch_chained(step_fill_kernel, ceil_div(max_tokens, kFillThreads), kFillThreads, smem,
-                       stream, p);
+  int ctas = 1;
+  while (ctas < kMaxTableCluster && (int64_t)ctas * kTableThreads < max_tokens) ctas *= 2;
+  const cudaError_t e = batch <= kTableThreads ? launch_tables<1>(p, ctas, stream)
+                                               : launch_tables<8>(p, ctas, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }
