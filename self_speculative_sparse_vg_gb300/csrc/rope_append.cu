@@ -28,8 +28,9 @@ namespace vg {
 namespace {
 
 // Most threads of a CTA, tokens of a thread.  8192 tokens of 32 + 2 * 8 heads:
-// 35.5 us (5.7 TB/s) as set, 36.1 with 256 threads, 37.2 with 512, 37.8 with
-// four tokens of a thread.
+// 34.6 us (5.8 TB/s) as set, 35.4 with one token of a thread, 35.1 with 256
+// threads, 35.6 with 512.  (Streaming stores: 33.2, but the next call reads what
+// this one wrote.)
 constexpr int kRopeThreads = 128;
 constexpr int kUnroll = 2;
 constexpr int kAxesMax = 8;
@@ -69,8 +70,10 @@ __device__ __forceinline__ float2 turn_of(int pos, float f) {
     const double turns = (double)pos * (double)f * 0.15915494309189533577;
     frac = (float)(turns - rint(turns));
   }
+  // the hardware sine and cosine: within 2^-21 on half a turn either way, far
+  // below the one rounding to bf16 that follows
   float s, c;
-  sincospif(2.f * frac, &s, &c);
+  __sincosf(6.2831853071795865f * frac, &s, &c);
   return make_float2(c, s);
 }
 
@@ -78,7 +81,8 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t v) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
 }
 
-// cs[j * stride] holds cosine and sine of the item's frequencies 2j and 2j + 1.
+// cs[j * stride] holds the cosines of the item's frequencies 2j and 2j + 1, then
+// their sines.
 template <bool NEAR>
 __device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float4* cs, int stride) {
   uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, b[4] = {x1.x, x1.y, x1.z, x1.w};
@@ -89,16 +93,19 @@ __device__ __forceinline__ void turn_item(uint4& x0, uint4& x1, const float4* cs
       uint32_t& p0 = j < 2 ? a[2 * j] : b[2 * j - 4];
       uint32_t& p1 = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
       const float2 u = unpack_bf16(p0), v = unpack_bf16(p1);
-      p0 = pack_bf16(u.x * w.x - u.y * w.y, u.y * w.x + u.x * w.y);
-      p1 = pack_bf16(v.x * w.z - v.y * w.w, v.y * w.z + v.x * w.w);
+      p0 = pack_bf16(u.x * w.x - u.y * w.z, u.y * w.x + u.x * w.z);
+      p1 = pack_bf16(v.x * w.y - v.y * w.w, v.y * w.y + v.x * w.w);
     }
-  } else {     // pairs run across the two pieces
+  } else {     // pairs run across the two pieces: two of them in each operation
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float4 w = cs[j * stride];
       const float2 u = unpack_bf16(a[j]), v = unpack_bf16(b[j]);
-      a[j] = pack_bf16(u.x * w.x - v.x * w.y, u.y * w.z - v.y * w.w);
-      b[j] = pack_bf16(v.x * w.x + u.x * w.y, v.y * w.z + u.y * w.w);
+      const uint64_t u2 = pair(u.x, u.y), v2 = pair(v.x, v.y);
+      const uint64_t c2 = pair(w.x, w.y), s2 = pair(w.z, w.w), m2 = pair(-w.z, -w.w);
+      const float2 y = unpair(fma2(u2, c2, mul2(v2, m2))), z = unpair(fma2(v2, c2, mul2(u2, s2)));
+      a[j] = pack_bf16(y.x, y.y);
+      b[j] = pack_bf16(z.x, z.y);
     }
   }
   x0 = make_uint4(a[0], a[1], a[2], a[3]);
@@ -149,8 +156,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
       flag_error(p.error_flag, VG_DEVERR_INDEX);
       axis = 0;
     }
-    float2* at = reinterpret_cast<float2*>(cs_s + tl * (p.half / 2) + (f % 8 / 2) * turning + f / 8) + f % 2;
-    *at = turn_of(p.positions[axis * p.pos_stride + t0 + tl], p.inv_freq[f]);
+    float* at = reinterpret_cast<float*>(cs_s + tl * (p.half / 2) + (f % 8 / 2) * turning + f / 8) + f % 2;
+    const float2 cs = turn_of(p.positions[axis * p.pos_stride + t0 + tl], p.inv_freq[f]);
+    at[0] = cs.x;
+    at[2] = cs.y;
   }
   __syncthreads();
   if (!on) return;
