@@ -1,21 +1,28 @@
-"""Build libvg.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libvg.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+vg_binding.so, the native part of its Python binding.
 
 Each .cu file is compiled to an object in parallel, then linked into
-self_speculative_sparse_vg_gb300/libvg.so.  No torch, no cmake.
+self_speculative_sparse_vg_gb300/libvg.so, which knows nothing of torch or
+Python.  vg_binding.so reads tensors through torch's headers and links to
+libvg.so beside it.  No cmake.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvg.so")
+BINDING = os.path.join(PKG, "vg_binding.so")
+CXX = os.environ.get("CXX", "g++")
 SOURCES = ["vg_host.cu", "verify.cu", "select.cu", "sparse_draft.cu", "step_tables.cu",
            "rope_append.cu", "chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -43,9 +50,29 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    obj, inc = os.path.join(BUILD, "vg_binding.o"), os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run([CXX, "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-c",
+          os.path.join(CSRC, "vg_binding.cpp"), "-o", obj], "vg_binding.cpp")
+    return obj
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
@@ -53,6 +80,11 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    lib = os.path.join(_torch_dir(), "lib")
+    _run([CXX, "-shared", "-o", BINDING + ".tmp", binding.result(), "-L", PKG, "-l:libvg.so", "-L", lib,
+          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN:" + lib],
+         "link of vg_binding.so")
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

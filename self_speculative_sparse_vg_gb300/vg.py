@@ -99,6 +99,7 @@ def _load():
 
 
 _lib = _load()
+from . import vg_binding as _binding  # noqa: E402  (links to the library loaded above)
 
 
 def set_wait_limit_ns(limit_ns: int) -> None:
@@ -155,19 +156,6 @@ class PagedKV:
         P, H, S, D = self.k_pages.shape
         return PagedKVStruct(self.k_pages.data_ptr(), self.v_pages.data_ptr(),
                              self.page_table.data_ptr(), P, S, self.page_table.shape[1], H, D)
-
-    def handle(self):
-        """(struct() by reference, num_kv_heads, head_dim) for a call.  They are
-        made again when the tensors are not what they say."""
-        k, v, t = self.k_pages, self.v_pages, self.page_table
-        now = (k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, t.shape)
-        kept = self.__dict__.get("_kept")
-        if kept is None or kept[0] != now:
-            if not (k.is_cuda and v.is_cuda and t.is_cuda):
-                raise ValueError("the paged cache has to be on a GPU")
-            s = self.struct()
-            kept = self.__dict__["_kept"] = (now, (ctypes.byref(s), s.num_kv_heads, s.head_dim), s)
-        return kept[1]
 
 
 # --------------------------------------------------------------------- verify
@@ -328,50 +316,8 @@ def sparse_draft_attention(kv: PagedKV, q, indices, counts, per_head, tail_start
 
 
 # ------------------------------------------------------------ filling the cache
-# These calls are made once per layer or step, for a single token too, so their
-# checks are written out for little host time (a tensor attribute costs 50 ns).
-_I32, _BF16 = torch.int32, torch.bfloat16
-_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device, without a Stream object
-_current_device = torch._C._cuda_getDevice
-
-
-def _int32(t, n, name):
-    """Device pointer of a contiguous int32 tensor of n elements."""
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: a contiguous int32 GPU tensor of {n} elements is needed")
-    return t.data_ptr()
-
-
-def _heads(t, name):
-    """(pointer, tokens, heads, head_dim, elements between tokens) of bf16 rows
-    [T][H][d] whose heads are contiguous within a token."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name}: a bfloat16 GPU tensor [tokens][heads][head_dim] is needed")
-    n, h, d = t.shape
-    if n <= 1 or t.is_contiguous():
-        s0, s1, s2 = h * d, d, 1
-        if n == 1:
-            _, s1, s2 = t.stride()
-    else:
-        s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != d and h > 1):
-        raise ValueError(f"{name}: the heads of a token have to be contiguous")
-    return t.data_ptr(), n, h, d, s0
-
-
-def _call(fn, dev, args, stream):
-    """Call an entry point on the given stream (None: device dev's current
-    stream) with device dev current."""
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if dev == _current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != 0:
-        raise VGError(fn.__name__, status)
-
-
+# Checks and calls are native (vg_binding.so): ValueError for tensors of the wrong
+# type, shape or place, VGError for what the library refuses.
 def step_tables(page_table, num_pages, cached_lens, new_lens, cu_tokens, kv_lens, positions, slots,
                 owned=None, free_pages=None, free_count=None, error_flag=None, stream=None):
     """vg_step_tables: resize the block tables to cached_lens + new_lens tokens
@@ -380,25 +326,11 @@ def step_tables(page_table, num_pages, cached_lens, new_lens, cu_tokens, kv_lens
     page_table int32 [B][max_pages]; owned, free_pages, free_count (int32 [B],
     [capacity], [1]) are updated in place, or all None for a fixed table.
     Outputs: cu_tokens [B + 1], kv_lens [B], positions and slots [max_tokens]."""
-    if page_table.dim() != 2:
-        raise ValueError("page_table: [batch][max_pages] is needed")
-    B, width = page_table.shape
-    T = positions.numel()
-    own = pages = count = None
-    room = 0
-    if owned is not None or free_pages is not None or free_count is not None:
-        if owned is None or free_pages is None or free_count is None:
-            raise ValueError("owned, free_pages and free_count are given together")
-        room = free_pages.numel()
-        own, pages = _int32(owned, B, "owned"), _int32(free_pages, room, "free_pages")
-        count = _int32(free_count, 1, "free_count")
-    _call(_lib.vg_step_tables, page_table.get_device(),
-          (_int32(cached_lens, B, "cached_lens"), _int32(new_lens, B, "new_lens"), B,
-           _int32(page_table, B * width, "page_table"), width, num_pages, own, pages, room, count, T,
-           _int32(cu_tokens, B + 1, "cu_tokens"), _int32(kv_lens, B, "kv_lens"),
-           _int32(positions, T, "positions"), _int32(slots, T, "slots"),
-           None if error_flag is None else _int32(error_flag, error_flag.numel(), "error_flag")),
-          stream)
+    s = _binding.step_tables(page_table, num_pages, cached_lens, new_lens, cu_tokens, kv_lens,
+                             positions, slots, owned, free_pages, free_count, error_flag,
+                             None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_step_tables", s)
     return cu_tokens, kv_lens, positions, slots
 
 
@@ -410,46 +342,11 @@ def rope_append(kv: PagedKV, q, k, v, slots, q_out=None, positions=None, inv_fre
     q [T][Hq][d] (or None), k and v [T][Hkv][d] bf16, slices of a fused
     projection included; slots int32 [T]; positions int32 [T] or [axes][T];
     inv_freq float32 [rot / 2] (None: nothing turns); freq_axis int32 [rot / 2]."""
-    kp, T, H, d, ks = _heads(k, "k")
-    vp, Tv, Hv, dv, vs = _heads(v, "v")
-    kvp, Hc, dc = kv.handle()
-    if not (T == Tv and H == Hv == Hc and d == dv == dc):
-        raise ValueError("k and v do not match each other or the cache")
-    qp = op = None
-    Hq = qs = os_ = 0
-    if q is not None:
-        qp, Tq, Hq, dq, qs = _heads(q, "q")
-        if Tq != T or dq != d:
-            raise ValueError("q does not match k")
-        if q_out is None or q_out is q:
-            op, os_ = qp, qs
-        else:
-            op, To, Ho, do, os_ = _heads(q_out, "q_out")
-            if To != T or Ho != Hq or do != d:
-                raise ValueError("q_out does not match q")
-    pos = freq = axis = None
-    axes, ps, rot = 0, 0, 0
-    if inv_freq is not None:
-        if inv_freq.dtype is not torch.float32 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq: a contiguous float32 GPU tensor is needed")
-        if positions is None:
-            raise ValueError("positions are needed with inv_freq")
-        shape = positions.shape
-        if (positions.dtype is not _I32 or not positions.is_cuda or len(shape) > 2
-                or shape[-1] != T or not (positions.is_contiguous() or T < 2
-                                          or positions.stride(-1) == 1)):
-            raise ValueError("positions: int32 [tokens] or [axes][tokens] on the GPU is needed")
-        axes = 1 if len(shape) == 1 else shape[0]
-        ps = T if axes == 1 else positions.stride(0)
-        half = inv_freq.numel()
-        pos, freq, rot = positions.data_ptr(), inv_freq.data_ptr(), 2 * half
-        if freq_axis is not None:
-            axis = _int32(freq_axis, half, "freq_axis")
-    _call(_lib.vg_rope_append, k.get_device(),
-          (kvp, qp, qs, kp, ks, vp, vs, op, os_, T, Hq, pos, ps, axes, freq, axis, rot,
-           1 if interleaved else 0, _int32(slots, T, "slots"),
-           None if error_flag is None else _int32(error_flag, error_flag.numel(), "error_flag")),
-          stream)
+    s = _binding.rope_append(kv.k_pages, kv.v_pages, kv.page_table, q, k, v, slots, q_out, positions,
+                             inv_freq, freq_axis, interleaved, error_flag,
+                             None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_rope_append", s)
     return q if q_out is None else q_out
 
 
@@ -464,30 +361,15 @@ def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None,
     int32 [B] (new tokens included), lse (optional) float32 [T][Hq].
     workspace: uint8 tensor of chunk_workspace_bytes() (allocated here when not
     given)."""
-    qp, T, Hq, d, qs = _heads(q, "q")
-    op, To, Ho, do, os_ = _heads(out, "out")
-    kvp, Hkv, dc = kv.handle()
-    if T != To or Hq != Ho or d != do or d != dc:
-        raise ValueError("out or the cache does not match q")
-    B = kv_lens.numel()
-    if kv.page_table.shape[0] != B:
-        raise ValueError("the cache's page table has another batch size")
-    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_cuda
-                            or not lse.is_contiguous() or lse.numel() != T * Hq):
-        raise ValueError("lse: a contiguous float32 GPU tensor [T][Hq] is needed")
-    dev = q.get_device()
     if workspace is None:
-        with torch.cuda.device(dev):   # its size goes by the device
-            n = chunk_workspace_bytes(B, T, Hq, Hkv, d)
+        with torch.cuda.device(q.device):   # its size goes by the device
+            n = chunk_workspace_bytes(kv_lens.numel(), *q.shape[:2], kv.num_kv_heads, kv.head_dim)
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace: a contiguous GPU tensor is needed")
-    _call(_lib.vg_chunk_attention, dev,
-          (kvp, qp, qs, _int32(cu_q, B + 1, "cu_q"), _int32(kv_lens, B, "kv_lens"), B, T, Hq,
-           softmax_scale, op, os_, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-           workspace.nbytes,
-           None if error_flag is None else _int32(error_flag, error_flag.numel(), "error_flag")),
-          stream)
+    s = _binding.chunk_attention(kv.k_pages, kv.v_pages, kv.page_table, q, cu_q, kv_lens, softmax_scale,
+                                 out, lse, workspace, error_flag,
+                                 None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_chunk_attention", s)
     return out
 
 
