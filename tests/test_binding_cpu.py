@@ -16,12 +16,14 @@ def test_what_is_no_tensor_is_refused(bad):
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="page_table"):
         vg.step_tables(bad, 2, i, i, i, i, i, i)
+    kv = _cache()
+    kv.k_pages = bad
     with pytest.raises(ValueError, match="cache"):   # of the host: refused before k and v are looked at
         vg.rope_append(_cache(), None, bad, bad, i)
     with pytest.raises(ValueError, match="k_pages: a tensor"):
-        vg.rope_append(vg.PagedKV(bad, bad, i), None, i, i, i)
+        vg.rope_append(kv, None, i, i, i)
     with pytest.raises(ValueError, match="k_pages: a tensor"):
-        vg.chunk_attention(vg.PagedKV(bad, bad, i), i, i, i, 1.0, i, workspace=i)
+        vg.chunk_attention(kv, i, i, i, 1.0, i, workspace=i)
 
 
 def test_tensors_of_the_host_are_refused():
