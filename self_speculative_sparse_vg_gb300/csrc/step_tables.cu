@@ -13,9 +13,11 @@
 // neighbouring requests, so one pass of warp shuffles makes each sum.  Then the
 // tokens' positions and slots are written, a token per thread; past 1024 tokens
 // the CTA is the first of a cluster whose others wait for it and share that
-// part.  64 tokens of 8 requests 4.2 us, 4096 tokens 5.4, 114K 9; a second
-// kernel for the tokens instead of the cluster took 4.7 - 5.6 us and 2 us more
-// of host time for its launch, one CTA alone 3.8 us for 64 and 6.5 for 4096.
+// part.  4096 tokens of 8 requests take 5.4 us, 114K 9; a second kernel for the
+// tokens instead of the cluster took 4.7 - 5.6 us and 2 us more of host time for
+// its launch, one CTA alone 6.5 us for 4096.  A few requests and tokens get a CTA
+// of 128 threads, whose start and barriers are shorter: 3.2 us for 64 tokens of 8
+// requests against 4.4 with 1024 (and three barriers a sum).
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -25,6 +27,7 @@ namespace vg {
 namespace {
 
 constexpr int kTableThreads = 1024;
+constexpr int kFewThreads = 128;       // of a CTA for a few requests and tokens
 constexpr int kMaxTableCluster = 16;
 constexpr int kMaxTableBatch = 8192;   // requests: 8 per thread
 constexpr int kFillBatch = 4;          // tokens of a thread whose loads are in flight together
@@ -44,31 +47,33 @@ struct TableParams {
   int batch, width, num_pages, free_capacity, max_tokens;
 };
 
-// Inclusive sum of v over the CTA's threads in thread order.  `part` holds one
-// entry per warp and is free again when the call returns.
-template <typename T>
-__device__ __forceinline__ T cta_inclusive_sum(T v, T* part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// A prefix sum over the CTA's threads in thread order, in two halves with a
+// barrier between them, so that several sums share it: the inclusive sum within
+// the warp, whose total goes to part[warp], ...
+__device__ __forceinline__ long long warp_inclusive_sum(long long v, long long* part) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
-  if (lane == 31) part[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    T w = part[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    part[lane] = w;
-  }
-  __syncthreads();
-  if (warp > 0) v += part[warp - 1];
-  __syncthreads();
+  if (lane == 31) part[threadIdx.x >> 5] = v;
   return v;
+}
+
+// ... and what the warps before this one add; `all` is the CTA's total.
+template <int NT>
+__device__ __forceinline__ long long sum_of_warps_before(const long long* part, long long* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long sum = lane < NT / 32 ? part[lane] : 0, before = lane < warp ? sum : 0;
+#pragma unroll
+  for (int o = 1; o < NT / 32; o <<= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  // lanes of one group of NT / 32 hold the entries
+  *all = __shfl_sync(0xffffffffu, sum, 0);
+  return __shfl_sync(0xffffffffu, before, 0);
 }
 
 // Positions and slots of token rows first, first + stride, ...; ends[b] =
@@ -112,8 +117,9 @@ __device__ __forceinline__ void fill_tokens(const TableParams& p, const int32_t*
 }
 
 // The tables, by one CTA; also leaves the requests' end rows in ends_s.
-template <int IPT>
-__device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* ends_s, long long* part64) {
+template <int NT, int IPT>
+__device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* ends_s,
+                                              long long (*part)[NT / 32]) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int b0 = tid * IPT;
   // a fixed table has no free list: every request keeps the pages it has
@@ -132,7 +138,9 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     rows += max(fresh[i], 0);
   }
   // -------- rows of the packed token buffer
-  long long end = cta_inclusive_sum(rows, part64) - rows;
+  long long end = warp_inclusive_sum(rows, part[0]) - rows, all;
+  __syncthreads();
+  end += sum_of_warps_before<NT>(part[0], &all);
   int back = 0;
 #pragma unroll
   for (int i = 0; i < IPT; ++i) {
@@ -177,12 +185,11 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     int grow = 0;  // a thread's own pages: at most 8 requests of < 2^27 pages
 #pragma unroll
     for (int i = 0; i < IPT; ++i) grow += ok[i] ? max(need[i] - own[i], 0) : 0;
-    const long long back_sum = cta_inclusive_sum((long long)back, part64);
-    long long want = cta_inclusive_sum((long long)grow, part64) - grow;  // asked for before this thread
-    __shared__ long long total_s;
-    if (tid == kTableThreads - 1) total_s = back_sum;
+    long long back_sum = warp_inclusive_sum(back, part[1]), back_all;
+    long long want = warp_inclusive_sum(grow, part[2]) - grow;  // asked for before this thread
     __syncthreads();
-    const long long back_all = total_s;
+    back_sum += sum_of_warps_before<NT>(part[1], &back_all);
+    want += sum_of_warps_before<NT>(part[2], &all);
     // a free list that is not one (its count is outside it, or the pages
     // coming back do not fit) changes nobody's pages
     const bool list_ok = top0 >= 0 && top0 + back_all <= p.free_capacity;
@@ -241,39 +248,41 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
         taken += more;
       }
     }
-    const long long all = cta_inclusive_sum((long long)taken, part64);
-    if (tid == kTableThreads - 1 && list_ok) *p.free_count = top - (int)all;
+    warp_inclusive_sum(taken, part[3]);
+    __syncthreads();
+    sum_of_warps_before<NT>(part[3], &all);
+    if (tid == 0 && list_ok) *p.free_count = top - (int)all;
   }
 #pragma unroll
   for (int i = 0; i < IPT; ++i)
     if (b0 + i < p.batch) p.kv_lens[b0 + i] = ok[i] ? cached[i] + fresh[i] : 0;
 }
 
-template <int IPT>
-__global__ void __launch_bounds__(kTableThreads) step_tables_kernel(const TableParams p) {
+template <int NT, int IPT>
+__global__ void __launch_bounds__(NT) step_tables_kernel(const TableParams p) {
   extern __shared__ int32_t ends_s[];  // [batch]
-  __shared__ long long part64[32];
+  __shared__ long long part[4][NT / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x == 0) resize_tables<IPT>(p, ends_s, part64);
+  if (blockIdx.x == 0) resize_tables<NT, IPT>(p, ends_s, part);
   if (gridDim.x > 1) {  // the grid is one cluster
     cluster_arrive_release();
     cluster_wait_acquire();
     if (blockIdx.x > 0)
-      for (int b = threadIdx.x; b < p.batch; b += kTableThreads) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
+      for (int b = threadIdx.x; b < p.batch; b += NT) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
   }
   __syncthreads();
-  fill_tokens(p, ends_s, blockIdx.x * kTableThreads + threadIdx.x, gridDim.x * kTableThreads);
+  fill_tokens(p, ends_s, blockIdx.x * NT + threadIdx.x, gridDim.x * NT);
 }
 
-template <int IPT>
+template <int NT, int IPT>
 cudaError_t launch_tables(const TableParams& p, int ctas, cudaStream_t stream) {
   if (ctas > 8) {
     static bool attr_set[64] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel<IPT>,
+      const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel<NT, IPT>,
                                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       if (dev < 64) attr_set[dev] = true;
@@ -288,12 +297,12 @@ cudaError_t launch_tables(const TableParams& p, int ctas, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTableThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = (size_t)p.batch * sizeof(int32_t);  // at most 32 KB
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, step_tables_kernel<IPT>, p);
+  return cudaLaunchKernelEx(&cfg, step_tables_kernel<NT, IPT>, p);
 }
 
 }  // namespace
@@ -338,7 +347,10 @@ extern "C" vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* n
   p.max_tokens = max_tokens;
   int ctas = 1;
   while (ctas < kMaxTableCluster && (int64_t)ctas * kTableThreads < max_tokens) ctas *= 2;
-  const cudaError_t e = batch <= kTableThreads ? launch_tables<1>(p, ctas, stream)
-                                               : launch_tables<8>(p, ctas, stream);
+  const cudaError_t e =
+      batch <= kFewThreads && max_tokens <= kFewThreads * kFillBatch
+          ? launch_tables<kFewThreads, 1>(p, 1, stream)
+          : batch <= kTableThreads ? launch_tables<kTableThreads, 1>(p, ctas, stream)
+                                   : launch_tables<kTableThreads, 8>(p, ctas, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }

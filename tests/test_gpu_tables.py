@@ -45,6 +45,19 @@ def test_many_tokens(tokens):
     check_tables(table, pool, cached, list(tokens), sum(tokens), owned, free, n)
 
 
+@pytest.mark.parametrize("B,tokens", [(127, 511), (128, 512), (128, 513), (129, 512), (1, 512),
+                                      (1, 513), (40, 1025)])
+def test_both_sides_of_the_small_call(B, tokens):
+    """Where the number of threads changes: shrinking, growing, finished and
+    untouched requests, and a token buffer with rows left over."""
+    rng = np.random.default_rng(1000 * B + tokens)
+    cached, new = rng.integers(0, 90, B), rng.multinomial(tokens - min(tokens, 3), np.ones(B) / B)
+    extra = rng.integers(0, 4, B)
+    cached[B // 2] = new[B // 2] = 0
+    table, owned, free, n, pool = _pool(rng, B, cached, extra, 2 * B + tokens, new=new)
+    check_tables(table, pool, cached, new, tokens, owned, free, n)
+
+
 @pytest.mark.parametrize("spare", [0, 1, 2, 3, 4, 5, 9])
 def test_pool_runs_out(spare):
     """Requests are served in order until the list is short; one that needs no
