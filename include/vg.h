@@ -451,6 +451,7 @@ vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride,
  *   lse          NULL, or float32 [num_tokens][num_q_heads]: natural log of
  *                the row's sum of exponentials, -inf for a row that attends
  *                nothing.
+ *   workspace    vg_chunk_workspace_bytes() bytes, 16-byte aligned.
  * What lies in the cache past a row's own position does not reach the row,
  * whatever it holds.  A sequence whose rows are not a range inside
  * [0, num_tokens), or whose length is negative or longer than its table row,

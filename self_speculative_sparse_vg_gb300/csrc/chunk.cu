@@ -1294,6 +1294,7 @@ extern "C" vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, in
     return VG_ERR_UNSUPPORTED;
   const ChunkPlan pl = make_chunk_plan(num_tokens, g, kv->head_dim);
   if (!workspace || workspace_bytes < pl.bytes) return VG_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 15) return VG_ERR_INVALID_ARGUMENT;
   CUtensorMap tq, tk, tv;
   if (!page_chunk_tensor_map(kv->k_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tk) ||
       !page_chunk_tensor_map(kv->v_pages, kv->num_pages, kv->num_kv_heads, kv->head_dim, &tv) ||

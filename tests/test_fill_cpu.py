@@ -85,6 +85,8 @@ def test_chunk_attention_refusals(vg):
     assert call(n=0) == 0
     need = vg._lib.vg_chunk_workspace_bytes(2, 5, 32, 8, 128)
     assert need > 0 and call() == 3 and call(ws=FAKE, wsb=need - 1) == 3
+    for off in (1, 4, 8):
+        assert call(ws=FAKE + off, wsb=need + 64) == 1, off
     for bad in ((0, 5, 32, 8, 128), (2, 0, 32, 8, 128), (2, 5, 33, 8, 128), (2, 5, 32, 8, 96),
                 (2, 5, 136, 8, 128)):
         assert vg._lib.vg_chunk_workspace_bytes(*bad) == 0, bad
