@@ -16,8 +16,13 @@
 // part.  4096 tokens of 8 requests take 5.4 us, 114K 9; a second kernel for the
 // tokens instead of the cluster took 4.7 - 5.6 us and 2 us more of host time for
 // its launch, one CTA alone 6.5 us for 4096.  A few requests and tokens get a CTA
-// of 128 threads, whose start and barriers are shorter: 3.2 us for 64 tokens of 8
+// of 128 threads, whose start and barriers are shorter: 3.3 us for 64 tokens of 8
 // requests against 4.4 with 1024 (and three barriers a sum).
+//
+// Pages that move are loads with stores that wait for them, so the CTA shares the
+// longer runs: 7 prompts of 8K - 16K tokens 12 us (46 with a request's run left to
+// one warp), 8 requests that give 20K pages back 17 (52), 12 prompts beside 288
+// other requests 14 (19).
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -30,7 +35,9 @@ constexpr int kTableThreads = 1024;
 constexpr int kFewThreads = 128;       // of a CTA for a few requests and tokens
 constexpr int kMaxTableCluster = 16;
 constexpr int kMaxTableBatch = 8192;   // requests: 8 per thread
-constexpr int kFillBatch = 4;          // tokens of a thread whose loads are in flight together
+constexpr int kFillBatch = 4;          // tokens or pages of a thread whose loads are in flight together
+constexpr int kRuns = 128;             // runs of pages that a CTA shares; a thread moves the others alone
+constexpr int kRunBatch = 8;           // pages of a lane whose loads are in flight together in a shared run
 
 struct TableParams {
   const int32_t* cached;
@@ -116,12 +123,88 @@ __device__ __forceinline__ void fill_tokens(const TableParams& p, const int32_t*
   }
 }
 
+// Pages [lo, hi) of request b that move: page j goes to place at + j of the free
+// list, or comes from place at - j.
+struct PageRun {
+  int b, lo, hi;
+  long long at;
+};
+
+// Whether pages [lo, hi) of request b are page ids (those of this thread: first,
+// first + step, ...).  Here and below the loads of N pages are issued together.
+template <int N>
+__device__ __forceinline__ bool pages_fine(const TableParams& p, int b, int lo, int hi, int first,
+                                           int step) {
+  const int32_t* row = p.page_table + (size_t)b * p.width;
+  bool fine = true;
+  for (int j = lo + first; j < hi; j += N * step) {
+    int page[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) page[k] = j + k * step < hi ? row[j + k * step] : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) fine &= page[k] >= 0 && page[k] < p.num_pages;
+  }
+  return fine;
+}
+
+template <int N>
+__device__ __forceinline__ void push_pages(const TableParams& p, int b, int lo, int hi, long long at,
+                                           int first, int step) {
+  int32_t* row = p.page_table + (size_t)b * p.width;
+  for (int j = lo + first; j < hi; j += N * step) {
+    int page[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) page[k] = j + k * step < hi ? row[j + k * step] : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (j + k * step < hi) {
+        p.free_pages[at + j + k * step] = page[k];
+        row[j + k * step] = -1;
+      }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void pop_pages(const TableParams& p, int b, int lo, int hi, long long at,
+                                          int first, int step) {
+  int32_t* row = p.page_table + (size_t)b * p.width;
+  for (int j = lo + first; j < hi; j += N * step) {
+    int page[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      page[k] = j + k * step < hi ? p.free_pages[at - (j + k * step)] : 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (j + k * step < hi) {
+        const bool fine = page[k] >= 0 && page[k] < p.num_pages;
+        if (!fine) flag_error(p.error_flag, VG_DEVERR_PAGE);
+        row[j + k * step] = fine ? page[k] : -1;
+      }
+  }
+}
+
+// f(run, lo, hi) for this warp's share of the runs' pieces.
+template <int NT, typename F>
+__device__ __forceinline__ void for_pieces(const PageRun* runs, int n, F f) {
+  constexpr int kWarps = NT / 32, kPiece = 32 * kRunBatch;
+  const int warp = threadIdx.x >> 5;
+#pragma unroll 4
+  for (int e = 0; e < n; ++e) {
+    const int lo = runs[e].lo, count = runs[e].hi - lo;
+    for (int k = (warp - e) & (kWarps - 1); k * kPiece < count; k += kWarps)
+      f(e, lo + k * kPiece, lo + min(count, (k + 1) * kPiece));
+  }
+}
+
 // The tables, by one CTA; also leaves the requests' end rows in ends_s.
 template <int NT, int IPT>
 __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* ends_s,
                                               long long (*part)[NT / 32]) {
+  __shared__ PageRun runs[kRuns];  // of pages that go back, then of pages that are taken
+  __shared__ int runs_n[2], run_bad[kRuns];
   const int tid = threadIdx.x, lane = tid & 31;
   const int b0 = tid * IPT;
+  if (tid < 2) runs_n[tid] = 0;
   // a fixed table has no free list: every request keeps the pages it has
   const bool fixed = p.owned == nullptr;
   const int top0 = fixed ? 0 : *p.free_count;
@@ -160,25 +243,36 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
   }
   if (tid == 0) p.cu_tokens[0] = 0;
   if (!fixed) {
-    // -------- pages that go back: checked by whole warps, then pushed
+    // -------- pages that go back: checked, then pushed.  A thread moves a few
+    // pages of its request itself, longer runs are shared by the CTA.
+    int run[IPT];
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-      uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && own[i] > need[i]);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int lo = __shfl_sync(0xffffffffu, need[i], src);
-        const int hi = __shfl_sync(0xffffffffu, own[i], src);
-        const int b = __shfl_sync(0xffffffffu, b0, src) + i;
-        bool fine = true;
-        for (int j = lo + lane; j < hi; j += 32) {
-          const int page = p.page_table[(size_t)b * p.width + j];
-          fine &= page >= 0 && page < p.num_pages;
-        }
-        if (!__all_sync(0xffffffffu, fine) && lane == src) {
+      run[i] = kRuns;
+      if (ok[i] && own[i] > need[i]) {
+        if (own[i] - need[i] > kFillBatch) run[i] = atomicAdd(&runs_n[0], 1);
+        if (run[i] < kRuns) {
+          runs[run[i]] = {b0 + i, need[i], own[i], 0};
+          run_bad[run[i]] = 0;
+        } else if (!pages_fine<kFillBatch>(p, b0 + i, need[i], own[i], 0, 1)) {
           ok[i] = false;
           flag_error(p.error_flag, VG_DEVERR_PAGE);
         }
+      }
+    }
+    __syncthreads();
+    const int returns = min(runs_n[0], kRuns);
+    if (returns > 0) {
+      for_pieces<NT>(runs, returns, [&](int e, int lo, int hi) {
+        if (!pages_fine<kRunBatch>(p, runs[e].b, lo, hi, lane, 32)) run_bad[e] = 1;
+      });
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      if (run[i] < kRuns && run_bad[run[i]]) {
+        ok[i] = false;
+        flag_error(p.error_flag, VG_DEVERR_PAGE);
       }
       back += ok[i] ? max(own[i] - need[i], 0) : 0;
     }
@@ -197,22 +291,20 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     int at = top0 + (int)back_sum - back;  // this thread's first push
     if (list_ok) {
 #pragma unroll
-      for (int i = 0; i < IPT; ++i) {
-        uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && own[i] > need[i]);
-        while (todo) {
-          const int src = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const int lo = __shfl_sync(0xffffffffu, need[i], src);
-          const int hi = __shfl_sync(0xffffffffu, own[i], src);
-          const int b = __shfl_sync(0xffffffffu, b0, src) + i;
-          const int to = __shfl_sync(0xffffffffu, at, src);
-          for (int j = lo + lane; j < hi; j += 32) {
-            int32_t* e = p.page_table + (size_t)b * p.width + j;
-            p.free_pages[to + j - lo] = *e;
-            *e = -1;
-          }
+      for (int i = 0; i < IPT; ++i)
+        if (ok[i] && own[i] > need[i]) {
+          const long long to = (long long)at - need[i];
+          if (run[i] < kRuns)
+            runs[run[i]].at = to;
+          else
+            push_pages<kFillBatch>(p, b0 + i, need[i], own[i], to, 0, 1);
+          at += own[i] - need[i];
         }
-        if (ok[i]) at += max(own[i] - need[i], 0);
+      if (returns > 0) {
+        __syncthreads();
+        for_pieces<NT>(runs, returns, [&](int e, int lo, int hi) {
+          if (!run_bad[e]) push_pages<kRunBatch>(p, runs[e].b, lo, hi, runs[e].at, lane, 32);
+        });
       }
     }
     __syncthreads();
@@ -227,20 +319,13 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
         ok[i] = false;
         flag_error(p.error_flag, VG_DEVERR_POOL);
       }
-      uint32_t todo = __ballot_sync(0xffffffffu, ok[i] && more > 0);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int lo = __shfl_sync(0xffffffffu, own[i], src);
-        const int hi = __shfl_sync(0xffffffffu, need[i], src);
-        const int b = __shfl_sync(0xffffffffu, b0, src) + i;
-        const int from = top - 1 - (int)__shfl_sync(0xffffffffu, want, src);
-        for (int j = lo + lane; j < hi; j += 32) {
-          const int page = p.free_pages[from - (j - lo)];
-          const bool fine = page >= 0 && page < p.num_pages;
-          if (!fine) flag_error(p.error_flag, VG_DEVERR_PAGE);
-          p.page_table[(size_t)b * p.width + j] = fine ? page : -1;
-        }
+      if (ok[i] && more > 0) {
+        const long long from = (long long)top - 1 - want + own[i];
+        const int e = more > kFillBatch ? atomicAdd(&runs_n[1], 1) : kRuns;
+        if (e < kRuns)
+          runs[e] = {b0 + i, own[i], need[i], from};
+        else
+          pop_pages<kFillBatch>(p, b0 + i, own[i], need[i], from, 0, 1);
       }
       want += more;
       if (ok[i] && b0 + i < p.batch) {
@@ -250,6 +335,9 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     }
     warp_inclusive_sum(taken, part[3]);
     __syncthreads();
+    for_pieces<NT>(runs, min(runs_n[1], kRuns), [&](int e, int lo, int hi) {
+      pop_pages<kRunBatch>(p, runs[e].b, lo, hi, runs[e].at, lane, 32);
+    });
     sum_of_warps_before<NT>(part[3], &all);
     if (tid == 0 && list_ok) *p.free_count = top - (int)all;
   }

@@ -58,6 +58,31 @@ def test_both_sides_of_the_small_call(B, tokens):
     check_tables(table, pool, cached, new, tokens, owned, free, n)
 
 
+@pytest.mark.parametrize("B", [100, 400, 1100])
+def test_long_runs_of_pages(B):
+    """Requests that give back or take 4, 5, 255, 256, 257 and more pages: more
+    long runs than the CTA shares at once, of both kinds, and none at all."""
+    rng = np.random.default_rng(B)
+    sizes = np.array([0, 1, 4, 5, 12, 31, 32, 33, 255, 256, 257, 700])
+    move = rng.choice(sizes, B, p=[.1, .1, .1, .2, .15, .1, .1, .05, .03, .02, .03, .02])
+    grows = rng.random(B) < 0.5
+    cached = rng.integers(0, 60, B)
+    new = np.where(grows, np.maximum(16 * move - rng.integers(0, 15, B), 0), rng.integers(0, 3, B))
+    extra = np.where(grows, 0, move + (-(-(cached + new) // PAGE)) - (-(-cached // PAGE)))
+    table, owned, free, n, pool = _pool(rng, B, cached, extra, int(move.sum()) + B, new=new)
+    check_tables(table, pool, cached, new, int(new.sum()), owned, free, n)
+
+
+@pytest.mark.parametrize("where", [0, 128, 255, 256, 699])
+def test_a_foreign_page_in_a_long_run(where):
+    """A run with a page id that is none stays where it is; the others move."""
+    rng = np.random.default_rng(where)
+    cached, new, extra = [16, 5, 64, 0], [0, 3, 0, 4000], [700, 300, 0, 0]
+    table, owned, free, n, pool = _pool(rng, 4, cached, extra, 300, new=new)
+    table[0, 1 + where] = pool + where
+    check_tables(table, pool, cached, new, sum(new), owned, free, n)
+
+
 @pytest.mark.parametrize("spare", [0, 1, 2, 3, 4, 5, 9])
 def test_pool_runs_out(spare):
     """Requests are served in order until the list is short; one that needs no
