@@ -12,15 +12,16 @@
 // the requests fix every request's place in it): a thread owns IPT
 // neighbouring requests, so one pass of warp shuffles makes each sum.  Then the
 // tokens' positions and slots are written, a token per thread; past 1024 tokens
-// the CTA is the first of a cluster whose others wait for it and share that
-// part.  4096 tokens of 8 requests take 5.4 us, 114K 9; a second kernel for the
-// tokens instead of the cluster took 4.7 - 5.6 us and 2 us more of host time for
-// its launch, one CTA alone 6.5 us for 4096.  A few requests and tokens get a CTA
-// of 128 threads, whose start and barriers are shorter: 3.3 us for 64 tokens of 8
+// the CTA is the first of a cluster that shares that part: the others find the
+// rows' requests and positions while it works on the tables (114K tokens 8.2 us,
+// 9.2 when they wait first).  When the cluster was chosen, 4096 tokens took 5.4
+// us, 6.5 with one CTA alone, and 4.7 - 5.6 with a second kernel for the tokens,
+// which cost 2 us more of host time.  A few requests and tokens get a CTA of 128
+// threads, whose start and barriers are shorter: 3.1 us for 64 tokens of 8
 // requests against 4.4 with 1024 (and three barriers a sum).
 //
 // Pages that move are loads with stores that wait for them, so the CTA shares the
-// longer runs: 7 prompts of 8K - 16K tokens 12 us (46 with a request's run left to
+// longer runs: 7 prompts of 8K - 16K tokens 11 us (46 with a request's run left to
 // one warp), 8 requests that give 20K pages back 17 (52), 12 prompts beside 288
 // other requests 14 (19).
 #include <limits.h>
@@ -84,11 +85,14 @@ __device__ __forceinline__ long long sum_of_warps_before(const long long* part, 
 }
 
 // Positions and slots of token rows first, first + stride, ...; ends[b] =
-// clamped end row of request b.
+// clamped end row of request b.  What needs no table comes before `tables_done`,
+// which every thread calls once.
+template <typename F>
 __device__ __forceinline__ void fill_tokens(const TableParams& p, const int32_t* ends, int first,
-                                            int stride) {
-  for (int64_t t0 = first; t0 < p.max_tokens; t0 += (int64_t)kFillBatch * stride) {
-    int req[kFillBatch], pos[kFillBatch], page[kFillBatch];
+                                            int stride, F tables_done) {
+  for (int64_t t0 = first; t0 == first || t0 < p.max_tokens; t0 += (int64_t)kFillBatch * stride) {
+    int req[kFillBatch], len[kFillBatch], page[kFillBatch];
+    uint32_t pos[kFillBatch];  // means nothing where the request is refused
 #pragma unroll
     for (int k = 0; k < kFillBatch; ++k) {
       const int64_t t = t0 + (int64_t)k * stride;
@@ -100,24 +104,29 @@ __device__ __forceinline__ void fill_tokens(const TableParams& p, const int32_t*
         else
           lo = mid + 1;
       }
-      req[k] = t < p.max_tokens && lo < p.batch && __ldcg(p.kv_lens + lo) > 0 ? lo : -1;
-      pos[k] = req[k] >= 0 ? __ldcg(p.cached + lo) + (int)(t - (lo > 0 ? ends[lo - 1] : 0)) : 0;
+      req[k] = t < p.max_tokens && lo < p.batch ? lo : -1;
+      pos[k] = req[k] >= 0 ? (uint32_t)__ldg(p.cached + lo) + (uint32_t)(t - (lo > 0 ? ends[lo - 1] : 0)) : 0;
     }
+    if (t0 == first) tables_done();
 #pragma unroll
-    for (int k = 0; k < kFillBatch; ++k)
-      page[k] = req[k] >= 0 ? __ldcg(p.page_table + (size_t)req[k] * p.width + pos[k] / kPageSize) : 0;
+    for (int k = 0; k < kFillBatch; ++k) {
+      const bool in = req[k] >= 0 && pos[k] / kPageSize < (uint32_t)p.width;
+      len[k] = req[k] >= 0 ? __ldcg(p.kv_lens + req[k]) : 0;
+      page[k] = in ? __ldcg(p.page_table + (size_t)req[k] * p.width + pos[k] / kPageSize) : -1;
+    }
 #pragma unroll
     for (int k = 0; k < kFillBatch; ++k) {
       const int64_t t = t0 + (int64_t)k * stride;
       if (t >= p.max_tokens) break;
+      const bool served = len[k] > 0;
       int slot = -1;
-      if (req[k] >= 0) {
+      if (served) {
         if (page[k] >= 0 && page[k] < p.num_pages)
-          slot = page[k] * kPageSize + pos[k] % kPageSize;
+          slot = page[k] * kPageSize + (int)(pos[k] % kPageSize);
         else
           flag_error(p.error_flag, VG_DEVERR_PAGE);
       }
-      p.positions[t] = pos[k];
+      p.positions[t] = served ? (int)pos[k] : 0;
       p.slots[t] = slot;
     }
   }
@@ -196,7 +205,7 @@ __device__ __forceinline__ void for_pieces(const PageRun* runs, int n, F f) {
   }
 }
 
-// The tables, by one CTA; also leaves the requests' end rows in ends_s.
+// The requests' end rows, in ends_s; and, by the grid's first CTA, the tables.
 template <int NT, int IPT>
 __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* ends_s,
                                               long long (*part)[NT / 32]) {
@@ -206,8 +215,8 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
   const int b0 = tid * IPT;
   if (tid < 2) runs_n[tid] = 0;
   // a fixed table has no free list: every request keeps the pages it has
-  const bool fixed = p.owned == nullptr;
-  const int top0 = fixed ? 0 : *p.free_count;
+  const bool fixed = p.owned == nullptr, leads = blockIdx.x == 0;
+  const int top0 = fixed || !leads ? 0 : *p.free_count;
   int cached[IPT], fresh[IPT], own[IPT], need[IPT];
   bool ok[IPT];
   long long rows = 0;
@@ -217,7 +226,7 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     const bool in = b < p.batch;
     cached[i] = in ? p.cached[b] : 0;
     fresh[i] = in ? p.fresh[b] : 0;
-    own[i] = in && !fixed ? p.owned[b] : 0;
+    own[i] = in && !fixed && leads ? p.owned[b] : 0;
     rows += max(fresh[i], 0);
   }
   // -------- rows of the packed token buffer
@@ -237,10 +246,12 @@ __device__ __forceinline__ void resize_tables(const TableParams& p, int32_t* end
     if (b < p.batch) {
       const int e = (int)(end < p.max_tokens ? end : p.max_tokens);
       ends_s[b] = e;
+      if (!leads) continue;
       p.cu_tokens[b + 1] = e;
       if (!ok[i]) flag_error(p.error_flag, VG_DEVERR_LENGTH);
     }
   }
+  if (!leads) return;
   if (tid == 0) p.cu_tokens[0] = 0;
   if (!fixed) {
     // -------- pages that go back: checked, then pushed.  A thread moves a few
@@ -352,15 +363,15 @@ __global__ void __launch_bounds__(NT) step_tables_kernel(const TableParams p) {
   __shared__ long long part[4][NT / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x == 0) resize_tables<NT, IPT>(p, ends_s, part);
-  if (gridDim.x > 1) {  // the grid is one cluster
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    if (blockIdx.x > 0)
-      for (int b = threadIdx.x; b < p.batch; b += NT) ends_s[b] = __ldcg(p.cu_tokens + b + 1);
-  }
+  const bool cluster = gridDim.x > 1;  // the grid is one
+  if (cluster && blockIdx.x > 0) cluster_arrive_release();
+  resize_tables<NT, IPT>(p, ends_s, part);
+  if (cluster && blockIdx.x == 0) cluster_arrive_release();
   __syncthreads();
-  fill_tokens(p, ends_s, blockIdx.x * NT + threadIdx.x, gridDim.x * NT);
+  fill_tokens(p, ends_s, blockIdx.x * NT + threadIdx.x, gridDim.x * NT, [&]() {
+    __syncwarp();
+    if (cluster) cluster_wait_acquire();
+  });
 }
 
 template <int NT, int IPT>
