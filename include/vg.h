@@ -420,10 +420,11 @@ vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, in
  *   interleaved  0: dim i turns with i + rot_dim / 2; 1: 2i with 2i + 1.
  *   slots        int32 [num_tokens]; a negative slot writes nothing to the
  *                cache (padding; the query is still turned), one past the pool
- *                is flagged VG_DEVERR_INDEX and skipped.  Of two tokens with
- *                the same slot either may be the one that stays.
- * Angles are exact up to the reduction to a turn, whatever the position; the
- * rotation is float32, rounded once.
+ *                is flagged VG_DEVERR_INDEX and skipped.  Tokens have slots of
+ *                their own: the rows of a slot given twice may hold parts of
+ *                either token.
+ * An angle's fraction of a turn is good to 2^-22 whatever the position, for
+ * frequencies up to 1 in size; the rotation is float32, rounded once.
  * ------------------------------------------------------------------------- */
 vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride, const void* k,
                          int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
