@@ -54,8 +54,10 @@ class PagedKVStruct(ctypes.Structure):
 
 
 def _load():
-    if not os.path.exists(_LIB_PATH):
-        raise ImportError(f"{_LIB_PATH} is not built; run `python -c \"import __graft_entry__ as g; "
+    for path in (_LIB_PATH, os.path.join(os.path.dirname(_LIB_PATH), "vg_binding.so")):
+        if os.path.exists(path):
+            continue
+        raise ImportError(f"{path} is not built; run `python -c \"import __graft_entry__ as g; "
                           f"g.build()\"` (needs nvcc with sm_103a support)")
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
