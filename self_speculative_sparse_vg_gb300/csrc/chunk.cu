@@ -247,6 +247,19 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
   return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
+// note_flags[slot * 2 + half]: the unit in this slot has notes of that half of
+// the dimensions.  The producer clears both before it publishes the unit, a
+// checking warp sets its own once its notes are laid out.  A row tile may end
+// while later tiles are still checked, so the store and the load are ordered.
+__device__ __forceinline__ void raise_notes(int* flag) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(flag)), "r"(1) : "memory");
+}
+__device__ __forceinline__ bool has_notes(const int* flag) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(flag)) : "memory");
+  return v != 0;
+}
+
 // The non-finite value that dimension c of a row attends, or 0: rel = the row's
 // token within the unit, notes = first token distance of a NaN, +inf and -inf.
 template <int HD>
@@ -441,11 +454,12 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
         }
         __syncwarp();
       }
-      if (valid && (note_flags[slot * 2] | note_flags[slot * 2 + 1])) {
+      const bool noted_lo = has_notes(&note_flags[slot * 2]), noted_hi = has_notes(&note_flags[slot * 2 + 1]);
+      if (valid && (noted_lo || noted_hi)) {
         // rows that attend a non-finite value of a checked tile
 #pragma unroll 1
         for (int c = 0; c < HD; ++c) {
-          if (!note_flags[slot * 2 + (c >= HD / 2)]) continue;
+          if (!(c < HD / 2 ? noted_lo : noted_hi)) continue;
           const float x = noted<HD>(notes, c, tok);
           if (x == 0.f) continue;
           if (direct)
@@ -628,7 +642,6 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
     if (un.kt0 == un.kt1) return;
     uint16_t* notes = notes_s + slot * 3 * HD;
     bool noting = false;
-    if (lane == 0) note_flags[slot * 2 + half] = 0;
     // the checked tiles are the last ones, from the first that has a position
     // past the first row's
     const int from = max(un.kt0, un.pos0 < 0 ? 0 : (un.pos0 + 1) / kTile);
@@ -657,7 +670,8 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
           for (int c = lane; c < 3 * HD / 2; c += 32)
             notes[c / (HD / 2) * HD + half * (HD / 2) + c % (HD / 2)] = 0xffff;
           noting = true;
-          if (lane == 0) note_flags[slot * 2 + half] = 1;
+          __syncwarp();
+          if (lane == 0) raise_notes(&note_flags[slot * 2 + half]);
         }
         __syncwarp();
         // a lane per dimension, rows in order
@@ -834,7 +848,7 @@ template <int HD>
 __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkBars& bars,
                                               const Share& s, const CUtensorMap& tmq,
                                               const CUtensorMap& tmk, const CUtensorMap& tmv,
-                                              Unit* units, uint8_t* smem, int lane) {
+                                              Unit* units, int* note_flags, uint8_t* smem, int lane) {
   using Lay = ChunkLayout<HD>;
   constexpr int NST = Lay::kStages;
   const int g = p.group, tt = kTile / g, tu = 2 * tt;
@@ -897,6 +911,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
     q_armed = false;
     if (lane == 0) {
       units[slot] = un;
+      note_flags[slot * 2] = note_flags[slot * 2 + 1] = 0;
       mbar_arrive(&bars.ufull[slot]);
     }
     __syncwarp();
@@ -1039,7 +1054,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const Share share = find_share(p, tab, lane);
     fence_proxy_async_smem();
     __syncwarp();
-    producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, smem, lane);
+    producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, note_flags, smem, lane);
   } else if (warp == kMma) {
     const uint32_t base = smem_u32(smem);
     if (!mma_role<HD>(p, bars, units, tmem, base + Lay::kRing, base, lane)) {
