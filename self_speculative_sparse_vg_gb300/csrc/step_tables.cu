@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(NT) step_tables_kernel(const TableParams p) {
   const bool cluster = gridDim.x > 1;  // the grid is one
   if (cluster && blockIdx.x > 0) cluster_arrive_release();
   resize_tables<NT, IPT>(p, ends_s, part);
+  __syncwarp();  // the tables' work leaves a warp's lanes apart, the cluster's barrier wants them together
   if (cluster && blockIdx.x == 0) cluster_arrive_release();
   __syncthreads();
   fill_tokens(p, ends_s, blockIdx.x * NT + threadIdx.x, gridDim.x * NT, [&]() {
