@@ -7,6 +7,7 @@ import -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -127,6 +128,13 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocating_for(stream):
+    """Where a call makes its own workspace: on the stream it runs on, so that
+    the block, free again when the call returns, goes to later work of that
+    stream only (and is filled in its order)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _check(fn, status):
     if status != 0:
         raise VGError(fn, status)
@@ -211,8 +219,9 @@ def sparse_verify_attention(kv: PagedKV, q, prefix_lens, max_prefix, softmax_sca
     B, R, Hq, d = q.shape
     max_blocks = blocks.shape[-1]
     if workspace is None:
-        workspace = zero_workspace(sparse_verify_workspace_bytes(
-            B, R, Hq, kv.num_kv_heads, d, max_prefix, max_blocks, num_splits), q.device)
+        with _allocating_for(stream):
+            workspace = zero_workspace(sparse_verify_workspace_bytes(
+                B, R, Hq, kv.num_kv_heads, d, max_prefix, max_blocks, num_splits), q.device)
     st = kv.struct()
     s = _lib.vg_sparse_verify_attention(ctypes.byref(st), _ptr(q), _ptr(prefix_lens), B, R, Hq,
                                         int(max_prefix), float(softmax_scale), _ptr(blocks),
@@ -253,8 +262,9 @@ def select_kv(capture, capture_mode, prefix_lens, num_q_heads, num_kv_heads, max
     B = prefix_lens.shape[0]
     cap = indices.shape[-1]
     if workspace is None:
-        workspace = zero_workspace(select_workspace_bytes(B, num_kv_heads, max_prefix, per_head),
-                                   indices.device)
+        with _allocating_for(stream):
+            workspace = zero_workspace(select_workspace_bytes(B, num_kv_heads, max_prefix, per_head),
+                                       indices.device)
     st, slots = _kv_arg(kv, slots)
     s = _lib.vg_select_kv(_ptr(capture), int(capture_mode), _ptr(prefix_lens), B, num_q_heads,
                           num_kv_heads, int(max_prefix), int(top_k), int(n_sink), int(n_recent),
@@ -278,8 +288,9 @@ def select_kv_weights(capture, n_rows, prefix_lens, num_q_heads, num_kv_heads, m
     B = prefix_lens.shape[0]
     cap = indices.shape[-1]
     if workspace is None:
-        workspace = zero_workspace(select_workspace_bytes(B, num_kv_heads, max_prefix, per_head),
-                                   indices.device)
+        with _allocating_for(stream):
+            workspace = zero_workspace(select_workspace_bytes(B, num_kv_heads, max_prefix, per_head),
+                                       indices.device)
     st, slots = _kv_arg(kv, slots)
     s = _lib.vg_select_kv_weights(_ptr(capture), int(n_rows), _ptr(prefix_lens), B, num_q_heads,
                                   num_kv_heads, int(max_prefix), int(top_k), int(n_sink),
@@ -366,7 +377,8 @@ def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None,
     if workspace is None:
         with torch.cuda.device(q.device):   # its size goes by the device
             n = chunk_workspace_bytes(kv_lens.numel(), *q.shape[:2], kv.num_kv_heads, kv.head_dim)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+            with _allocating_for(stream):
+                workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
     s = _binding.chunk_attention(kv.k_pages, kv.v_pages, kv.page_table, q, cu_q, kv_lens, softmax_scale,
                                  out, lse, workspace, error_flag,
                                  None if stream is None else stream.cuda_stream)
