@@ -456,16 +456,20 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
       }
       const bool noted_lo = has_notes(&note_flags[slot * 2]), noted_hi = has_notes(&note_flags[slot * 2 + 1]);
       if (valid && (noted_lo || noted_hi)) {
-        // rows that attend a non-finite value of a checked tile
+        // rows that attend a non-finite value of a checked tile: added to what
+        // this thread has just stored, which may hold another from a tile that
+        // was not checked, or a NaN of the row's scores
 #pragma unroll 1
         for (int c = 0; c < HD; ++c) {
           if (!(c < HD / 2 ? noted_lo : noted_hi)) continue;
           const float x = noted<HD>(notes, c, tok);
           if (x == 0.f) continue;
-          if (direct)
-            p.out[t * p.out_stride + (int64_t)qh * HD + c] = __float2bfloat16(x);
-          else
-            p.part_o[(((size_t)un.part * (HD / 4) + c / 4) * p.rows + prow) * 4 + c % 4] = x;
+          if (direct) {
+            __nv_bfloat16* e = p.out + t * p.out_stride + (int64_t)qh * HD + c;
+            *e = __float2bfloat16(__bfloat162float(*e) + x);
+          } else {
+            p.part_o[(((size_t)un.part * (HD / 4) + c / 4) * p.rows + prow) * 4 + c % 4] += x;
+          }
         }
       }
       if (valid && direct && p.lse)

@@ -36,3 +36,64 @@ def test_notes_of_one_unit_do_not_reach_later_ones(d):
         vg.chunk_attention(c.gpu(), qd, i32(cu), i32(lens), d ** -0.5, out, lse=lse)
         assert torch.equal(out.isnan(), w.isnan())
         assert torch.equal(out[~w.isnan()], w[~w.isnan()]) and torch.equal(lse, want_lse)
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+def _special(c, Hq, new, want, values=(), keys=(), seed=5):
+    """One call over sequence 0 of `c` after values[(position, dim)] and
+    keys[(position, dim)] were put into V and K; (out, want) with what the
+    formula gives: a value that is not finite adds to every row that attends it,
+    a NaN in a key makes NaN of every row that attends it."""
+    from self_speculative_sparse_vg_gb300 import vg
+    L, d = c.lens[0], c.kp.shape[3]
+    k, v, w = c.k[0].clone(), c.v[0].clone(), want.clone()
+    for (p, x), value in dict(values).items():
+        v[p, 0, x] = value
+        w[max(0, p - (L - new)):, :Hq, x] += value
+    for (p, x), value in dict(keys).items():
+        k[p, 0, x] = value
+        w[max(0, p - (L - new)):, :Hq] = NAN
+    c.write(0, k, v)
+    q = torch.randn(new, Hq, d, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    out = torch.zeros_like(q)
+    vg.chunk_attention(c.gpu(), q, i32([0, new]), i32([L]), d ** -0.5, out)
+    return out, w
+
+
+def _same(out, want):
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out[~out.isnan()], want[~want.isnan()])
+
+
+# one tile, which no cut divides, of one row tile or two; a few tiles, each in a
+# part of its own; long ones
+SHAPES = [(64, 100, 30, 4), (128, 120, 50, 4), (128, 128, 3, 8), (64, 200, 60, 4), (128, 300, 9, 4), (64, 30011, 90, 4), (128, 20003, 5, 2), (64, 9001, 1, 8)]
+
+
+@pytest.mark.parametrize("d,L,new,Hq", SHAPES)
+def test_values_of_both_kinds_add_up(d, L, new, Hq):
+    """In one dimension, a value before the chunk (in a tile that needs no look,
+    and in the one that does) and another inside it."""
+    c = Cache([L], 1, d, seed=32)
+    _, want, _ = check_chunk(c, [new], Hq)
+    pos0 = L - new
+    inside = pos0 + new // 2
+    values = {}
+    for at, (a, b) in enumerate([(NAN, INF), (-INF, INF), (INF, -INF), (INF, INF), (NAN, -INF), (-INF, -INF),
+                                 (INF, NAN)]):
+        values[(3, 2 * at)] = a                     # a far position
+        values[(pos0, d - 2 - 2 * at)] = a          # the first row's own
+        if new > 1:
+            values[(inside, 2 * at)] = b
+            values[(inside, d - 2 - 2 * at)] = b
+    _same(*_special(c, Hq, new, want, values))
+
+
+@pytest.mark.parametrize("d,L,new,Hq", SHAPES)
+def test_rows_of_nan_scores_stay_nan(d, L, new, Hq):
+    """A NaN in a key makes all of a row NaN, dimensions of an infinite value too."""
+    c = Cache([L], 1, d, seed=33)
+    _, want, _ = check_chunk(c, [new], Hq)
+    _same(*_special(c, Hq, new, want, {(L - 1, 5): INF, (L - 1, d - 1): -INF}, {(1, 3): NAN}))
