@@ -1082,7 +1082,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 // parts, which sit in slot 1 of the CTA where the unit begins and in slot 0 of
 // the following ones.  A CTA takes 32 rows, a lane each (the parts' layout);
 // a warp takes an eighth of the dimensions, and the rows leave through shared
-// memory in whole lines.
+// memory in whole lines.  A part is never passed over: one that a row does not
+// attend is zero, and a NaN or an infinity of one whose weight underflows still
+// has to show (as NaN), as it does where no cut falls.
 constexpr int kMergeWarps = 8, kMergeRows = 32;
 
 template <int HD>
@@ -1116,17 +1118,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 #pragma unroll
       for (int k = 0; k < NP; ++k) v[k] = __ldcg(po + (slot(i) * (HD / 4) + k) * p.rows);
       const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-      const float f = ex2(m - ref), w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
-      l *= f;
-      if (w != 0.f) l += w * x.y;
+      const float f = ex2(m - ref), w = ex2(x.x - ref);
+      l = fmaf(l, f, w * x.y);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const float y[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[k][e] *= f;
-          if (w != 0.f) acc[k][e] = fmaf(w, y[e], acc[k][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(w, y[e], acc[k][e] * f);
       }
       m = mn;
     }
@@ -1181,15 +1179,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_row_kernel(const
       v[0] = y.x, v[1] = y.y;
     }
     const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-    const float f = ex2(m - ref), w = x.x == -INFINITY ? (x.y == x.y ? 0.f : NAN) : ex2(x.x - ref);
-    l *= f;
+    const float f = ex2(m - ref), w = ex2(x.x - ref);
+    l = fmaf(l, f, w * x.y);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-    if (w != 0.f) {
-      l += w * x.y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
-    }
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e] * f);
     m = mn;
   }
 #pragma unroll
@@ -1207,12 +1200,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_row_kernel(const
   float l_all = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
   for (int i = 0; i < kMergeWarps; ++i) {
-    const float li = l_s[i], w = li == li ? ex2(m_s[i] - ref) : NAN;
-    if (w != 0.f) {
-      l_all += w * li;
-      o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
-      o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
-    }
+    const float w = ex2(m_s[i] - ref);
+    l_all += w * l_s[i];
+    o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
+    o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
   }
   const float inv = l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN;
   const int t = mu.tok0 + row / g, qh = mu.h * g + row % g;

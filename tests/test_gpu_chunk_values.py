@@ -97,3 +97,39 @@ def test_rows_of_nan_scores_stay_nan(d, L, new, Hq):
     c = Cache([L], 1, d, seed=33)
     _, want, _ = check_chunk(c, [new], Hq)
     _same(*_special(c, Hq, new, want, {(L - 1, 5): INF, (L - 1, d - 1): -INF}, {(1, 3): NAN}))
+
+
+# a CTA per row merges up to 32 rows, one per 32 rows more of them
+@pytest.mark.parametrize("falls", [False, True])
+@pytest.mark.parametrize("d,new,Hq", [(64, 1, 4), (128, 1, 8), (64, 40, 4), (128, 33, 2), (64, 1, 1)])
+def test_a_part_of_no_weight_still_shows_what_is_not_finite(d, new, Hq, falls):
+    """Scores that rise or fall by hundreds along the positions: the first or
+    the last parts weigh nothing, but a NaN or an infinity that a row attends
+    there shows, and a NaN score makes the row NaN."""
+    from self_speculative_sparse_vg_gb300 import vg
+    L = 20000
+    c = Cache([L], 1, d, seed=34)
+    ramp = (torch.arange(L) * ((-400.0 if falls else 400.0) / L) / (0.5 * d ** 0.5))[:, None, None]
+    c.k[0] = (c.k[0].float() * 0.1 + ramp).bfloat16()
+    c.write(0, c.k[0], c.v[0])
+    q = torch.full((new, Hq, d), 0.5, dtype=torch.bfloat16)
+    _, want, want_lse = check_chunk(c, [new], Hq, q=q)
+
+    def call():
+        out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+        vg.chunk_attention(c.gpu(), q.cuda(), i32([0, new]), i32([L]), d ** -0.5, out, lse=lse)
+        return out, lse
+    v = c.v[0].clone()
+    at = (lambda p: L - 1 - new - p) if falls else (lambda p: p)  # noqa: E731
+    v[at(3), 0, 2], v[at(5), 0, 4], v[at(9000), 0, d - 1] = NAN, INF, -INF
+    c.write(0, c.k[0], v)
+    out, lse = call()
+    bad = [2, 4, d - 1]
+    rest = [x for x in range(d) if x not in bad]
+    assert torch.equal(out[..., rest], want[..., rest]) and torch.equal(lse, want_lse)
+    assert out[..., 2].isnan().all() and not out[..., bad].isfinite().any()
+    k = c.k[0].clone()
+    k[at(7), 0, 1] = NAN
+    c.write(0, k, c.v[0])
+    out, lse = call()
+    assert out.isnan().all() and lse.isnan().all()
