@@ -146,6 +146,7 @@ class DecodeStack:
         self.inv_freq = None if not s.rope_theta else (
             s.rope_theta ** (-torch.arange(d // 2, dtype=torch.float64) * 2 / d)).float().to(dev)
         self.placed = [int(L) for L in s.prefix_lens]   # tokens cached by prefill, on the host
+        self.seeded = False                             # decoding has started: no more prompt
         self._places = {}
         self.draws = make_acceptance(s)
         self.iteration = 0
@@ -235,12 +236,14 @@ class DecodeStack:
 
     def prefill(self, inputs: torch.Tensor, new_lens) -> torch.Tensor:
         """Add a chunk of prompt tokens to every sequence, before the seed
-        verify: inputs float64 [T][hidden], the sequences' input vectors one
+        verify (refused after it): inputs float64 [T][hidden], the sequences' input vectors one
         after another, new_lens the number of each (0 allowed).  Their rows
         attend everything cached and themselves causally.  The next token's
         input becomes the normalised residual of each sequence's last row.
         Returns the final residuals [T][hidden]."""
         s = self.spec
+        if self.seeded:
+            raise ValueError("prefill: decoding has started, a prompt enters before it")
         new = [int(n) for n in new_lens]
         if len(new) != s.batch or min(new) < 0 or sum(new) != inputs.shape[0]:
             raise ValueError("prefill: new_lens does not match the batch or the input rows")
@@ -277,6 +280,7 @@ class DecodeStack:
         """A one-row verify of the first token over the initial context
         seeds every layer's selection; the token is committed."""
         s = self.spec
+        self.seeded = True
         x = self.e[:, None, :]                                   # [B][1][H]
         self._place(self.lens, 1)
         for l in range(s.layers):
