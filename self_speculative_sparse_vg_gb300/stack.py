@@ -169,22 +169,24 @@ class DecodeStack:
 
     def _place(self, pos, n):
         """Rows, lengths, positions and cache slots of a step that adds n tokens
-        (an int, or an int32 tensor of as many per sequence as `total` rows hold)
-        to every sequence from position pos[b]; the layers' writes use them."""
-        B = self.spec.batch
-        new, total = (n, int(n.sum())) if isinstance(n, torch.Tensor) else (n, n * B)
-        key = n if isinstance(n, int) else -total
-        if key not in self._places:
-            i32 = lambda m: torch.empty(m, dtype=torch.int32, device=self.device)  # noqa: E731
-            self._places[key] = dict(new=i32(B), cu=i32(B + 1), lens=i32(B), positions=i32(total),
-                                     slots=i32(total))
-            if isinstance(n, int):
-                self._places[key]["new"].fill_(n)
-        self.at = at = self._places[key]
+        (an int, or an int32 tensor of as many per sequence) to every sequence
+        from position pos[b]; the layers' writes use them.  The tensors of an int
+        are kept for its next step, those of a chunk go with it."""
         if isinstance(n, torch.Tensor):
-            at["new"].copy_(new)
+            at = self._new_place(n.to(self.device), int(n.sum()))
+        else:
+            if n not in self._places:
+                new = torch.full((self.spec.batch,), n, dtype=torch.int32, device=self.device)
+                self._places[n] = self._new_place(new, n * self.spec.batch)
+            at = self._places[n]
+        self.at = at
         vg.step_tables(self.page_table, self.num_pages, pos, at["new"], at["cu"], at["lens"],
                        at["positions"], at["slots"], error_flag=self.flag)
+
+    def _new_place(self, new, total):
+        i32 = lambda m: torch.empty(m, dtype=torch.int32, device=self.device)  # noqa: E731
+        B = self.spec.batch
+        return dict(new=new, cu=i32(B + 1), lens=i32(B), positions=i32(total), slots=i32(total))
 
     def _write_kv(self, l, k, v, pos):
         """k, v [B][n][Hkv][d] to positions pos[b] + 0..n-1, where _place put

@@ -27,3 +27,18 @@ def test_no_prompt_once_decoding_has_started():
         assert torch.equal(st.lens, lens) and torch.equal(st.e, e)
         assert all(torch.equal(a, b) for a, b in zip(st.kp + st.vp, pools))
     assert int(st.flag.item()) == 0
+
+
+def test_what_a_chunk_used_goes_with_it():
+    """Chunks of many sizes leave no buffers behind; the decode steps' own, one
+    set for each block length, are kept."""
+    st = _stack()
+    for n in range(1, 9):
+        st.prefill(torch.randn(2 * n + 1, st.spec.hidden, dtype=torch.float64, device="cuda"), [n, n + 1])
+    assert len(st._places) == 0
+    st.run()
+    kept = {n: id(p) for n, p in st._places.items()}
+    assert set(kept) == {1, st.spec.n_drafts + 1}
+    st.draws = st.draws.repeat(2, 1, 1)
+    st.step()
+    assert {n: id(p) for n, p in st._places.items()} == kept and int(st.flag.item()) == 0
