@@ -179,7 +179,7 @@ class DecodeStack:
                 new = torch.full((self.spec.batch,), n, dtype=torch.int32, device=self.device)
                 self._places[n] = self._new_place(new, n * self.spec.batch)
             at = self._places[n]
-        self.at = at
+        self.at, self.at_pos = at, pos
         vg.step_tables(self.page_table, self.num_pages, pos, at["new"], at["cu"], at["lens"],
                        at["positions"], at["slots"], error_flag=self.flag)
 
@@ -190,7 +190,9 @@ class DecodeStack:
 
     def _write_kv(self, l, k, v, pos):
         """k, v [B][n][Hkv][d] to positions pos[b] + 0..n-1, where _place put
-        them."""
+        them: pos is the tensor that it was given last."""
+        if pos is not self.at_pos:
+            raise ValueError("_write_kv: the rows were placed at other positions")
         vg.rope_append(self.kv[l], None, k.flatten(0, 1), v.flatten(0, 1), self.at["slots"],
                        error_flag=self.flag)
 

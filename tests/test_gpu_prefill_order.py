@@ -42,3 +42,18 @@ def test_what_a_chunk_used_goes_with_it():
     st.draws = st.draws.repeat(2, 1, 1)
     st.step()
     assert {n: id(p) for n, p in st._places.items()} == kept and int(st.flag.item()) == 0
+
+
+def test_rows_are_written_where_they_were_placed():
+    """Rows for positions that were not the last to be placed are refused (they
+    would be written over other tokens)."""
+    st = _stack()
+    s, before = st.spec, st.lens
+    k = torch.ones(s.batch, 1, s.num_kv_heads, s.head_dim, dtype=torch.bfloat16, device="cuda")
+    st._place(before, 1)
+    st._write_kv(0, k, k, before)
+    st._place(before + 1, 1)
+    pool = st.kp[0].clone()
+    with pytest.raises(ValueError, match="other positions"):
+        st._write_kv(0, k * 2, k * 2, before)
+    assert torch.equal(st.kp[0], pool)
