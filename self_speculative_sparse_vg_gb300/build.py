@@ -4,7 +4,9 @@ vg_binding.so, the native part of its Python binding.
 Each .cu file is compiled to an object in parallel, then linked into
 self_speculative_sparse_vg_gb300/libvg.so, which knows nothing of torch or
 Python.  vg_binding.so reads tensors through torch's headers and links to
-libvg.so beside it.  No cmake.
+libvg.so beside it; where its headers or libraries are not installed it is left
+out, with a warning: the calls that fill the cache then raise, the others work.
+No cmake.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -60,6 +63,20 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def binding_lacks() -> str:
+    """What vg_binding.so would need that is not installed here; "" for nothing."""
+    if not shutil.which(CXX):
+        return f"a C++ compiler ({CXX})"
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    for path in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                 os.path.join(_torch_dir(), "include", "c10", "cuda", "CUDAGuard.h"),
+                 os.path.join(_torch_dir(), "lib", "libc10_cuda.so")):
+        if not os.path.exists(path):
+            return path
+    return ""
+
+
 def _compile_binding() -> str:
     obj, inc = os.path.join(BUILD, "vg_binding.o"), os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -69,22 +86,28 @@ def _compile_binding() -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+def _link_binding(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
-    _run([CXX, "-shared", "-o", BINDING + ".tmp", binding.result(), "-L", PKG, "-l:libvg.so", "-L", lib,
-          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN:" + lib],
+    _run([CXX, "-shared", "-o", BINDING + ".tmp", obj, "-L", PKG, "-l:libvg.so", "-L", lib, "-lc10",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN:" + lib],
          "link of vg_binding.so")
     os.replace(BINDING + ".tmp", BINDING)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    lacks = binding_lacks()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = None if lacks else ex.submit(_compile_binding)
+        objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+    _run([nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs], "link")
+    os.replace(LIB + ".tmp", LIB)
+    if lacks:
+        if os.path.exists(BINDING):   # one of another libvg.so
+            os.remove(BINDING)
+        warnings.warn(f"vg_binding.so is left out: {lacks} is missing; the calls that fill the cache need it")
+    else:
+        _link_binding(binding.result())
     return LIB
 
 

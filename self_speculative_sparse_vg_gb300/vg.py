@@ -3,7 +3,8 @@
 Argument marshalling only: tensors in, device pointers and sizes out, the
 current torch stream passed through.  Every step of the hot path runs in the
 library's CUDA kernels; if the library is missing this module raises on
-import -- there is no fallback.
+import -- there is no fallback.  The calls that fill the cache go through the
+native vg_binding.so, which checks their arguments; without it they raise.
 """
 from __future__ import annotations
 
@@ -55,10 +56,8 @@ class PagedKVStruct(ctypes.Structure):
 
 
 def _load():
-    for path in (_LIB_PATH, os.path.join(os.path.dirname(_LIB_PATH), "vg_binding.so")):
-        if os.path.exists(path):
-            continue
-        raise ImportError(f"{path} is not built; run `python -c \"import __graft_entry__ as g; "
+    if not os.path.exists(_LIB_PATH):
+        raise ImportError(f"{_LIB_PATH} is not built; run `python -c \"import __graft_entry__ as g; "
                           f"g.build()\"` (needs nvcc with sm_103a support)")
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -102,7 +101,23 @@ def _load():
 
 
 _lib = _load()
-from . import vg_binding as _binding  # noqa: E402  (links to the library loaded above)
+
+
+class _NoBinding:
+    """In the place of vg_binding.so: its calls raise."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"vg.{name} needs vg_binding.so, which is not built or does not load "
+                          f"({self._why}); building it needs a C++ compiler and the headers of Python and torch")
+
+
+try:
+    from . import vg_binding as _binding  # links to the library loaded above
+except ImportError as _e:
+    _binding = _NoBinding(_e)
 
 
 def set_wait_limit_ns(limit_ns: int) -> None:
