@@ -387,7 +387,8 @@ vg_status vg_verify_attention_noalloc(const vg_paged_kv* kv, const void* q,
  * ids outside [0, num_pages) are flagged VG_DEVERR_PAGE: a request that would
  * return one is refused, a token on one has slot -1.
  * Outputs must not overlap inputs.  One kernel.
- * Supported: batch <= 8192.
+ * Supported: batch <= 8192 (vg_chunk_attention takes 4096 sequences a call and
+ * says how it attends a larger step).
  * ------------------------------------------------------------------------- */
 vg_status vg_step_tables(const int32_t* cached_lens, const int32_t* new_lens, int batch,
                          int32_t* page_table, int max_pages_per_seq, int num_pages,
@@ -462,6 +463,9 @@ vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride,
  * Results do not depend on what else is in the batch up to float32 rounding,
  * and are the same on every run.
  * Supported: head_dim 64/128, num_q_heads / num_kv_heads <= 16, batch <= 4096.
+ * A step of more sequences takes a call for every 4096, with cu_q, kv_lens and
+ * the page table from the call's first sequence on and q, out, lse and
+ * num_tokens of the whole step; the calls may share a workspace in one stream.
  * ------------------------------------------------------------------------- */
 size_t vg_chunk_workspace_bytes(int batch, int num_tokens, int num_q_heads, int num_kv_heads,
                                 int head_dim);

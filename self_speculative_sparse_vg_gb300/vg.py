@@ -388,7 +388,8 @@ def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None,
     the paged cache.  q and out [T][Hq][d] bf16, cu_q int32 [B + 1], kv_lens
     int32 [B] (new tokens included), lse (optional) float32 [T][Hq].
     workspace: uint8 tensor of chunk_workspace_bytes() (allocated here when not
-    given)."""
+    given).  At most 4096 sequences: a larger step is attended in parts, cu_q[a:b
+    + 1], kv_lens[a:b] and a PagedKV of page_table[a:b] with the whole q and out."""
     if workspace is None:
         with torch.cuda.device(q.device):   # its size goes by the device
             n = chunk_workspace_bytes(kv_lens.numel(), *q.shape[:2], kv.num_kv_heads, kv.head_dim)
