@@ -448,20 +448,25 @@ vg_status vg_rope_append(const vg_paged_kv* kv, const void* q, int64_t q_stride,
  *                included (their K/V are in the cache).  Token i of n_b sits
  *                at position kv_lens[b] - n_b + i and attends the positions up
  *                to its own.  A row that attends nothing (kv_lens[b] < n_b
- *                leaves the first rows without) is zero.
+ *                leaves the first rows without, or its scores are all
+ *                -infinity) is zero.
  *   softmax_scale  > 0.
  *   lse          NULL, or float32 [num_tokens][num_q_heads]: natural log of
  *                the row's sum of exponentials, -inf for a row that attends
  *                nothing.
  *   workspace    vg_chunk_workspace_bytes() bytes, 16-byte aligned.
  * What lies in the cache past a row's own position does not reach the row,
- * whatever it holds.  A sequence whose rows are not a range inside
+ * whatever it holds.  A NaN or an infinity of V shows in its dimension of every
+ * row that attends it, as in the formula, or as NaN where its weight underflows.
+ * A sequence whose rows are not a range inside
  * [0, num_tokens), or whose length is negative or longer than its table row,
  * is flagged VG_DEVERR_LENGTH and its rows are left as they were (rows that
  * offsets out of order give to two sequences hold either's).  Positions on a page id
  * outside [0, num_pages) are flagged VG_DEVERR_PAGE and count as zero K and V.
- * Results do not depend on what else is in the batch up to float32 rounding,
- * and are the same on every run.
+ * Results are the same on every run.  They depend on what else is in the batch
+ * by rounding alone: it decides where a long sequence is cut, and a softmax
+ * weight is rounded to bf16 (half a step, 2^-8) against the largest score since
+ * the cut, or one up to 8 powers of two below it; sums are float32.
  * Supported: head_dim 64/128, num_q_heads / num_kv_heads <= 16, batch <= 4096.
  * A step of more sequences takes a call for every 4096, with cu_q, kv_lens and
  * the page table from the call's first sequence on and q, out, lse and

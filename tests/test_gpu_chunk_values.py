@@ -133,3 +133,23 @@ def test_a_part_of_no_weight_still_shows_what_is_not_finite(d, new, Hq, falls):
     c.write(0, k, c.v[0])
     out, lse = call()
     assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("L,new", [(1, 1), (100, 7), (20000, 3), (5000, 80)])
+def test_rows_whose_scores_are_all_minus_infinity(L, new):
+    """Zero, with a log-sum-exp of -infinity, as rows that attend nothing.  (The
+    heads whose queries are zero in that dimension have NaN scores.)"""
+    from self_speculative_sparse_vg_gb300 import vg
+    c = Cache([L], 1, 64, seed=35)
+    g = torch.Generator().manual_seed(6)
+    q = torch.randn(new, 4, 64, generator=g).bfloat16()
+    q[:, :, 9] = 0                       # the dimension that is -infinity in every key
+    _, want, want_lse = check_chunk(c, [new], 4, q=q)
+    q[:, 1, 9] = 1.0
+    k = c.k[0].clone()
+    k[:, 0, 9] = -INF
+    c.write(0, k, c.v[0])
+    out, lse = torch.full_like(want, 3.0), torch.full_like(want_lse, 3.0)
+    vg.chunk_attention(c.gpu(), q.cuda(), i32([0, new]), i32([L]), 0.125, out, lse=lse)
+    assert (out[:, 1] == 0).all() and torch.isneginf(lse[:, 1]).all()
+    assert out[:, [0, 2, 3]].isnan().all()
