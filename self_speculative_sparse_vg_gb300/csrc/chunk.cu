@@ -1257,7 +1257,7 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   // Up to 32 rows: a CTA per row, whose units have many parts (one token of 8
-  // heads over 2K: 10.0 us for the call, 12.7 with the other merge; eight tokens
+  // heads over 2K: 10.4 us for the call, 12.7 with the other merge; eight tokens
   // over 16K - 64K: the same).  More rows mean fewer parts, and a CTA takes 32.
   if (rows <= 32) {
     cfg.gridDim = dim3(pl.grid, (int)rows);

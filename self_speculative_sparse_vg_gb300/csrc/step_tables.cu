@@ -13,7 +13,7 @@
 // neighbouring requests, so one pass of warp shuffles makes each sum.  Then the
 // tokens' positions and slots are written, a token per thread; past 1024 tokens
 // the CTA is the first of a cluster that shares that part: the others find the
-// rows' requests and positions while it works on the tables (114K tokens 8.2 us,
+// rows' requests and positions while it works on the tables (114K tokens 8.0 us,
 // 9.2 when they wait first).  When the cluster was chosen, 4096 tokens took 5.4
 // us, 6.5 with one CTA alone, and 4.7 - 5.6 with a second kernel for the tokens,
 // which cost 2 us more of host time.  A few requests and tokens get a CTA of 128
@@ -23,7 +23,7 @@
 // Pages that move are loads with stores that wait for them, so the CTA shares the
 // longer runs: 7 prompts of 8K - 16K tokens 11 us (46 with a request's run left to
 // one warp), 8 requests that give 20K pages back 17 (52), 12 prompts beside 288
-// other requests 14 (19).
+// other requests 13 (19); perf/more_cases.py measures these.
 #include <limits.h>
 
 #include "vg_device.cuh"
