@@ -35,8 +35,8 @@
  *   - Workspaces: sized by the matching *_workspace_bytes() call for the same
  *     arguments on the same device (0 = none needed, the pointer may be
  *     NULL).  Calls that share a workspace must not overlap in time.  The
- *     verify and select workspaces need no initialisation: everything in
- *     them is written before it is read.  The sparse draft needs none.
+ *     verify, select and chunk workspaces need no initialisation: everything
+ *     in them is written before it is read.  The sparse draft needs none.
  */
 #ifndef VG_H_
 #define VG_H_
