@@ -82,3 +82,17 @@ def test_the_build_goes_on_without_the_binding(monkeypatch, tmp_path):
     with pytest.warns(UserWarning, match="Python.h is missing"):
         assert build.build() == str(lib)
     assert lib.exists() and not binding.exists()
+
+
+def test_the_build_command_without_the_binding(monkeypatch):
+    """build() of the entry module, where the binding is left out, ends well."""
+    ensure_lib()
+    import __graft_entry__ as entry
+    from self_speculative_sparse_vg_gb300 import build
+    monkeypatch.setattr(build, "build", lambda: build.LIB)
+    monkeypatch.setattr(build, "binding_lacks", lambda: "Python.h")
+    monkeypatch.setitem(sys.modules, "self_speculative_sparse_vg_gb300.vg_binding", None)   # an import raises
+    entry.build()
+    monkeypatch.setattr(build, "binding_lacks", lambda: "")
+    with pytest.raises(ImportError):
+        entry.build()
