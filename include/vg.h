@@ -12,6 +12,11 @@
  *   vg_step_tables             block tables and slot maps from lengths;
  *   vg_rope_append             rotary positions, new K/V rows to their slots;
  *   vg_chunk_attention         attention of a chunk of new tokens.
+ * Decoding with beams, and to the states of an encoder, adds:
+ *   vg_cross_attention         attention to states of another length;
+ *   vg_beam_select             the best continuations over beams and vocabulary;
+ *   vg_beam_tables             block tables of beams that continue other beams;
+ *   vg_copy_pages              the copies of pages that this leaves.
  *
  * Sources (page title, section):
  *   Vegas: Self-Speculative Decoding with Verification-Guided Sparse
@@ -35,8 +40,9 @@
  *   - Workspaces: sized by the matching *_workspace_bytes() call for the same
  *     arguments on the same device (0 = none needed, the pointer may be
  *     NULL).  Calls that share a workspace must not overlap in time.  The
- *     verify, select and chunk workspaces need no initialisation: everything
- *     in them is written before it is read.  The sparse draft needs none.
+ *     verify, select, chunk, cross and beam workspaces need no
+ *     initialisation: everything in them is written before it is read.  The
+ *     sparse draft needs none.
  */
 #ifndef VG_H_
 #define VG_H_
@@ -98,8 +104,12 @@ enum {
   VG_DEVERR_COUNT = 4,    /* selected count outside [0, cap]                  */
   VG_DEVERR_TIMEOUT = 8,  /* a pipeline wait outlasted its bound (see below)   */
   VG_DEVERR_LENGTH = 16,  /* a device length exceeds its host-side bound      */
-  VG_DEVERR_POOL = 32     /* the free list does not cover the pages asked for */
+  VG_DEVERR_POOL = 32,    /* the free list does not cover the pages asked for */
+  VG_DEVERR_VALUE = 64    /* a score or a row of logits holds a NaN or +inf    */
 };
+
+/* Element types of the calls that take several. */
+enum { VG_TYPE_FP32 = 0, VG_TYPE_BF16 = 1, VG_TYPE_FP16 = 2 };
 
 /* Paged KV cache.  Pages hold 16 consecutive positions of one sequence.
  *   k_pages, v_pages: bf16 [num_pages][num_kv_heads][page_size][head_dim];
@@ -480,6 +490,143 @@ vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, int64_t q_str
                              int num_tokens, int num_q_heads, float softmax_scale, void* out,
                              int64_t out_stride, float* lse, void* workspace,
                              size_t workspace_bytes, int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Cross attention: rows of new tokens to the states of an encoder, which have
+ * a length of their own; every row of a sequence attends the same states (no
+ * causal order).  The beams of a request, or the rows of a verify block, are
+ * rows of one sequence and share its states' reads.
+ *   q, out       [num_tokens][num_q_heads][head_dim], q_stride and out_stride
+ *                elements between tokens (multiples of 8), bases 16-byte
+ *                aligned; out must not overlap q.
+ *   k, v         [num_states][num_kv_heads][head_dim], k_stride and v_stride
+ *                elements between states (multiples of 8), bases 16-byte
+ *                aligned: slices of one projection will do.
+ *   type         VG_TYPE_BF16 or VG_TYPE_FP16, of q, k, v and out.
+ *   cu_q         int32 [batch + 1]: token rows [cu_q[e], cu_q[e + 1]) belong to
+ *                sequence e.  Rows outside every sequence are not read or written.
+ *   state_starts, state_lens  int32 [batch]: sequence e attends the states
+ *                [start, start + len) (packed, or in slots of a fixed size;
+ *                sequences may share states).
+ *   mask         NULL, or uint8 [num_states]: states whose byte is 0 are not
+ *                attended by any row.
+ *   softmax_scale  > 0.
+ *   lse          NULL, or float32 [num_tokens][num_q_heads]: natural log of the
+ *                row's sum of exponentials, -inf for a row that attends nothing.
+ *   workspace    vg_cross_workspace_bytes() bytes, 16-byte aligned.
+ * A row that attends nothing (no states, all masked, or scores that are all
+ * -infinity) is zero.  What lies in states that a row does not attend does not
+ * reach it, whatever it holds.  A sequence whose rows or states are not a range
+ * inside [0, num_tokens) or [0, num_states) is flagged VG_DEVERR_LENGTH and its
+ * rows are left as they were.
+ * Results are the same on every run; what else is in the batch changes them by
+ * rounding alone: it decides where a long sequence is cut, and a softmax weight
+ * is rounded to the call's type (half a step) against the largest score since
+ * the cut, or one up to 8 powers of two below it; sums are float32.
+ * Supported: head_dim 64/128, num_q_heads / num_kv_heads <= 128, batch <= 4096,
+ * num_states <= 2^30.
+ * ------------------------------------------------------------------------- */
+size_t vg_cross_workspace_bytes(int batch, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim);
+
+vg_status vg_cross_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, int type, const int32_t* cu_q,
+                             const int32_t* state_starts, const int32_t* state_lens,
+                             const uint8_t* mask, int batch, int num_tokens, int num_states,
+                             int num_q_heads, int num_kv_heads, int head_dim, float softmax_scale,
+                             void* out, int64_t out_stride, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam search: the num_out best continuations of each request.
+ *   logits       [batch * beams][vocab] of VG_TYPE_FP32, _BF16 or _FP16, rows
+ *                logits_stride elements apart (any, also of odd vocabularies);
+ *                -infinity bans a token.
+ *   scores       float32 [batch][beams]: log-probability of each beam; -infinity
+ *                for a beam that does not live (at a request's first step, all
+ *                beams but one).
+ *   ended        NULL, or uint8 [batch][beams]: beams that have ended (not 0).
+ * A living beam w offers its tokens t at scores[w] + logits[w][t] - log sum_u
+ * exp logits[w][u]; an ended one offers end_token at its score; their logits, and
+ * those of beams at -infinity, are not read.  A candidate at -infinity is none.
+ * The best of a request are written in order, ties to the lower beam, then the
+ * lower token:
+ *   out_scores   float32 [batch][num_out], out_tokens, out_parents int32 (the
+ *                beam, within the request); -infinity, -1 and -1 where there are
+ *                no more candidates.
+ *   out_ended    NULL, or uint8 [batch][num_out]: 1 where the token is end_token
+ *                or the parent had ended.
+ * out_scores may be scores and out_ended ended where num_out = beams; else
+ * outputs must not overlap inputs.
+ *   workspace    vg_beam_select_workspace_bytes() bytes, 16-byte aligned.
+ * Scores are compared to about 2^-23 of the row's sum of exponentials, and rounded
+ * to float32 once; candidates of one beam compare as their logits do.  A beam
+ * with a NaN or +infinity as its score or among its logits is flagged
+ * VG_DEVERR_VALUE and offers nothing.  Two kernels.
+ * Supported: beams <= 32, num_out <= 64, rows of at most 3 MB.
+ * ------------------------------------------------------------------------- */
+size_t vg_beam_select_workspace_bytes(int batch, int beams, int vocab, int type, int num_out);
+
+vg_status vg_beam_select(const void* logits, int type, int64_t logits_stride, const float* scores,
+                         const uint8_t* ended, int end_token, int batch, int beams, int vocab,
+                         int num_out, float* out_scores, int32_t* out_tokens, int32_t* out_parents,
+                         uint8_t* out_ended, void* workspace, size_t workspace_bytes,
+                         int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Block tables of beams that continue other beams: row j of a request takes the
+ * pages and the length of its row parents[j].  Once per step.
+ *   parents      int32 [batch][beams]: a row of the same request, or -1: the row
+ *                is emptied (a finished request empties all its rows).
+ *   lens         int32 [batch * beams], in and out: positions that each row holds
+ *                in the cache.
+ *   page_table   int32 [batch * beams][max_pages_per_seq], owned int32
+ *                [batch * beams], free_pages int32 [free_capacity], free_count
+ *                int32 [1], in and out, as for vg_step_tables.
+ * The rows of a request share full pages: the same page stands in several rows,
+ * at the same column.  A new request is one row's prompt whose row all others
+ * take (parents 0).  A row's partly filled last page is its own: vg_step_tables
+ * then extends every row by pages of its own.  (That call must not shrink rows
+ * that share the pages given back.)  In this order:
+ *   1. pages that a request's rows held and no new row holds are pushed on the
+ *      free list (requests, then columns, then rows ascending), once each, also
+ *      those past a row's length;
+ *   2. of the rows of a request that take the same partly filled last page the
+ *      first keeps it; each other one pops a page from the list's end (rows
+ *      ascending) and is to get a copy.  A row for which there is none left is
+ *      emptied and flagged VG_DEVERR_POOL.
+ * Table entries that a row held and holds no more become -1.  Written:
+ *   copies       int32 [batch * beams][3]: page to copy from, page to copy to and
+ *                the positions held, for vg_copy_pages; -1, -1, 0 where there is
+ *                nothing to copy.
+ * A request with a parent that is none is flagged VG_DEVERR_INDEX, one with a
+ * negative length, or with fewer owned pages than its length needs or more than
+ * max_pages_per_seq, VG_DEVERR_LENGTH; it stays as it was.  A list whose count is
+ * out of range, or that the returned pages do not fit, is flagged VG_DEVERR_POOL and
+ * nothing changes.  A returned page id outside [0, num_pages) is flagged
+ * VG_DEVERR_PAGE and dropped; one popped from the list too (the row's last page is
+ * then -1).  Arrays must not overlap.  One kernel.
+ * Supported: beams <= 32, batch * beams <= 4096.
+ * ------------------------------------------------------------------------- */
+vg_status vg_beam_tables(const int32_t* parents, int batch, int beams, int32_t* lens,
+                         int32_t* page_table, int max_pages_per_seq, int num_pages, int32_t* owned,
+                         int32_t* free_pages, int free_capacity, int32_t* free_count,
+                         int32_t* copies, int32_t* error_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Copies of the first positions of pages, in every layer's pools.
+ *   k_pages, v_pages  HOST arrays of num_layers pools each (device pointers, bf16
+ *                [num_pages][num_kv_heads][16][head_dim], 16-byte aligned).
+ *   copies       int32 [num_copies][3]: page to copy from, page to copy to,
+ *                positions (0: nothing to do; at most 16).  No page is copied to
+ *                twice, or to and from.
+ * Positions past those copied stay as they were.  A page id outside
+ * [0, num_pages), or a number of positions outside [0, 16], is flagged
+ * VG_DEVERR_PAGE and skipped.  One kernel for up to 64 layers.
+ * ------------------------------------------------------------------------- */
+vg_status vg_copy_pages(void* const* k_pages, void* const* v_pages, int num_layers, int num_pages,
+                        int num_kv_heads, int head_dim, const int32_t* copies, int num_copies,
+                        int32_t* error_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Failure detection: the bound on pipeline waits (host).

@@ -27,7 +27,7 @@ LIB = os.path.join(PKG, "libvg.so")
 BINDING = os.path.join(PKG, "vg_binding.so")
 CXX = os.environ.get("CXX", "g++")
 SOURCES = ["vg_host.cu", "verify.cu", "select.cu", "sparse_draft.cu", "step_tables.cu",
-           "rope_append.cu", "chunk.cu"]
+           "rope_append.cu", "chunk.cu", "cross.cu", "beam_select.cu", "beam_tables.cu", "copy_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

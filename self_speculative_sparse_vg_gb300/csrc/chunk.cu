@@ -43,13 +43,14 @@
 #include <limits.h>
 #include <math.h>
 
+#include "units.cuh"
 #include "vg_device.cuh"
 #include "vg_host.h"
 
 namespace vg {
 namespace {
 
-constexpr int kTile = 128;             // positions of a KV tile, rows of a row tile
+constexpr int kTile = kUnitTile;       // positions of a KV tile, rows of a row tile
 constexpr int kPagesPerTile = kTile / kPageSize;
 constexpr int kChunkThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax; two checkers)
@@ -69,19 +70,13 @@ struct ChunkParams {
   float* lse;
   float* part_o;      // [grid][2][HD / 4][rows][4]
   float* part_ml;     // [grid][2][rows][2]
-  struct MergeUnit* merge;  // [grid]
+  MergeUnit* merge;   // [grid]
   int32_t* error_flag;
   int64_t out_stride;
   uint64_t wait_ns;    // a longer wait is reported
   int polls;           // polls of a wait between two looks at the timer
   float scale_log2;
   int batch, num_tokens, num_q_heads, num_kv_heads, group, num_pages, width, rows;
-};
-
-// A unit that several CTAs share, written by the CTA where it begins.
-struct MergeUnit {
-  int parts;          // 0: none
-  int tok0, ntok, h;
 };
 
 // A unit of work as the CTA's roles see it.
@@ -191,56 +186,6 @@ __device__ __forceinline__ bool checked_tile(int pos0, int kt) {
   return kt * kTile + kTile - 1 > pos0;
 }
 
-// Waits for the phase with the given parity, as mbar_wait_checked does, in less
-// code.  Past the report bound the wait flags VG_DEVERR_TIMEOUT, past
-// kWaitLimitNs it gives up.  (The timer is slow to read: with a look at it after
-// every poll the whole kernel was 5 % slower; polls is 1 under a report bound
-// shorter than the limit, and the polls then do not sleep.)
-__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
-  uint64_t t0 = 0;
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < p.polls; ++i)
-      if (p.polls > 1 ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)) return true;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > p.wait_ns) flag_error(p.error_flag, VG_DEVERR_TIMEOUT);
-    if (now - t0 > kWaitLimitNs) return false;
-  }
-}
-// The same for a whole warp, which stays together: mostly one look and one vote
-// (a loop that the lanes leave one by one costs some 50 cycles more, and the
-// tensor-core warp waits six times for a tile).
-__device__ __forceinline__ bool chunk_wait_warp(uint64_t* bar, uint32_t parity, const ChunkParams& p) {
-  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, chunk_wait(bar, parity, p));
-}
-
-// 64 consecutive columns of this warp's lanes, load and wait in one statement
-// (no register is read before it has landed).
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// 32-byte store (a whole sector of a row per lane).
-__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // Non-zero when one of two packed bf16 is an infinity or a NaN (an exponent of
 // ones: adding the exponent's lowest bit carries out of it).
 __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
@@ -286,7 +231,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
   uint32_t sc = 0, oc = 0, xc = 0;
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
-    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
+    if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
     const Unit un = units[slot];
     if (un.kt0 == un.kt1) return;
     const int tok = un.two ? wg * tt + tok_r : tok_r;       // token within the unit
@@ -298,7 +243,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
     const int end = un.two && wg == 0 ? min(un.kt1, un.n0) : un.kt1;
     float m_used = -INFINITY, lsum = 0.f;
     for (int kt = first; kt < end; kt += step) {
-      if (!chunk_wait_warp(&bars.sfull[wg], sc & 1, p)) return;
+      if (!wait_phase_warp(&bars.sfull[wg], sc & 1, p)) return;
       ++sc;
       tc_fence_after();
       if (rows) {
@@ -381,7 +326,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
     // -------- epilogue
     const bool has = end > first;
     if (has) {
-      if (!chunk_wait_warp(&bars.ofull[wg], oc & 1, p)) return;
+      if (!wait_phase_warp(&bars.ofull[wg], oc & 1, p)) return;
       ++oc;
       tc_fence_after();
     }
@@ -394,7 +339,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.xfull);
       } else {
-        if (!chunk_wait_warp(bars.xfull, xc & 1, p)) return;
+        if (!wait_phase_warp(bars.xfull, xc & 1, p)) return;
         tc_fence_after();
         const float2 o = ml_s[r];
         m_all = fmaxf(m_used, o.x);
@@ -482,7 +427,7 @@ __device__ __forceinline__ void softmax_role(const ChunkParams& p, const ChunkBa
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.xdone);
-      } else if (!chunk_wait_warp(bars.xdone, xc & 1, p)) {
+      } else if (!wait_phase_warp(bars.xdone, xc & 1, p)) {
         return;
       }
       ++xc;
@@ -539,7 +484,7 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   // next K's and V's ring stage and parity; entries are K(0), V(0), K(1) ...
   uint32_t sk = 0, pk = 0, sv = 1, pv = 0;
   auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return chunk_wait_warp(bar, parity, p); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_phase_warp(bar, parity, p); };
   auto next = [](uint32_t& st, uint32_t& par) {
     st += 2;
     if (st >= NST) {
@@ -551,20 +496,20 @@ __device__ __forceinline__ bool mma_role(const ChunkParams& p, const ChunkBars& 
   auto pv_product = [&](int wg, uint32_t st, bool accumulate) {
     const uint32_t par = (pc >> wg) & 1;
     pc ^= 1u << wg;
-    if (!chunk_wait_warp(&bars.pfull[wg], par, p)) return false;
+    if (!wait_phase_warp(&bars.pfull[wg], par, p)) return false;
     tc_fence_after();
     mma.pv(wg, st, accumulate);
     return true;
   };
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
-    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
+    if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
     const int kt0 = same(units[slot].kt0), kt1 = same(units[slot].kt1), n0 = same(units[slot].n0);
     const int two = same(units[slot].two);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.uempty[slot]);
     if (kt0 == kt1) return true;
-    if (!chunk_wait_warp(bars.qfull, u & 1, p)) return false;
+    if (!wait_phase_warp(bars.qfull, u & 1, p)) return false;
     const int n = kt1 - kt0;
     if (two) {
       const int e0 = min(kt1, n0) - kt0;  // tiles of the first row tile
@@ -641,7 +586,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
   uint32_t tiles = 0, landed = 0;
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
-    if (!chunk_wait_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
+    if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
     const Unit un = units[slot];
     if (un.kt0 == un.kt1) return;
     uint16_t* notes = notes_s + slot * 3 * HD;
@@ -651,7 +596,7 @@ __device__ __forceinline__ void check_role(const ChunkParams& p, const ChunkBars
     const int from = max(un.kt0, un.pos0 < 0 ? 0 : (un.pos0 + 1) / kTile);
     for (int kt = from; kt < un.kt1; ++kt) {
       const uint32_t st = (2 * (tiles + kt - un.kt0) + 1) % NST;
-      if (!chunk_wait_warp(&bars.landed[st], (landed >> st) & 1, p)) return;
+      if (!wait_phase_warp(&bars.landed[st], (landed >> st) & 1, p)) return;
       landed ^= 1u << st;
       uint8_t* tile = ring + st * Lay::kStageBytes;
       // rows past the length are zeroed, those past the first row's position
@@ -709,20 +654,6 @@ struct Share {
   int b, h, rt, kt0;
   int q0, n, len;     // the first unit's sequence
 };
-
-// a / b of non-negative numbers that mostly fit 32 bits.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-__device__ __forceinline__ long long warp_inclusive_sum(long long v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long w = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += w;
-  }
-  return v;
-}
 
 __device__ __forceinline__ int row_tiles(int n, int tu) {
   return (int)(((unsigned)n + (unsigned)tu - 1u) / (unsigned)tu);
@@ -866,7 +797,7 @@ __device__ __forceinline__ void producer_role(const ChunkParams& p, const ChunkB
   MergeUnit cut = {};
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     int go = 1;
-    if (lane == 0) go = chunk_wait(bar, parity, p);
+    if (lane == 0) go = wait_phase(bar, parity, p);
     return __shfl_sync(0xffffffffu, go, 0) != 0;
   };
   while (live) {
@@ -1078,151 +1009,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
 }
 
-// Merge of the units that several CTAs share, weights 2^(m - max m) of the
-// parts, which sit in slot 1 of the CTA where the unit begins and in slot 0 of
-// the following ones.  A CTA takes 32 rows, a lane each (the parts' layout);
-// a warp takes an eighth of the dimensions, and the rows leave through shared
-// memory in whole lines.  No part is left out for its weight: one that a row does
-// not attend is zero, and a NaN or an infinity of one whose weight underflows
-// still has to show (as NaN), as it does where no cut falls.
-constexpr int kMergeWarps = 8, kMergeRows = 32;
-
-template <int HD>
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int NP = HD / 4 / kMergeWarps;   // 4-dim pieces of a warp
-  constexpr int kRow = HD / 2 + 4;           // words of a staged row (spread over the banks)
-  __shared__ __align__(16) uint32_t out_s[kMergeRows][kRow];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.y * kMergeRows, row = row0 + lane;  // row of the partial
-  const MergeUnit mu = p.merge[c];
-  const int g = p.group, tt = kTile / g;
-  const int rows = mu.ntok > tt ? kTile + (mu.ntok - tt) * g : mu.ntok * g;
-  if (mu.parts == 0 || row0 >= rows) return;
-  const int tr = row % kTile, tok = row / kTile * tt + tr / g;
-  const bool mine = tr < tt * g && tok < mu.ntok;  // else no token's row
-  auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)(warp * NP) * p.rows + row;
-  float m = -INFINITY, l = 0.f, acc[NP][4];
-#pragma unroll
-  for (int k = 0; k < NP; ++k)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-  if (mine) {
-#pragma unroll 4
-    for (int i = 0; i < mu.parts; ++i) {
-      const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
-      float4 v[NP];
-#pragma unroll
-      for (int k = 0; k < NP; ++k) v[k] = __ldcg(po + (slot(i) * (HD / 4) + k) * p.rows);
-      const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-      const float f = ex2(m - ref), w = ex2(x.x - ref);
-      l = fmaf(l, f, w * x.y);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const float y[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(w, y[e], acc[k][e] * f);
-      }
-      m = mn;
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
-#pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    out_s[lane][(warp * NP + k) * 2] = pack_bf16(acc[k][0] * inv, acc[k][1] * inv);
-    out_s[lane][(warp * NP + k) * 2 + 1] = pack_bf16(acc[k][2] * inv, acc[k][3] * inv);
-  }
-  if (mine && warp == 0 && p.lse)
-    p.lse[(int64_t)(mu.tok0 + tok) * p.num_q_heads + mu.h * g + tr % g] =
-        (m + log2f(l)) * 0.6931471805599453f;
-  __syncthreads();
-  constexpr int kPieces = HD / 8;  // 16-byte pieces of a row
-  for (int i = threadIdx.x; i < kMergeRows * kPieces; i += kMergeWarps * 32) {
-    const int r = row0 + i / kPieces, rr = r % kTile, tk = r / kTile * tt + rr / g;
-    if (rr >= tt * g || tk >= mu.ntok) continue;
-    *reinterpret_cast<uint4*>(p.out + (int64_t)(mu.tok0 + tk) * p.out_stride +
-                              (int64_t)(mu.h * g + rr % g) * HD + (i % kPieces) * 8) =
-        *reinterpret_cast<const uint4*>(&out_s[i / kPieces][(i % kPieces) * 4]);
-  }
-}
-
-// The same for calls of few rows (single tokens), whose units have many parts:
-// a CTA per row, its warps over the parts, every load in flight at once.
-template <int HD>
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_row_kernel(const ChunkParams p) {
-  constexpr int E = HD / 32;
-  __shared__ float acc_s[kMergeWarps][HD], l_s[kMergeWarps], m_s[kMergeWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const MergeUnit mu = p.merge[c];
-  const int g = p.group;
-  if (mu.parts == 0 || row >= mu.ntok * g) return;
-  auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float m = -INFINITY, l = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < mu.parts; i += kMergeWarps) {
-    const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
-    const float* src = p.part_o + ((slot(i) * (HD / 4) + lane * E / 4) * p.rows + row) * 4 + lane * E % 4;
-    float v[E];
-    if (E == 4) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-      v[0] = y.x, v[1] = y.y, v[E - 2] = y.z, v[E - 1] = y.w;
-    } else {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-      v[0] = y.x, v[1] = y.y;
-    }
-    const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-    const float f = ex2(m - ref), w = ex2(x.x - ref);
-    // a part without weight is passed over if all of it is finite (one token of
-    // 8 heads over 2K: 9.9 us for the call, 10.4 when none is)
-    bool finite = fabsf(x.y) < INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) finite &= fabsf(v[e]) < INFINITY;
-    l *= f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-    if (w != 0.f || !finite) {
-      l += w * x.y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
-    }
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    l_s[warp] = l;
-    m_s[warp] = m;
-  }
-  __syncthreads();
-  if (threadIdx.x >= HD / 2) return;
-  float m_all = m_s[0];
-#pragma unroll
-  for (int i = 1; i < kMergeWarps; ++i) m_all = fmaxf(m_all, m_s[i]);
-  const float ref = safe_ref(m_all);
-  float l_all = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) {
-    const float w = ex2(m_s[i] - ref);
-    l_all += w * l_s[i];
-    o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
-    o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
-  }
-  const float inv = l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN;
-  const int t = mu.tok0 + row / g, qh = mu.h * g + row % g;
-  *reinterpret_cast<uint32_t*>(p.out + t * p.out_stride + (int64_t)qh * HD + 2 * threadIdx.x) =
-      pack_bf16(o0 * inv, o1 * inv);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
-}
-
 struct ChunkPlan {
   int grid, rows;
   size_t off_ml, off_merge, bytes;
@@ -1263,18 +1049,9 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_kernel<HD>, tq, tk, tv, p);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)p.num_tokens * p.group;  // no unit has more
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.dynamicSmemBytes = 0;
-  // Up to 32 rows: a CTA per row, whose units have many parts (one token of 8
-  // heads over 2K: 9.9 us for the call, 12.7 with the other merge; eight tokens
-  // over 16K - 64K: the same).  More rows mean fewer parts, and a CTA takes 32.
-  if (rows <= 32) {
-    cfg.gridDim = dim3(pl.grid, (int)rows);
-    return cudaLaunchKernelEx(&cfg, chunk_merge_row_kernel<HD>, p);
-  }
-  cfg.gridDim = dim3(pl.grid, ceil_div(pl.rows == kTile ? (int)rows : pl.rows, kMergeRows));
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<HD>, p);
+  const MergeParams m = {reinterpret_cast<uint16_t*>(p.out), p.lse,          p.part_o,  p.part_ml, p.merge,
+                         p.out_stride,                       p.num_q_heads, p.group,   p.rows};
+  return launch_unit_merge<HD, false>(cfg, pl.grid, (long long)p.num_tokens * p.group, m);
 }
 
 }  // namespace

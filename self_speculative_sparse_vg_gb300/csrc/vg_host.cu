@@ -116,6 +116,19 @@ bool page_chunk_tensor_map(const void* base, int num_pages, int num_kv_heads, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool head_tile_tensor_map(const void* base, int num_tokens, int num_heads, int head_dim,
+                          int64_t token_stride, int box_tokens, CUtensorMap* out) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)num_tokens, (cuuint64_t)head_dim / 64, (cuuint64_t)num_heads};
+  cuuint64_t strides[3] = {(cuuint64_t)token_stride * 2, 128, (cuuint64_t)head_dim * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, (cuuint32_t)head_dim / 64, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 vg_status check_paged_kv(const vg_paged_kv* kv) {
   if (!kv || !kv->k_pages || !kv->v_pages || !kv->page_table) return VG_ERR_INVALID_ARGUMENT;
   if (kv->num_pages <= 0 || kv->max_pages_per_seq <= 0 || kv->num_kv_heads <= 0)

@@ -43,6 +43,14 @@ bool token_rows_tensor_map(const void* base, int num_tokens, int num_heads, int 
 bool page_chunk_tensor_map(const void* base, int num_pages, int num_kv_heads, int head_dim,
                            CUtensorMap* out);
 
+// 4-D tiled TMA descriptor over token rows [num_tokens][num_heads][head_dim] of
+// 16-bit values with token_stride elements between tokens, viewed as
+// [num_heads][head_dim / 64][num_tokens][64], so that one box of 64 x box_tokens
+// x head_dim / 64 x 1 is a tile of one head, 64-dim block by block, with the
+// 128-byte swizzle (tokens past the end read zeros).  Made anew on every call.
+bool head_tile_tensor_map(const void* base, int num_tokens, int num_heads, int head_dim,
+                          int64_t token_stride, int box_tokens, CUtensorMap* out);
+
 // Basic checks of a vg_paged_kv; VG_OK or an error status.
 vg_status check_paged_kv(const vg_paged_kv* kv);
 

@@ -29,6 +29,9 @@ DEVERR_COUNT = 4
 DEVERR_TIMEOUT = 8
 DEVERR_LENGTH = 16
 DEVERR_POOL = 32
+DEVERR_VALUE = 64
+
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 EXPORTED = (
     "vg_verify_workspace_bytes", "vg_verify_attention",
@@ -39,6 +42,8 @@ EXPORTED = (
     "vg_sparse_verify_workspace_bytes", "vg_sparse_verify_attention",
     "vg_set_wait_limit_ns",
     "vg_step_tables", "vg_rope_append", "vg_chunk_workspace_bytes", "vg_chunk_attention",
+    "vg_cross_workspace_bytes", "vg_cross_attention",
+    "vg_beam_select_workspace_bytes", "vg_beam_select", "vg_beam_tables", "vg_copy_pages",
 )
 
 
@@ -89,6 +94,14 @@ def _load():
         "vg_chunk_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
         "vg_chunk_attention": (i32, [kvp, vp, i64, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp, sz,
                                      vp, vp]),
+        "vg_cross_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "vg_cross_attention": (i32, [vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
+                                     i32, i32, i32, f32, vp, i64, vp, vp, sz, vp, vp]),
+        "vg_beam_select_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "vg_beam_select": (i32, [vp, i32, i64, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp,
+                                 sz, vp, vp]),
+        "vg_beam_tables": (i32, [vp, i32, i32, vp, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp]),
+        "vg_copy_pages": (i32, [vp, vp, i32, i32, i32, i32, vp, i32, vp, vp]),
         "vg_set_wait_limit_ns": (i32, [ctypes.c_uint64]),
         "vg_status_string": (ctypes.c_char_p, [i32]),
         "vg_version": (ctypes.c_char_p, []),
@@ -401,6 +414,85 @@ def chunk_attention(kv: PagedKV, q, cu_q, kv_lens, softmax_scale, out, lse=None,
     if s:
         raise VGError("vg_chunk_attention", s)
     return out
+
+
+# --------------------------------------------------- beams and encoder states
+# Checked and called natively, like those that fill the cache.
+def cross_workspace_bytes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(_lib.vg_cross_workspace_bytes(batch, num_tokens, num_q_heads, num_kv_heads, head_dim))
+
+
+def cross_attention(q, k, v, cu_q, state_starts, state_lens, softmax_scale, out, mask=None, lse=None,
+                    workspace=None, error_flag=None, stream=None):
+    """vg_cross_attention: packed rows of new tokens to the states of their
+    sequences' encoders.  q and out [T][Hq][d], k and v [S][Hkv][d], bf16 or
+    fp16, slices of a projection included; cu_q int32 [E + 1], state_starts and
+    state_lens int32 [E]; mask (optional) bool or uint8 [S], false: not attended;
+    lse (optional) float32 [T][Hq].  The beams of a request are rows of one
+    sequence.  workspace: uint8 tensor of cross_workspace_bytes() (allocated here
+    when not given)."""
+    if workspace is None:
+        with torch.cuda.device(q.device):   # its size goes by the device
+            n = cross_workspace_bytes(state_lens.numel(), *q.shape[:2], k.shape[1], q.shape[2])
+            with _allocating_for(stream):
+                workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    s = _binding.cross_attention(q, k, v, cu_q, state_starts, state_lens, softmax_scale, out, mask, lse,
+                                 workspace, error_flag, None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_cross_attention", s)
+    return out
+
+
+def beam_select_workspace_bytes(batch, beams, vocab, dtype, num_out) -> int:
+    """dtype: torch.float32, bfloat16 or float16, of the logits."""
+    return int(_lib.vg_beam_select_workspace_bytes(batch, beams, vocab, TYPES.get(dtype, -1), num_out))
+
+
+def beam_select(logits, scores, out_scores, out_tokens, out_parents, ended=None, end_token=-1, out_ended=None,
+                workspace=None, error_flag=None, stream=None):
+    """vg_beam_select: the best continuations of each request, in order.
+
+    logits [B * W][V] float32, bfloat16 or float16 (a slice of wider rows will
+    do), scores float32 [B][W], ended (optional) bool or uint8 [B][W]; written:
+    out_scores float32, out_tokens and out_parents int32, out_ended (optional)
+    bool or uint8, all [B][num_out].  workspace: uint8 tensor of
+    beam_select_workspace_bytes() (allocated here when not given)."""
+    if workspace is None:
+        with torch.cuda.device(logits.device):   # its size goes by the device
+            n = beam_select_workspace_bytes(*scores.shape, logits.shape[1], logits.dtype, out_scores.shape[1])
+            with _allocating_for(stream):
+                workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=logits.device)
+    s = _binding.beam_select(logits, scores, ended, end_token, out_scores, out_tokens, out_parents, out_ended,
+                             workspace, error_flag, None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_beam_select", s)
+    return out_scores, out_tokens, out_parents
+
+
+def beam_tables(page_table, num_pages, parents, lens, owned, free_pages, free_count, copies, error_flag=None,
+                stream=None):
+    """vg_beam_tables: row j of a request takes the pages and length of its row
+    parents[j] (-1: the row is emptied).
+
+    parents int32 [B][W]; page_table int32 [B * W][max_pages], lens and owned
+    int32 [B * W], free_pages and free_count as for step_tables, all updated in
+    place.  Written: copies int32 [B * W][3], for copy_pages."""
+    s = _binding.beam_tables(page_table, num_pages, parents, lens, owned, free_pages, free_count, copies,
+                             error_flag, None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_beam_tables", s)
+    return copies
+
+
+def copy_pages(kv, copies, error_flag=None, stream=None):
+    """vg_copy_pages: for each row (from, to, positions) of copies, int32
+    [n][3], the first positions of a page to another, in the pools of a PagedKV
+    or of a list of them (one per layer, of one shape)."""
+    layers = [kv] if isinstance(kv, PagedKV) else kv
+    s = _binding.copy_pages([x.k_pages for x in layers], [x.v_pages for x in layers], copies, error_flag,
+                            None if stream is None else stream.cuda_stream)
+    if s:
+        raise VGError("vg_copy_pages", s)
 
 
 def zero_workspace(nbytes: int, device) -> torch.Tensor:
