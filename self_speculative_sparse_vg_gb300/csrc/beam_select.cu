@@ -37,13 +37,12 @@ namespace {
 
 constexpr int kSliceThreads = 256;
 constexpr int kSliceWarps = kSliceThreads / 32;
-constexpr int kMaxSlices = 32;           // of a row: a lane each in the merge
+constexpr int kMaxSlices = 96;           // of a row
 constexpr int kMaxBeams = 32;
 constexpr int kMaxOut = 64;
-constexpr int kListed = 1024;            // candidates that a slice has room for
-constexpr int kSliceBytes = 32 * 1024;   // of a slice, longer only where a row has more than 32 of them
+constexpr int kListed = 512;             // candidates that a slice, or a request, has room for
+constexpr int kSliceBytes = 32 * 1024;   // of a slice, at most
 constexpr int kLeastSliceBytes = 4 * 1024;
-constexpr int kMostSliceBytes = 96 * 1024;
 
 struct SelectParams {
   const uint8_t* logits;
@@ -76,11 +75,14 @@ __device__ __forceinline__ float from_ordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// A 32-bit word of logits as floats: two of 16 bits, or one.
+// Words of logits: two of 16 bits in each, or one of 32.
 template <int TYPE>
 struct Word {
   static constexpr int kPer = TYPE == VG_TYPE_FP32 ? 1 : 2;
   static constexpr int kSize = 4 / kPer;
+  static constexpr uint32_t kNone = TYPE == VG_TYPE_FP32   ? 0xff800000u
+                                    : TYPE == VG_TYPE_BF16 ? 0xff80ff80u
+                                                           : 0xfc00fc00u;  // -inf
   static __device__ __forceinline__ void get(uint32_t w, float (&x)[kPer]) {
     if constexpr (TYPE == VG_TYPE_FP32) {
       x[0] = __uint_as_float(w);
@@ -93,24 +95,98 @@ struct Word {
       x[1] = f.y;
     }
   }
-};
-
-// The slice in shared memory: element i at byte `off` + i * size.
-template <int TYPE>
-struct Slice {
-  static constexpr int kPer = Word<TYPE>::kPer;
-  const uint32_t* words;   // the word that holds element 0
-  bool odd;                // element 0 is its upper half
-  int n;
-  __device__ __forceinline__ int count() const { return (n + kPer - 1) / kPer; }
-  // word w: elements kPer * w .., -inf past the end
-  __device__ __forceinline__ void get(int w, float (&x)[kPer]) const {
-    uint32_t v = words[w];
-    if (kPer == 2 && odd) v = __funnelshift_r(v, words[w + 1], 16);
-    Word<TYPE>::get(v, x);
-    if (kPer == 2 && 2 * w + 1 >= n) x[kPer - 1] = -INFINITY;
+  // maximum by element (a NaN gives way)
+  static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (TYPE == VG_TYPE_FP32)
+      r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else if constexpr (TYPE == VG_TYPE_BF16)
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+      asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // the larger element of a word
+  static __device__ __forceinline__ float top(uint32_t w) {
+    float x[kPer];
+    get(w, x);
+    return kPer == 1 ? x[0] : fmaxf(x[0], x[kPer - 1]);
   }
 };
+
+// A slice lies in shared memory in pieces of 16 bytes, element 0 at the beginning
+// of piece 0 wherever its row begins, -inf past the end; thread t takes pieces
+// t + 256 j.  So equal rows have equal sums.
+//
+// A slice on a 16-byte boundary comes as one bulk copy (which completes on `bar`),
+// but for the last piece if it is not whole.
+template <int TYPE>
+__device__ __forceinline__ void copy_slice(uint4* data, const uint8_t* src, int bytes, uint64_t* bar) {
+  const int whole = bytes & ~15;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(bar, whole);
+    if (whole > 0) bulk_load(data, src, whole, bar);
+  }
+  if (bytes > whole && threadIdx.x >= 32 && threadIdx.x < 48) {
+    constexpr int SIZE = Word<TYPE>::kSize;
+    const int at = whole + (threadIdx.x - 32) * SIZE;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(data) + at;
+    if (at < whole + 16) {
+      if (SIZE == 2)
+        *reinterpret_cast<uint16_t*>(dst) =
+            at < bytes ? *reinterpret_cast<const uint16_t*>(src + at) : (uint16_t)Word<TYPE>::kNone;
+      else
+        *reinterpret_cast<uint32_t*>(dst) = at < bytes ? *reinterpret_cast<const uint32_t*>(src + at) : Word<TYPE>::kNone;
+    }
+  }
+}
+
+// Any other slice, `off` = 4 SHIFT (+ 2 if odd) bytes past a boundary: a piece out
+// of two aligned loads (`base`), of which no more are made than hold an element
+// of the slice (an allocation begins and ends on such a boundary).
+template <int TYPE, int SHIFT>
+__device__ __forceinline__ void shift_slice(uint4* data, const uint8_t* base, int off, int bytes) {
+  const uint32_t none = Word<TYPE>::kNone;
+  const bool odd = (off & 2) != 0;
+#pragma unroll 4
+  for (int at = 16 * threadIdx.x; at < bytes; at += 16 * kSliceThreads) {
+    uint4 a = __ldg(reinterpret_cast<const uint4*>(base + at)), b = make_uint4(none, none, none, none);
+    if (at + 16 - off < bytes) b = __ldg(reinterpret_cast<const uint4*>(base + at + 16));
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = TYPE != VG_TYPE_FP32 && odd ? __funnelshift_r(x[SHIFT + i], x[SHIFT + i + 1], 16) : x[SHIFT + i];
+      const int left = bytes - at - 4 * i;  // of the slice, from this word on
+      if (left <= 0)
+        w[i] = none;
+      else if (left < 4)
+        w[i] = (w[i] & 0xffffu) | (none & 0xffff0000u);
+    }
+    data[at / 16] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// f(element number, value) for the elements of a thread's pieces that `may` let
+// through (by the largest of a piece).
+template <int TYPE, typename M, typename F>
+__device__ __forceinline__ void for_elements(const uint4* data, int pieces, M may, F f) {
+  constexpr int PER = Word<TYPE>::kPer;
+#pragma unroll 2
+  for (int q = threadIdx.x; q < pieces; q += kSliceThreads) {
+    const uint4 v = data[q];
+    using W = Word<TYPE>;
+    if (!may(W::top(W::most(W::most(v.x, v.y), W::most(v.z, v.w))))) continue;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[PER];
+      W::get(w[i], x);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) f((4 * q + i) * PER + j, x[j]);
+    }
+  }
+}
 
 // The CTA's sum of v, for every thread (two barriers).
 __device__ __forceinline__ int cta_sum(int v, int* part) {
@@ -124,24 +200,39 @@ __device__ __forceinline__ int cta_sum(int v, int* part) {
   return sum;
 }
 
+// Of 32 or 64 values in shared memory the num_out-th largest, found by counting
+// in one warp, written to *kth.
+__device__ __forceinline__ void kth_of_groups(const float* group, int groups, int num_out, float* kth) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int own = lane; own < groups; own += 32) {
+    const float v = group[own];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < groups; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(group + j);
+      rank += o.x > v || (o.x == v && j < own);
+      rank += o.y > v || (o.y == v && j + 1 < own);
+      rank += o.z > v || (o.z == v && j + 2 < own);
+      rank += o.w > v || (o.w == v && j + 3 < own);
+    }
+    if (rank == num_out - 1) *kth = v;
+  }
+}
+
 // The num_out best where the list overflows: the num_out-th largest value by
 // bisection, the larger ones listed, then its ties in order.  `least` has at least
 // num_out elements at or above it, or is -inf.  Returns the list's length.
 template <int TYPE>
-__device__ __noinline__ int list_by_bisection(const Slice<TYPE>& sl, float least, float most, int num_out,
+__device__ __noinline__ int list_by_bisection(const uint4* data, int pieces, float least, float most, int num_out,
                                               float2* list, int* counter, int* part) {
-  const int tid = threadIdx.x, words = sl.count();
-  float x[Slice<TYPE>::kPer];
+  const int tid = threadIdx.x;
   uint32_t lo = ordered(least), hi = ordered(most);
   while (lo < hi) {  // the largest key with num_out elements at or above it
     const uint32_t mid = lo + (hi - lo + 1) / 2;
     const float t = from_ordered(mid);
     int n = 0;
-    for (int w = tid; w < words; w += kSliceThreads) {
-      sl.get(w, x);
-#pragma unroll
-      for (int j = 0; j < Slice<TYPE>::kPer; ++j) n += x[j] >= t;
-    }
+    for_elements<TYPE>(data, pieces, [&](float top) { return top >= t; }, [&](int, float x) { n += x >= t; });
     if (cta_sum(n, part) >= num_out)
       lo = mid;
     else
@@ -150,59 +241,53 @@ __device__ __noinline__ int list_by_bisection(const Slice<TYPE>& sl, float least
   const float t = from_ordered(lo);
   if (tid == 0) *counter = 0;
   __syncthreads();
-  for (int w = tid; w < words; w += kSliceThreads) {
-    sl.get(w, x);
-#pragma unroll
-    for (int j = 0; j < Slice<TYPE>::kPer; ++j)
-      if (x[j] > t) {
-        const int at = atomicAdd(counter, 1);
-        list[at] = make_float2(x[j], __int_as_float(Slice<TYPE>::kPer * w + j));
-      }
-  }
+  for_elements<TYPE>(data, pieces, [&](float top) { return top > t; }, [&](int e, float x) {
+    if (x > t) list[atomicAdd(counter, 1)] = make_float2(x, __int_as_float(e));
+  });
   __syncthreads();
   int have = *counter;  // below num_out, or every element above -inf
-  if (t > -INFINITY) {
-    for (int w0 = 0; w0 < words && have < num_out; w0 += kSliceThreads) {
-      const int w = w0 + tid;
-      int own = 0;
-      if (w < words) {
-        sl.get(w, x);
+  if (t == -INFINITY) return have;
+  for (int q0 = 0; q0 < pieces && have < num_out; q0 += kSliceThreads) {
+    // this thread's piece of the 256 from q0 on; their elements are in order
+    const int end = min(pieces, q0 + kSliceThreads);
+    int own = 0;
+    if (q0 + tid < end)
+      for_elements<TYPE>(data + q0, end - q0, [&](float top) { return top >= t; }, [&](int, float x) { own += x == t; });
+    int before = own;  // inclusive sum over the warp, then the warps before
 #pragma unroll
-        for (int j = 0; j < Slice<TYPE>::kPer; ++j) own += x[j] == t;
-      }
-      int before = own;  // inclusive sum over the warp, then the warps before
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if ((tid & 31) >= o) before += v;
-      }
-      if ((tid & 31) == 31) part[tid >> 5] = before;
-      __syncthreads();
-      int all = 0;
-#pragma unroll
-      for (int i = 0; i < kSliceWarps; ++i) {
-        if (i < (tid >> 5)) before += part[i];
-        all += part[i];
-      }
-      int at = have + before - own;
-#pragma unroll
-      for (int j = 0; j < Slice<TYPE>::kPer; ++j)
-        if (w < words && x[j] == t && at < num_out)
-          list[at++] = make_float2(t, __int_as_float(Slice<TYPE>::kPer * w + j));
-      have = min(have + all, num_out);
-      __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if ((tid & 31) >= o) before += v;
     }
+    if ((tid & 31) == 31) part[tid >> 5] = before;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < kSliceWarps; ++i) {
+      if (i < (tid >> 5)) before += part[i];
+      all += part[i];
+    }
+    int at = have + before - own;
+    if (own > 0)
+      for_elements<TYPE>(data + q0, end - q0, [&](float top) { return top >= t; }, [&](int e, float x) {
+        if (x == t && at < num_out)
+          list[at++] = make_float2(t, __int_as_float(q0 * 4 * Word<TYPE>::kPer + e));
+      });
+    have = min(have + all, num_out);
+    __syncthreads();
   }
   return have;
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kSliceThreads) beam_slice_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const SelectParams p) {
   constexpr int PER = Word<TYPE>::kPer, SIZE = Word<TYPE>::kSize;
-  extern __shared__ __align__(16) uint8_t data[];  // 16 bytes more than a slice, twice
+  extern __shared__ __align__(16) uint4 data[];
   __shared__ __align__(8) uint64_t bar;
   __shared__ float2 list[kListed];
-  __shared__ float group_max[kSliceWarps][32], sums[kSliceWarps];
+  __shared__ __align__(16) float group_max[64];
+  __shared__ float thread_max[kSliceThreads];
+  __shared__ float warp_max[kSliceWarps], warp_sum[kSliceWarps], kth;
   __shared__ int counter, part[kSliceWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.slices, s = blockIdx.x - row * p.slices;
@@ -214,88 +299,103 @@ __global__ void __launch_bounds__(kSliceThreads) beam_slice_kernel(const SelectP
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   if (!row_lives(p, row)) return;
-  const int first = s * p.slice, n = min(p.slice, p.vocab - first);
-  // whole 16-byte pieces by one bulk copy, the ends by element
+  const int first = s * p.slice, n = min(p.slice, p.vocab - first), bytes = n * SIZE;
   const uint8_t* src = p.logits + row * p.stride + (int64_t)first * SIZE;
   const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
-  const int begin = (16 - off) & 15, bytes = n * SIZE;
-  const int middle = max(bytes - begin, 0) & ~15;
-  uint8_t* dst = data + off;
+  if (off == 0)
+    copy_slice<TYPE>(data, src, bytes, &bar);
+  else if (off < 4)
+    shift_slice<TYPE, 0>(data, src - off, off, bytes);
+  else if (off < 8)
+    shift_slice<TYPE, 1>(data, src - off, off, bytes);
+  else if (off < 12)
+    shift_slice<TYPE, 2>(data, src - off, off, bytes);
+  else
+    shift_slice<TYPE, 3>(data, src - off, off, bytes);
   __syncthreads();
-  if (tid == 0) {
-    mbar_arrive_expect_tx(&bar, middle);
-    if (middle > 0) bulk_load(dst + begin, src + begin, middle, &bar);
+  if (off == 0 && !mbar_wait_checked(&bar, 0, p.wait_ns, p.error_flag)) return;
+  const int pieces = (bytes + 15) / 16;
+  // -------- maxima (a NaN is passed over; the sum shows it)
+  uint32_t most = Word<TYPE>::kNone;
+#pragma unroll 4
+  for (int q = tid; q < pieces; q += kSliceThreads) {
+    const uint4 v = data[q];
+    most = Word<TYPE>::most(most, Word<TYPE>::most(Word<TYPE>::most(v.x, v.y), Word<TYPE>::most(v.z, v.w)));
   }
-  if (tid >= 32 && tid < 64) {  // at most 7 elements on either side (3 of 32 bits)
-    const int i = (tid & 15) * SIZE, at = tid < 48 ? i : begin + middle + i;
-    if (tid < 48 ? i < min(begin, bytes) : at < bytes) {
-      if (SIZE == 2)
-        *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(src + at);
-      else
-        *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(src + at);
+  const float mine = Word<TYPE>::top(most);
+  thread_max[tid] = mine;
+  float m_warp = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m_warp = fmaxf(m_warp, __shfl_xor_sync(0xffffffffu, m_warp, o));
+  if (lane == 0) warp_max[warp] = m_warp;
+  __syncthreads();
+  // -------- a value that at least num_out elements reach, and few more
+  if (warp == 0) {
+    const int groups = p.num_out <= 16 ? 32 : 64;
+    float even = -INFINITY, odd = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSliceWarps; i += 2) {
+      even = fmaxf(even, thread_max[i * 32 + lane]);
+      odd = fmaxf(odd, thread_max[i * 32 + 32 + lane]);
     }
+    group_max[lane] = groups == 32 ? fmaxf(even, odd) : even;
+    group_max[32 + lane] = odd;
+    __syncwarp();
+    kth_of_groups(group_max, groups, p.num_out, &kth);
   }
-  __syncthreads();
-  const bool landed = mbar_wait_checked(&bar, 0, p.wait_ns, p.error_flag);
-  if (!landed) return;  // flagged; after a second nothing more is expected
-  const Slice<TYPE> sl = {reinterpret_cast<const uint32_t*>(data + (off & ~3)), (off & 2) != 0, n};
-  const int words = sl.count();
-  // -------- the groups' maxima (fmaxf passes a NaN over; the sum shows it)
-  float mx = -INFINITY;
-#pragma unroll 4
-  for (int w = tid; w < words; w += kSliceThreads) {
-    float x[PER];
-    sl.get(w, x);
+  // -------- sum of exponentials relative to the warp's maximum
+  const float base = safe_ref(m_warp);
+  uint64_t acc = 0;
+  const uint64_t c2 = pair(kLog2e, kLog2e), base2 = pair(-base, -base);
+#pragma unroll 2
+  for (int q = tid; q < pieces; q += kSliceThreads) {
+    const uint4 v = data[q];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < PER; ++j) mx = fmaxf(mx, x[j]);
-  }
-  int groups = 4;
-  while (groups < p.num_out) groups *= 2;
-  for (int o = 16; o >= groups; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  group_max[warp][lane] = mx;
-  __syncthreads();
-  float even = -INFINITY, uneven = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kSliceWarps; i += 2) {
-    even = fmaxf(even, group_max[i][lane]);
-    uneven = fmaxf(uneven, group_max[i + 1][lane]);
-  }
-  float m = fmaxf(even, uneven), least = groups > 32 ? fminf(even, uneven) : m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-  }
-  // -------- the sum of exponentials, and what is at or above `least`
-  const float ref = safe_ref(m), floor = fmaxf(least, -FLT_MAX);  // -inf is never listed
-  float sum = 0.f;
-#pragma unroll 4
-  for (int w = tid; w < words; w += kSliceThreads) {
-    float x[PER];
-    sl.get(w, x);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      sum += ex2((x[j] - ref) * kLog2e);
-      if (x[j] >= floor) {
-        const int at = atomicAdd(&counter, 1);
-        if (at < kListed) list[at] = make_float2(x[j], __int_as_float(PER * w + j));
+    for (int i = 0; i < 4; i += 2 / PER) {
+      float x[2];
+      if constexpr (PER == 2) {
+        Word<TYPE>::get(w[i], x);
+      } else {
+        x[0] = __uint_as_float(w[i]);
+        x[1] = __uint_as_float(w[i + 1]);
       }
+      const float2 y = unpair(mul2(add2(pair(x[0], x[1]), base2), c2));
+      acc = add2(acc, pair(ex2(y.x), ex2(y.y)));
     }
   }
+  const float2 a = unpair(acc);
+  float sum = a.x + a.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sums[warp] = sum;
+  if (lane == 0) warp_sum[warp] = sum;
+  __syncthreads();
+  // -------- what reaches it (never -inf)
+  const float least = kth, floor = fmaxf(least, -FLT_MAX);
+  if (mine >= floor)
+    for_elements<TYPE>(data, pieces, [&](float top) { return top >= floor; }, [&](int e, float x) {
+      if (x >= floor) {
+        const int at = atomicAdd(&counter, 1);
+        if (at < kListed) list[at] = make_float2(x, __int_as_float(e));
+      }
+    });
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kSliceWarps; ++i) m = fmaxf(m, warp_max[i]);
   __syncthreads();
   if (tid == 0) {
     float l = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSliceWarps; ++i) l += sums[i];
+    for (int i = 0; i < kSliceWarps; ++i) {
+      const float wl = warp_sum[i];
+      l += wl == 0.f ? 0.f : wl * expf(safe_ref(warp_max[i]) - safe_ref(m));
+    }
     p.slice_ml[(int64_t)row * p.slices + s] = make_float2(m, l);
   }
   int listed = counter;
   if (listed > kListed) {
     __syncthreads();
-    listed = list_by_bisection<TYPE>(sl, least, m, p.num_out, list, &counter, part);
+    listed = list_by_bisection<TYPE>(data, pieces, least, m, p.num_out, list, &counter, part);
     __syncthreads();
   }
   // -------- their order, by counting
@@ -339,116 +439,230 @@ __device__ __forceinline__ float2 row_offset(float s, float m, float l) {
   return pair_add(c, -fmaf((float)e, kLn2Lo, logf(f)));
 }
 
-constexpr int kRequestThreads = 256;
+constexpr int kRequestThreads = 256, kRequestWarps = kRequestThreads / 32;
+constexpr int kHeads = 2 * kMaxOut;  // front entries that a bound is found from
+constexpr int kEarly = 4;            // entries of a thread that are loaded with the normalisers
 
-// Shared memory: [warps][slices * num_out] entries of the rows being merged, then
-// [beams][num_out] entries of the rows' lists.
+// A row of the request: what it adds to its logits, or that it offers one entry
+// (it has ended) or nothing.
+struct Row {
+  float2 offset;
+  float score;
+  int kind;  // 0: nothing, 1: its entries, 2: the end token
+};
+
+struct Pick {
+  uint64_t key;  // order of the score (hi, then lo); 0: none
+  int at;        // list * num_out + depth: beam, then token, among equal scores
+  int token;
+};
+
+__device__ __forceinline__ uint64_t score_key(float2 y) {
+  return y.x > -INFINITY ? (uint64_t)ordered(y.x) << 32 | ordered(y.y) : 0;  // past float's range: none
+}
+
+// Entry `depth` of list `list` (a slice of a row), given what lies there.
+__device__ __forceinline__ Pick pick_of(const SelectParams& p, const Row* rows, int list, int depth, float2 raw) {
+  const int w = list / p.slices;
+  const Row& r = rows[w];
+  Pick k = {0, list * p.num_out + depth, __float_as_int(raw.y)};
+  if (r.kind == 1) {
+    if (k.token >= 0) k.key = score_key(pair_add(r.offset, raw.x));
+  } else if (r.kind == 2 && depth == 0 && list == w * p.slices) {
+    k.key = score_key(make_float2(r.score, 0.f));
+    k.token = p.end_token;
+  }
+  return k;
+}
+
+__device__ __forceinline__ void write_place(const SelectParams& p, const Row* rows, int b, int place, const Pick& k) {
+  const int64_t at = (int64_t)b * p.num_out + place;
+  const bool none = k.key == 0;
+  const int w = none ? -1 : k.at / (p.slices * p.num_out);
+  p.out_scores[at] = none ? -INFINITY : from_ordered((uint32_t)(k.key >> 32));
+  p.out_tokens[at] = none ? -1 : k.token;
+  p.out_parents[at] = w;
+  if (p.out_ended) p.out_ended[at] = !none && (rows[w].kind == 2 || k.token == p.end_token);
+}
+
+// Where more entries are level than there is room for: the best front entry of
+// all lists, one place after another (one warp, a lane takes every 32nd list).
+__device__ __noinline__ void merge_one_by_one(const SelectParams& p, const Row* rows, const float2* best, int b,
+                                              uint8_t* depth) {
+  const int lane = threadIdx.x & 31, lists = p.beams * p.slices;
+  for (int l = lane; l < lists; l += 32) depth[l] = 0;
+  for (int place = 0; place < p.num_out; ++place) {
+    Pick top = {0, INT_MAX, -1};
+    for (int l = lane; l < lists; l += 32) {
+      if (depth[l] >= p.num_out) continue;
+      const Pick k = pick_of(p, rows, l, depth[l], __ldcg(best + (int64_t)l * p.num_out + depth[l]));
+      if (k.key > top.key) top = k;  // equal: the lower list
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Pick k;
+      k.key = __shfl_xor_sync(0xffffffffu, top.key, o);
+      k.at = __shfl_xor_sync(0xffffffffu, top.at, o);
+      k.token = __shfl_xor_sync(0xffffffffu, top.token, o);
+      if (k.key > top.key || (k.key == top.key && k.at < top.at)) top = k;
+    }
+    if (lane == 0) write_place(p, rows, b, place, top);
+    const int l = top.at / p.num_out;
+    if (top.key && l % 32 == lane) ++depth[l];
+    __syncwarp();
+  }
+}
+
+// A CTA per request.  Its rows' slices left sorted lists; a bound that num_out
+// entries reach is the num_out-th largest of front entries, as in the slices.
 __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const SelectParams p) {
-  extern __shared__ __align__(16) float2 entries[];
-  __shared__ float2 offset[kMaxBeams];
-  __shared__ float own_score[kMaxBeams];
-  __shared__ int length[kMaxBeams];  // of a row's list; -1: an ended beam's one entry
+  __shared__ Row rows[kMaxBeams];
+  __shared__ __align__(16) uint64_t heads[kHeads];
+  __shared__ Pick picks[kListed];
+  __shared__ uint64_t bound;
+  __shared__ int counter;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
-  const int per_row = p.slices * p.num_out;
-  float2* lists = entries + (kRequestThreads / 32) * per_row;
+  const int lists = p.beams * p.slices, entries = lists * p.num_out, row0 = b * p.beams;
+  const float2* best = p.slice_best + (int64_t)row0 * p.slices * p.num_out;
+  // how many front entries of each list, and how many values to bound from
+  const int front = (p.num_out + lists - 1) / lists, values = lists * front;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  for (int w = warp; w < p.beams; w += kRequestThreads / 32) {
-    const int row = b * p.beams + w;
-    const float s = p.scores[row];
-    const bool ended = p.ended && p.ended[row];
-    bool bad = s != s || s == INFINITY;
-    int n = 0;
-    float2 c = make_float2(0.f, 0.f);
-    if (ended && !bad) {
-      n = s > -INFINITY ? -1 : 0;
-    } else if (row_lives(p, row)) {
-      // the row's entries, and its normaliser meanwhile
-      float2* mine = entries + warp * per_row;
-      const float2* src = p.slice_best + (int64_t)row * per_row;
-      for (int i = lane; i < per_row; i += 32) mine[i] = __ldcg(src + i);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < p.slices) ml = __ldcg(p.slice_ml + (int64_t)row * p.slices + lane);
-      float m = ml.x;
+  // -------- loads (of rows that left nothing as well: whatever lies there)
+  float2 early[kEarly], head = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // NaN where a slice's sum is one (it holds a NaN or +inf)
-      float l = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.y * expf(ml.x - safe_ref(m));
+  for (int k = 0; k < kEarly; ++k)
+    if (tid + k * kRequestThreads < entries) early[k] = __ldcg(best + tid + k * kRequestThreads);
+  const int head_list = tid % lists, head_depth = tid / lists;
+  if (tid < values) head = __ldcg(best + (int64_t)head_list * p.num_out + head_depth);
+  constexpr int kRowsPerWarp = kMaxBeams / kRequestWarps;
+  float2 ml[kRowsPerWarp];
+  float score[kRowsPerWarp];
+  bool ended[kRowsPerWarp];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      bad = !(l < INFINITY);
-      if (!bad && l > 0.f) {
-        c = row_offset(s, m, l);
-        __syncwarp();
-        // the slices' lists, a lane each, by logit; a lower lane's tokens are lower
-        const float2* head = mine + lane * p.num_out;
-        int d = 0;
-        float2 x = lane < p.slices ? head[0] : make_float2(0.f, __int_as_float(-1));
-        for (; n < p.num_out; ++n) {
-          const uint32_t key = __float_as_int(x.y) >= 0 ? ordered(x.x) : 0u;
-          const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-          if (top == 0u) break;
-          const int win = __ffs(__ballot_sync(0xffffffffu, key == top)) - 1;
-          if (lane == win) {
-            lists[w * p.num_out + n] = x;
-            x = ++d < p.num_out ? head[d] : make_float2(0.f, __int_as_float(-1));
-          }
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    const int w = warp + k * kRequestWarps;
+    if (w >= p.beams) break;
+    score[k] = p.scores[row0 + w];
+    ended[k] = p.ended && p.ended[row0 + w];
+    ml[k] = lane < p.slices ? __ldcg(p.slice_ml + (int64_t)(row0 + w) * p.slices + lane) : make_float2(-INFINITY, 0.f);
+  }
+  if (tid == 0) {
+    bound = 0;
+    counter = 0;
+  }
+  // -------- the rows' normalisers
+#pragma unroll
+  for (int k = 0; k < kRowsPerWarp; ++k) {
+    const int w = warp + k * kRequestWarps;
+    if (w >= p.beams) break;
+    Row r = {make_float2(0.f, 0.f), score[k], 0};
+    bool bad = !(score[k] < INFINITY);
+    if (!bad && score[k] > -INFINITY) {
+      if (ended[k]) {
+        r.kind = 2;
+      } else {
+        float m = ml[k].x;
+        for (int s = lane + 32; s < p.slices; s += 32)
+          m = fmaxf(m, __ldcg(p.slice_ml + (int64_t)(row0 + w) * p.slices + s).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // NaN where a slice's sum is one (it holds a NaN or +inf)
+        auto part = [&](float2 x) { return x.y == 0.f ? 0.f : x.y * expf(x.x - safe_ref(m)); };
+        float l = part(ml[k]);
+        for (int s = lane + 32; s < p.slices; s += 32)
+          l += part(__ldcg(p.slice_ml + (int64_t)(row0 + w) * p.slices + s));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        bad = !(l < INFINITY);
+        if (!bad && l > 0.f) {
+          r.kind = 1;
+          r.offset = row_offset(score[k], m, l);
         }
       }
     }
     if (lane == 0) {
       if (bad) flag_error(p.error_flag, VG_DEVERR_VALUE);
-      offset[w] = c;
-      own_score[w] = s;
-      length[w] = bad ? 0 : n;
+      rows[w] = r;
     }
-    __syncwarp();
   }
   __syncthreads();  // scores and marks have been read: the outputs may be the same arrays
-  if (warp > 0) return;
-  // the rows' lists, a lane each, by score; a lower lane is a lower beam
-  const int n = lane < p.beams ? length[lane] : 0;
-  const bool ended = n < 0;
-  const float2 c = lane < p.beams ? offset[lane] : make_float2(0.f, 0.f);
-  int d = 0, token = -1;
-  float2 y = make_float2(0.f, 0.f);
-  bool has = false;
-  auto front = [&]() {
-    has = d < (ended ? 1 : n);
-    if (!has) return;
-    if (ended) {
-      y = make_float2(own_score[lane], 0.f);
-      token = p.end_token;
-    } else {
-      const float2 x = lists[lane * p.num_out + d];
-      y = pair_add(c, x.x);
-      token = __float_as_int(x.y);
-      has = y.x > -INFINITY;  // a sum past float's range is no candidate
+  // -------- the bound
+  if (lists > kRequestThreads) {
+    // many lists: threads are dealt the front entries, the largest of each
+    uint64_t most = 0;
+    for (int l = tid; l < lists; l += kRequestThreads) {
+      const Pick k = pick_of(p, rows, l, 0, l == tid ? head : __ldcg(best + (int64_t)l * p.num_out));
+      most = k.key > most ? k.key : most;
     }
-  };
-  front();
-  for (int k = 0; k < p.num_out; ++k) {
-    const uint32_t hi = has ? ordered(y.x) : 0u, top = __reduce_max_sync(0xffffffffu, hi);
-    const int64_t at = (int64_t)b * p.num_out + k;
-    if (top == 0u) {
-      if (lane == 0) {
-        p.out_scores[at] = -INFINITY;
-        p.out_tokens[at] = p.out_parents[at] = -1;
-        if (p.out_ended) p.out_ended[at] = 0;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, most, o);
+      most = other > most ? other : most;
+    }
+    if ((tid & 3) == 0) heads[tid >> 2] = most;
+  } else {
+    // (values <= 2 num_out where there are fewer lists than places, else lists)
+    uint64_t own = tid < values ? pick_of(p, rows, head_list, head_depth, head).key : 0;
+    if (values > kHeads) {
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, own, o);
+        own = other > own ? other : own;
       }
-      continue;
-    }
-    const uint32_t lo = has && hi == top ? ordered(y.y) : 0u, low = __reduce_max_sync(0xffffffffu, lo);
-    const int win = __ffs(__ballot_sync(0xffffffffu, has && hi == top && lo == low)) - 1;
-    if (lane == win) {
-      p.out_scores[at] = y.x;
-      p.out_tokens[at] = token;
-      p.out_parents[at] = lane;
-      if (p.out_ended) p.out_ended[at] = ended || token == p.end_token;
-      ++d;
-      front();
+      if ((tid & 3) == 0) heads[tid >> 2] = own;
+    } else if (tid < kHeads) {
+      heads[tid] = own;
     }
   }
+  __syncthreads();
+  {
+    // two threads count for each value
+    const int n = values > kHeads ? kRequestThreads / 4 : values, own = tid >> 1, half = tid & 1;
+    const uint64_t v = heads[own < kHeads ? own : 0];
+    int rank = 0;
+    for (int j = half; j < n; j += 2) {
+      const uint64_t o = heads[j];
+      rank += o > v || (o == v && j < own);
+    }
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    if (own < n && rank == p.num_out - 1) bound = v;
+  }
+  __syncthreads();
+  // -------- what reaches it
+  const uint64_t least = bound > 0 ? bound : 1;
+  for (int i0 = 0, k = 0; i0 < entries; i0 += kRequestThreads, ++k) {
+    const int i = i0 + tid;
+    if (i >= entries) break;
+    const float2 raw = k == 0 ? early[0] : k == 1 ? early[1] : k == 2 ? early[2] : k == 3 ? early[3] : __ldcg(best + i);
+    const int list = i / p.num_out;
+    const Pick x = pick_of(p, rows, list, i - list * p.num_out, raw);
+    if (x.key >= least) {
+      const int at = atomicAdd(&counter, 1);
+      if (at < kListed) picks[at] = x;
+    }
+  }
+  __syncthreads();
+  const int listed = counter;
+  if (listed > kListed) {
+    if (warp == 0) merge_one_by_one(p, rows, best, b, reinterpret_cast<uint8_t*>(picks));
+    return;
+  }
+  // -------- their order: eight threads count for each
+  for (int c0 = 0; c0 < listed; c0 += kRequestThreads / 8) {
+    const int c = c0 + (tid >> 3);
+    const Pick own = picks[c < listed ? c : 0];
+    int rank = 0;
+    for (int j = tid & 7; j < listed; j += 8) {
+      const Pick& o = picks[j];
+      rank += o.key > own.key || (o.key == own.key && o.at < own.at);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (c < listed && rank < p.num_out && (tid & 7) == 0) write_place(p, rows, b, rank, own);
+  }
+  for (int place = listed + tid; place < p.num_out; place += kRequestThreads)
+    write_place(p, rows, b, place, Pick{0, 0, -1});
 }
 
 struct SelectPlan {
@@ -457,20 +671,20 @@ struct SelectPlan {
 };
 
 // Slices of 32 KB; more and shorter ones (down to 4 KB) while they are too few
-// to fill the GPU, longer ones where a row has more than the merge has lanes.
-// slices = 0: rows too long.
+// to fill the GPU.  slices = 0: rows too long.
 SelectPlan make_select_plan(int64_t rows, int vocab, int size, int num_out) {
   SelectPlan pl = {};
   const int64_t row = (int64_t)vocab * size;
-  int64_t n = (row + kSliceBytes - 1) / kSliceBytes;
+  const int64_t least = (row + kSliceBytes - 1) / kSliceBytes;
+  if (least > kMaxSlices) return pl;
   const int64_t most = (row + kLeastSliceBytes - 1) / kLeastSliceBytes;
   const int64_t fill = (3 * (int64_t)device_sm_count() + rows - 1) / rows;
-  n = n > (fill < most ? fill : most) ? n : (fill < most ? fill : most);
-  if (n > kMaxSlices) n = kMaxSlices;
+  int64_t n = fill < most ? fill : most;
+  if (n > 32) n = 32;
+  if (n < least) n = least;
   const int piece = 16 / size;
   int64_t slice = (vocab + n - 1) / n;
   slice = (slice + piece - 1) / piece * piece;
-  if (slice * size > kMostSliceBytes) return pl;
   pl.slice = (int)slice;
   pl.slices = (int)((vocab + slice - 1) / slice);
   pl.off_best = align_up((size_t)rows * pl.slices * sizeof(float2), 256);
@@ -480,23 +694,6 @@ SelectPlan make_select_plan(int64_t rows, int vocab, int size, int num_out) {
 
 int type_size(int type) {
   return type == VG_TYPE_FP32 ? 4 : type == VG_TYPE_BF16 || type == VG_TYPE_FP16 ? 2 : 0;
-}
-
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&set)[64]) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && set[dev]) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) set[dev] = true;
-  return e;
-}
-
-template <int TYPE>
-cudaError_t launch_slices(cudaLaunchConfig_t cfg, const SelectParams& p) {
-  static bool set[64] = {false};
-  const cudaError_t e = allow_smem(beam_slice_kernel<TYPE>, kMostSliceBytes + 32, set);
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, beam_slice_kernel<TYPE>, p);
 }
 
 }  // namespace
@@ -555,21 +752,19 @@ extern "C" vg_status vg_beam_select(const void* logits, int type, int64_t logits
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch * beams * pl.slices);
   cfg.blockDim = dim3(kSliceThreads);
-  cfg.dynamicSmemBytes = (size_t)pl.slice * size + 32;
+  cfg.dynamicSmemBytes = (size_t)pl.slice * size;
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e = type == VG_TYPE_FP32   ? launch_slices<VG_TYPE_FP32>(cfg, p)
-                  : type == VG_TYPE_BF16 ? launch_slices<VG_TYPE_BF16>(cfg, p)
-                                         : launch_slices<VG_TYPE_FP16>(cfg, p);
-  if (e != cudaSuccess) return VG_ERR_LAUNCH;
-  static bool set[64] = {false};
-  constexpr int kMostMerge = ((kRequestThreads / 32) * kMaxSlices + kMaxBeams) * kMaxOut * (int)sizeof(float2);
-  e = allow_smem(beam_merge_kernel, kMostMerge, set);
+  cudaError_t e = cudaLaunchKernelEx(&cfg,
+                                     type == VG_TYPE_FP32   ? beam_slice_kernel<VG_TYPE_FP32>
+                                     : type == VG_TYPE_BF16 ? beam_slice_kernel<VG_TYPE_BF16>
+                                                            : beam_slice_kernel<VG_TYPE_FP16>,
+                                     p);
   if (e != cudaSuccess) return VG_ERR_LAUNCH;
   cfg.gridDim = dim3(batch);
   cfg.blockDim = dim3(kRequestThreads);
-  cfg.dynamicSmemBytes = ((size_t)(kRequestThreads / 32) * pl.slices + beams) * num_out * sizeof(float2);
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, beam_merge_kernel, p);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }
