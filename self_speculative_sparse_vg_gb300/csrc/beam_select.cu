@@ -57,6 +57,7 @@ struct SelectParams {
   int32_t* error_flag;
   int64_t stride;        // bytes between rows
   uint64_t wait_ns;
+  uint32_t by_slices, by_out;  // ceil(2^32 / slices), / num_out; 0 for 1
   int end_token, batch, beams, vocab, num_out, slices, slice;
 };
 
@@ -200,24 +201,21 @@ __device__ __forceinline__ int cta_sum(int v, int* part) {
   return sum;
 }
 
-// Of 32 or 64 values in shared memory the num_out-th largest, found by counting
-// in one warp, written to *kth.
-__device__ __forceinline__ void kth_of_groups(const float* group, int groups, int num_out, float* kth) {
+// Of 32 or 64 values in shared memory the num_out-th largest: the least of those
+// that fewer than num_out exceed.  One warp.
+__device__ __forceinline__ float kth_of_groups(const float* group, int groups, int num_out) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int own = lane; own < groups; own += 32) {
-    const float v = group[own];
-    int rank = 0;
+  const float a = group[lane], b = groups > 32 ? group[32 + lane] : a;
+  int over_a = 0, over_b = 0;
 #pragma unroll 4
-    for (int j = 0; j < groups; j += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(group + j);
-      rank += o.x > v || (o.x == v && j < own);
-      rank += o.y > v || (o.y == v && j + 1 < own);
-      rank += o.z > v || (o.z == v && j + 2 < own);
-      rank += o.w > v || (o.w == v && j + 3 < own);
-    }
-    if (rank == num_out - 1) *kth = v;
+  for (int j = 0; j < groups; j += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(group + j);
+    over_a += (o.x > a) + (o.y > a) + (o.z > a) + (o.w > a);
+    if (groups > 32) over_b += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
   }
+  uint32_t least = over_a < num_out ? ordered(a) : 0xffffffffu;
+  if (groups > 32 && over_b < num_out) least = min(least, ordered(b));
+  return from_ordered(__reduce_min_sync(0xffffffffu, least));
 }
 
 // The num_out best where the list overflows: the num_out-th largest value by
@@ -288,13 +286,13 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
   __shared__ __align__(16) float group_max[64];
   __shared__ float thread_max[kSliceThreads];
   __shared__ float warp_max[kSliceWarps], warp_sum[kSliceWarps], kth;
-  __shared__ int counter, part[kSliceWarps];
+  __shared__ int counter, elements, dead, piece_list[kListed], part[kSliceWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.slices, s = blockIdx.x - row * p.slices;
   if (tid == 0) {
     mbar_init(&bar, 1);
     fence_barrier_init();
-    counter = 0;
+    counter = elements = dead = 0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -313,18 +311,22 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
   else
     shift_slice<TYPE, 3>(data, src - off, off, bytes);
   __syncthreads();
-  if (off == 0 && !mbar_wait_checked(&bar, 0, p.wait_ns, p.error_flag)) return;
-  const int pieces = (bytes + 15) / 16;
-  // -------- maxima (a NaN is passed over; the sum shows it)
-  uint32_t most = Word<TYPE>::kNone;
-#pragma unroll 4
-  for (int q = tid; q < pieces; q += kSliceThreads) {
-    const uint4 v = data[q];
-    most = Word<TYPE>::most(most, Word<TYPE>::most(Word<TYPE>::most(v.x, v.y), Word<TYPE>::most(v.z, v.w)));
+  if (off == 0) {
+    // one warp looks, the others wait for it (256 threads that poll take issue
+    // slots from the SM's other slices)
+    if (warp == 0 && !mbar_wait_checked(&bar, 0, p.wait_ns, p.error_flag)) dead = 1;
+    __syncthreads();
+    if (dead) return;
   }
-  const float mine = Word<TYPE>::top(most);
-  thread_max[tid] = mine;
-  float m_warp = mine;
+  const int pieces = (bytes + 15) / 16;
+  using W = Word<TYPE>;
+  auto piece_top = [](const uint4& v) { return W::most(W::most(v.x, v.y), W::most(v.z, v.w)); };
+  // -------- maxima (a NaN is passed over; the sum shows it)
+  uint32_t most = W::kNone;
+#pragma unroll 4
+  for (int q = tid; q < pieces; q += kSliceThreads) most = W::most(most, piece_top(data[q]));
+  float m_warp = W::top(most);
+  thread_max[tid] = m_warp;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m_warp = fmaxf(m_warp, __shfl_xor_sync(0xffffffffu, m_warp, o));
   if (lane == 0) warp_max[warp] = m_warp;
@@ -341,12 +343,19 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
     group_max[lane] = groups == 32 ? fmaxf(even, odd) : even;
     group_max[32 + lane] = odd;
     __syncwarp();
-    kth_of_groups(group_max, groups, p.num_out, &kth);
+    const float v = kth_of_groups(group_max, groups, p.num_out);
+    if (lane == 0) kth = v;
   }
-  // -------- sum of exponentials relative to the warp's maximum
+  __syncthreads();
+  // -------- sum of exponentials relative to the warp's maximum m, as 2^(c x - r)
+  // with r = c m rounded, which is put right at the end (where c m is no float,
+  // x - m is taken first); and the pieces that reach the value (never -inf)
+  const float least = kth, floor = fmaxf(least, -FLT_MAX);
   const float base = safe_ref(m_warp);
+  const bool plain = fabsf(base) < 1e30f;
+  const float r = plain ? base * kLog2e : 0.f, shift = plain ? 0.f : -base;
+  const uint64_t c2 = pair(kLog2e, kLog2e), r2 = pair(-r, -r);
   uint64_t acc = 0;
-  const uint64_t c2 = pair(kLog2e, kLog2e), base2 = pair(-base, -base);
 #pragma unroll 2
   for (int q = tid; q < pieces; q += kSliceThreads) {
     const uint4 v = data[q];
@@ -355,59 +364,73 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
     for (int i = 0; i < 4; i += 2 / PER) {
       float x[2];
       if constexpr (PER == 2) {
-        Word<TYPE>::get(w[i], x);
+        W::get(w[i], x);
       } else {
         x[0] = __uint_as_float(w[i]);
         x[1] = __uint_as_float(w[i + 1]);
       }
-      const float2 y = unpair(mul2(add2(pair(x[0], x[1]), base2), c2));
+      uint64_t x2 = pair(x[0], x[1]);
+      if (!plain) x2 = add2(x2, pair(shift, shift));
+      const float2 y = unpair(fma2(x2, c2, r2));
       acc = add2(acc, pair(ex2(y.x), ex2(y.y)));
+    }
+    if (W::top(piece_top(v)) >= floor) {
+      const int at = atomicAdd(&counter, 1);
+      if (at < kListed) piece_list[at] = q;
     }
   }
   const float2 a = unpair(acc);
-  float sum = a.x + a.y;
+  float sum = (a.x + a.y) * ex2(plain ? -fmaf(base, kLog2e, -r) : 0.f);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) warp_sum[warp] = sum;
   __syncthreads();
-  // -------- what reaches it (never -inf)
-  const float least = kth, floor = fmaxf(least, -FLT_MAX);
-  if (mine >= floor)
-    for_elements<TYPE>(data, pieces, [&](float top) { return top >= floor; }, [&](int e, float x) {
-      if (x >= floor) {
-        const int at = atomicAdd(&counter, 1);
-        if (at < kListed) list[at] = make_float2(x, __int_as_float(e));
-      }
-    });
-  float m = -INFINITY;
+  float m = warp_max[lane % kSliceWarps], m_own = m;
 #pragma unroll
-  for (int i = 0; i < kSliceWarps; ++i) m = fmaxf(m, warp_max[i]);
-  __syncthreads();
-  if (tid == 0) {
-    float l = 0.f;
+  for (int o = 1; o < kSliceWarps; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (warp == 0) {
+    const float own = warp_sum[lane % kSliceWarps];
+    float l = own == 0.f ? 0.f : own * expf(safe_ref(m_own) - safe_ref(m));
 #pragma unroll
-    for (int i = 0; i < kSliceWarps; ++i) {
-      const float wl = warp_sum[i];
-      l += wl == 0.f ? 0.f : wl * expf(safe_ref(warp_max[i]) - safe_ref(m));
-    }
-    p.slice_ml[(int64_t)row * p.slices + s] = make_float2(m, l);
+    for (int o = 1; o < kSliceWarps; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) p.slice_ml[(int64_t)row * p.slices + s] = make_float2(m, l);
   }
+  // -------- the elements of those pieces, a thread each
   int listed = counter;
+  constexpr int E = 4 * PER;
+  if (listed <= kListed) {
+    for (int i = tid; i < listed * E; i += kSliceThreads) {
+      const int e = piece_list[i / E] * E + i % E;
+      float x[PER];
+      W::get(reinterpret_cast<const uint32_t*>(data)[e / PER], x);
+      const float y = PER == 2 && (e & 1) ? x[PER - 1] : x[0];
+      if (y >= floor) {
+        const int at = atomicAdd(&elements, 1);
+        if (at < kListed) list[at] = make_float2(y, __int_as_float(e));
+      }
+    }
+    __syncthreads();
+    listed = elements;
+  }
   if (listed > kListed) {
     __syncthreads();
     listed = list_by_bisection<TYPE>(data, pieces, least, m, p.num_out, list, &counter, part);
     __syncthreads();
   }
-  // -------- their order, by counting
+  // -------- their order, by counting: four threads for each
   float2* best = p.slice_best + ((int64_t)row * p.slices + s) * p.num_out;
-  for (int i = tid; i < listed; i += kSliceThreads) {
-    const float2 c = list[i];
+  for (int i0 = 0; i0 + (tid & ~31) / 4 < listed; i0 += kSliceThreads / 4) {
+    const int i = i0 + tid / 4;
+    const float2 c = list[i < listed ? i : 0];
     int rank = 0;
-    for (int j = 0; j < listed; ++j) {
+    for (int j = tid & 3; j < listed; j += 4) {
       const float2 o = list[j];
       rank += o.x > c.x || (o.x == c.x && __float_as_int(o.y) < __float_as_int(c.y));
     }
-    if (rank < p.num_out) best[rank] = make_float2(c.x, __int_as_float(first + __float_as_int(c.y)));
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (i < listed && (tid & 3) == 0 && rank < p.num_out)
+      best[rank] = make_float2(c.x, __int_as_float(first + __float_as_int(c.y)));
   }
   for (int i = listed + tid; i < p.num_out; i += kSliceThreads) best[i] = make_float2(-INFINITY, __int_as_float(-1));
 }
@@ -445,7 +468,7 @@ constexpr int kEarly = 4;            // entries of a thread that are loaded with
 
 // A row of the request: what it adds to its logits, or that it offers one entry
 // (it has ended) or nothing.
-struct Row {
+struct alignas(16) Row {
   float2 offset;
   float score;
   int kind;  // 0: nothing, 1: its entries, 2: the end token
@@ -461,10 +484,14 @@ __device__ __forceinline__ uint64_t score_key(float2 y) {
   return y.x > -INFINITY ? (uint64_t)ordered(y.x) << 32 | ordered(y.y) : 0;  // past float's range: none
 }
 
+// n / d for the numbers of a request's entries, m = ceil(2^32 / d): exact while
+// n d < 2^32.
+__device__ __forceinline__ int quotient(int n, uint32_t m) { return m == 0 ? n : (int)__umulhi((uint32_t)n, m); }
+
 // Entry `depth` of list `list` (a slice of a row), given what lies there.
 __device__ __forceinline__ Pick pick_of(const SelectParams& p, const Row* rows, int list, int depth, float2 raw) {
-  const int w = list / p.slices;
-  const Row& r = rows[w];
+  const int w = quotient(list, p.by_slices);
+  const Row r = rows[w];
   Pick k = {0, list * p.num_out + depth, __float_as_int(raw.y)};
   if (r.kind == 1) {
     if (k.token >= 0) k.key = score_key(pair_add(r.offset, raw.x));
@@ -478,7 +505,7 @@ __device__ __forceinline__ Pick pick_of(const SelectParams& p, const Row* rows, 
 __device__ __forceinline__ void write_place(const SelectParams& p, const Row* rows, int b, int place, const Pick& k) {
   const int64_t at = (int64_t)b * p.num_out + place;
   const bool none = k.key == 0;
-  const int w = none ? -1 : k.at / (p.slices * p.num_out);
+  const int w = none ? -1 : quotient(quotient(k.at, p.by_out), p.by_slices);
   p.out_scores[at] = none ? -INFINITY : from_ordered((uint32_t)(k.key >> 32));
   p.out_tokens[at] = none ? -1 : k.token;
   p.out_parents[at] = w;
@@ -517,9 +544,9 @@ __device__ __noinline__ void merge_one_by_one(const SelectParams& p, const Row* 
 // entries reach is the num_out-th largest of front entries, as in the slices.
 __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const SelectParams p) {
   __shared__ Row rows[kMaxBeams];
-  __shared__ __align__(16) uint64_t heads[kHeads];
+  __shared__ __align__(16) float heads[kHeads];
   __shared__ Pick picks[kListed];
-  __shared__ uint64_t bound;
+  __shared__ uint32_t bound;
   __shared__ int counter;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
   const int lists = p.beams * p.slices, entries = lists * p.num_out, row0 = b * p.beams;
@@ -548,9 +575,10 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
     ml[k] = lane < p.slices ? __ldcg(p.slice_ml + (int64_t)(row0 + w) * p.slices + lane) : make_float2(-INFINITY, 0.f);
   }
   if (tid == 0) {
-    bound = 0;
+    bound = 0xffffffffu;
     counter = 0;
   }
+  if (tid < kHeads) heads[tid] = -INFINITY;
   // -------- the rows' normalisers
 #pragma unroll
   for (int k = 0; k < kRowsPerWarp; ++k) {
@@ -587,55 +615,40 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
     }
   }
   __syncthreads();  // scores and marks have been read: the outputs may be the same arrays
-  // -------- the bound
-  if (lists > kRequestThreads) {
-    // many lists: threads are dealt the front entries, the largest of each
-    uint64_t most = 0;
-    for (int l = tid; l < lists; l += kRequestThreads) {
-      const Pick k = pick_of(p, rows, l, 0, l == tid ? head : __ldcg(best + (int64_t)l * p.num_out));
-      most = k.key > most ? k.key : most;
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, most, o);
-      most = other > most ? other : most;
-    }
-    if ((tid & 3) == 0) heads[tid >> 2] = most;
-  } else {
-    // (values <= 2 num_out where there are fewer lists than places, else lists)
-    uint64_t own = tid < values ? pick_of(p, rows, head_list, head_depth, head).key : 0;
-    if (values > kHeads) {
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, own, o);
-        own = other > own ? other : own;
-      }
-      if ((tid & 3) == 0) heads[tid >> 2] = own;
-    } else if (tid < kHeads) {
-      heads[tid] = own;
-    }
+  // -------- the bound: on scores rounded to floats, whose order is that of scores
+  auto rounded = [&](const Pick& k) { return k.key ? from_ordered((uint32_t)(k.key >> 32)) : -INFINITY; };
+  float front_score = -INFINITY;
+  if (tid < values) front_score = rounded(pick_of(p, rows, head_list, head_depth, head));
+  int n = values;
+  if (values > kHeads) {  // many lists: the best front entry of every four threads
+    for (int l = tid + kRequestThreads; l < lists; l += kRequestThreads)
+      front_score = fmaxf(front_score, rounded(pick_of(p, rows, l, 0, __ldcg(best + (int64_t)l * p.num_out))));
+    front_score = fmaxf(front_score, __shfl_xor_sync(0xffffffffu, front_score, 1));
+    front_score = fmaxf(front_score, __shfl_xor_sync(0xffffffffu, front_score, 2));
+    n = kRequestThreads / 4;
+    if ((tid & 3) == 0) heads[tid >> 2] = front_score;
+  } else if (tid < values) {
+    heads[tid] = front_score;
   }
   __syncthreads();
-  {
-    // two threads count for each value
-    const int n = values > kHeads ? kRequestThreads / 4 : values, own = tid >> 1, half = tid & 1;
-    const uint64_t v = heads[own < kHeads ? own : 0];
-    int rank = 0;
-    for (int j = half; j < n; j += 2) {
-      const uint64_t o = heads[j];
-      rank += o > v || (o == v && j < own);
+  if (tid < n) {
+    const float v = heads[tid];
+    int over = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(heads + j);
+      over += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
     }
-    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-    if (own < n && rank == p.num_out - 1) bound = v;
+    if (over < p.num_out) atomicMin(&bound, ordered(v));
   }
   __syncthreads();
   // -------- what reaches it
-  const uint64_t least = bound > 0 ? bound : 1;
+  const uint64_t least = max((uint64_t)bound << 32, (uint64_t)1);
   for (int i0 = 0, k = 0; i0 < entries; i0 += kRequestThreads, ++k) {
     const int i = i0 + tid;
     if (i >= entries) break;
     const float2 raw = k == 0 ? early[0] : k == 1 ? early[1] : k == 2 ? early[2] : k == 3 ? early[3] : __ldcg(best + i);
-    const int list = i / p.num_out;
+    const int list = quotient(i, p.by_out);
     const Pick x = pick_of(p, rows, list, i - list * p.num_out, raw);
     if (x.key >= least) {
       const int at = atomicAdd(&counter, 1);
@@ -746,6 +759,8 @@ extern "C" vg_status vg_beam_select(const void* logits, int type, int64_t logits
   p.num_out = num_out;
   p.slices = pl.slices;
   p.slice = pl.slice;
+  p.by_slices = pl.slices == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + pl.slices - 1) / pl.slices);
+  p.by_out = num_out == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + num_out - 1) / num_out);
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
