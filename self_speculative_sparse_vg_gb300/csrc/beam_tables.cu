@@ -13,8 +13,15 @@
 // The columns of all requests form one line that the CTAs of one cluster share;
 // the places of the returned pages are in line order, so the CTAs exchange their
 // counts through distributed shared memory, and a second cluster barrier lies
-// between what is pushed and what is popped.  A share of one column per thread
-// (16K columns in a full cluster) is read once.
+// between what is pushed and what is popped.
+//
+// Most columns hold one page in all rows and go on doing so: a thread looks at
+// one, all its loads in flight, and leaves it.  The others are gone through by
+// lanes, one per row, several columns of a warp at a time: who holds the same page
+// is one `match` (a thread per column took 4000 cycles for eight rows, in loops
+// over shared memory).  Rows part at neighbouring columns, so a CTA's warps share
+// what each of them has found (32 requests of eight beams 14.7 us with a warp's
+// columns left to it).
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -28,6 +35,9 @@ constexpr int kFewThreads = 256;      // of a CTA for a few rows and columns
 constexpr int kMaxCluster = 16;
 constexpr int kMaxRows = 4096;
 constexpr int kMaxBeams = 32;
+constexpr int kBatch = 8;             // entries of a thread whose loads are in flight together
+constexpr int kTiles = 31;            // tiles of 32 columns of a warp that are remembered
+constexpr int kListed = 64;           // columns of a warp that the CTA's warps can share
 
 struct BeamParams {
   const int32_t* parents;
@@ -39,24 +49,25 @@ struct BeamParams {
   int32_t* copies;
   int32_t* error_flag;
   int batch, beams, width, num_pages, free_capacity;
+  int row_bits;  // log2 of the lanes that a column's rows take
 };
 
-// Shared memory of a CTA: numbers per row, per request, and the old entries of
-// the columns being worked on, [beams][threads].
+// Shared memory of a CTA: numbers per row and per request.
 struct BeamShared {
   int *len, *own, *tail, *rank;  // [rows]; tail: page of a new row's partly filled last page, -1: none;
                                  // rank: which of the pages asked for is its copy's, -1: none
-  int *ends, *alive;             // [batch]: columns up to the request's end; mask of rows that go on
-  int* stage;
+  int *ends, *alive, *full;      // [batch]: columns up to the request's end; mask of rows that go on (after
+                                 // its check); columns that are full pages in every row, 0 if one ends
+  int *bad;                      // [batch]: error bits
   int8_t* parent;                // [rows]; -1: the row is emptied, -2: the request is refused
 };
 
-__host__ __device__ inline size_t shared_bytes(int batch, int beams, int threads) {
+__host__ __device__ inline size_t shared_bytes(int batch, int beams) {
   const size_t rows = (size_t)batch * beams;
-  return (4 * rows + 2 * (size_t)batch + (size_t)beams * threads) * sizeof(int) + rows;
+  return (4 * rows + 4 * (size_t)batch) * sizeof(int) + rows;
 }
 
-__device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p, int threads) {
+__device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p) {
   const int rows = p.batch * p.beams;
   BeamShared sh;
   sh.len = s;
@@ -65,15 +76,16 @@ __device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p, int thr
   sh.rank = s + 3 * rows;
   sh.ends = s + 4 * rows;
   sh.alive = sh.ends + p.batch;
-  sh.stage = sh.alive + p.batch;
-  sh.parent = reinterpret_cast<int8_t*>(sh.stage + p.beams * threads);
+  sh.full = sh.alive + p.batch;
+  sh.bad = sh.full + p.batch;
+  sh.parent = reinterpret_cast<int8_t*>(sh.bad + p.batch);
   return sh;
 }
 
 // Inclusive sum of v over the CTA's threads in order; `all` is the total.  One
-// barrier before and one after `part` is used.
+// barrier; `part` is used again two sums later at the earliest.
 template <int NT>
-__device__ __forceinline__ int cta_inclusive_sum(int v, int* part, int* all) {
+__device__ __noinline__ int cta_inclusive_sum(int v, int* part, int* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -85,20 +97,18 @@ __device__ __forceinline__ int cta_inclusive_sum(int v, int* part, int* all) {
   int sum = lane < NT / 32 ? part[lane] : 0, before = lane < warp ? sum : 0;
   sum = __reduce_add_sync(0xffffffffu, sum);
   before = __reduce_add_sync(0xffffffffu, before);
-  __syncthreads();
   *all = sum;
   return v + before;
 }
 
 __device__ __forceinline__ int pages_of(int len) { return (int)(((unsigned)len + kPageSize - 1) / kPageSize); }
 
-// A column of the line: its request and number, and the old entries (stage).
+// A column of the line: its request and number.  b < 0: none.
 struct Column {
   int b, c;
 };
 
-template <int NT>
-__device__ __forceinline__ Column load_column(const BeamParams& p, const BeamShared& sh, int x) {
+__device__ __forceinline__ Column column_of(const BeamParams& p, const BeamShared& sh, int x) {
   int lo = 0, hi = p.batch - 1;  // the first request that ends past x
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -107,95 +117,145 @@ __device__ __forceinline__ Column load_column(const BeamParams& p, const BeamSha
     else
       lo = mid + 1;
   }
-  const Column col = {lo, x - (lo > 0 ? sh.ends[lo - 1] : 0)};
-  const int r0 = lo * p.beams;
-  int* old = sh.stage + threadIdx.x;
-#pragma unroll 8
-  for (int i = 0; i < p.beams; ++i)
-    old[i * NT] = col.c < sh.own[r0 + i] ? p.page_table[(int64_t)(r0 + i) * p.width + col.c] : -1;
-  return col;
+  return {lo, x - (lo > 0 ? sh.ends[lo - 1] : 0)};
 }
 
-// f(page) for each page of the column that no new row holds, once, rows in
-// order.  What is no page id is passed over, and flagged if `report`.
-template <int NT, typename F>
-__device__ __forceinline__ void for_returned(const BeamParams& p, const BeamShared& sh, const Column& col,
-                                             bool report, F f) {
-  const int r0 = col.b * p.beams;
-  const int alive = sh.alive[col.b];
-  const int* old = sh.stage + threadIdx.x;
-  for (int i = 0; i < p.beams; ++i) {
-    if (col.c >= sh.own[r0 + i]) continue;
-    if ((alive >> i & 1) && col.c < pages_of(sh.len[r0 + i])) continue;
-    const int page = old[i * NT];
-    bool held = false;
-    for (int k = 0; k < p.beams && !held; ++k)
-      held = k != i && col.c < sh.own[r0 + k] && old[k * NT] == page &&
-             (k < i || ((alive >> k & 1) && col.c < pages_of(sh.len[r0 + k])));
-    if (held) continue;
-    if (page < 0 || page >= p.num_pages) {
-      if (report) flag_error(p.error_flag, VG_DEVERR_PAGE);
-      continue;
-    }
-    f(page);
+// Whether the column is one full page in every row and stays that.
+__device__ __forceinline__ bool stays(const BeamParams& p, const BeamShared& sh, const Column& col) {
+  if (col.c >= sh.full[col.b]) return false;
+  const int32_t* at = p.page_table + (int64_t)col.b * p.beams * p.width + col.c;
+  const int first = at[0];
+  bool same = true;
+  for (int i0 = 1; i0 < p.beams; i0 += kBatch) {
+    int page[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) page[k] = i0 + k < p.beams ? at[(int64_t)(i0 + k) * p.width] : first;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) same &= page[k] == first;
   }
+  return same;
+}
+
+// The columns of a tile that change (x: this lane's), listed in order.  Returns how
+// many.
+__device__ __forceinline__ int list_columns(const BeamParams& p, const BeamShared& sh, int x, int end,
+                                            Column* list) {
+  Column col = {-1, 0};
+  bool works = false;
+  if (x < end) {
+    col = column_of(p, sh, x);
+    works = !stays(p, sh, col);
+  }
+  const uint32_t mask = __ballot_sync(0xffffffffu, works);
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (works) list[__popc(mask & ((1u << lane) - 1u))] = col;
+  __syncwarp();
+  return __popc(mask);
+}
+
+// One row of a column, in a lane: its old entry, and whether the page goes back
+// (no new row holds it; the first of the rows that did).
+struct Entry {
+  int b, c, r, page;
+  bool has, keeps, back;
+};
+
+__device__ __forceinline__ Entry load_entry(const BeamParams& p, const BeamShared& sh, const Column& col) {
+  const int i = threadIdx.x & ((1 << p.row_bits) - 1);
+  Entry e = {-1, 0, 0, -1, false, false, false};
+  if (col.b < 0 || i >= p.beams) return e;
+  e.b = col.b;
+  e.c = col.c;
+  e.r = col.b * p.beams + i;
+  e.has = col.c < sh.own[e.r];
+  if (e.has) e.page = p.page_table[(int64_t)e.r * p.width + col.c];
+  e.keeps = e.has && (sh.alive[col.b] >> i & 1) && col.c < pages_of(sh.len[e.r]);
+  return e;
+}
+
+// What goes back of the columns of a warp's entries; returns the lanes.
+__device__ __forceinline__ uint32_t find_returned(const BeamParams& p, Entry& e, bool report) {
+  const int lane = threadIdx.x & 31, bits = p.row_bits;
+  const uint32_t column = bits == 5 ? 0xffffffffu : ((1u << (1 << bits)) - 1u) << (lane >> bits << bits);
+  const uint32_t holders = __ballot_sync(0xffffffffu, e.has), keepers = __ballot_sync(0xffffffffu, e.keeps);
+  const uint32_t same = __match_any_sync(0xffffffffu, e.page) & holders & column;
+  e.back = e.has && !(same & keepers) && !(same & ((1u << lane) - 1u));
+  if (e.back && (e.page < 0 || e.page >= p.num_pages)) {
+    if (report) flag_error(p.error_flag, VG_DEVERR_PAGE);
+    e.back = false;
+  }
+  return __ballot_sync(0xffffffffu, e.back);
 }
 
 template <int NT>
 __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
   extern __shared__ int shared[];
-  __shared__ int part[NT / 32], counts[kMaxCluster];
-  const BeamShared sh = carve(shared, p, NT);
-  const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
+  __shared__ int parts[2][NT / 32], counts[kMaxCluster];
+  __shared__ Column lists[NT / 32][kListed], spread_list[NT / 32 * kListed];
+  const BeamShared sh = carve(shared, p);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  const int ctas = gridDim.x;  // the grid is one cluster
   const int rows = p.batch * p.beams;
+  int turn = 0;  // of `parts`
+  auto sum = [&](int v, int* all) { return cta_inclusive_sum<NT>(v, parts[turn ^= 1], all); };
+  for (int b = tid; b < p.batch; b += NT) {
+    sh.alive[b] = sh.bad[b] = sh.ends[b] = 0;
+    sh.full[b] = INT_MAX;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int top0 = *p.free_count;
+  __syncthreads();
+  // -------- the rows, and what they mean for their requests
   for (int r = tid; r < rows; r += NT) {
-    sh.len[r] = p.lens[r];
-    sh.own[r] = p.owned[r];
-    const int j = p.parents[r];
-    sh.parent[r] = (int8_t)(j >= -1 && j < p.beams ? j : -2);
+    const int b = r / p.beams;
+    const int len = p.lens[r], own = p.owned[r], j = p.parents[r];
+    const bool known = j >= -1 && j < p.beams;
+    sh.len[r] = len;
+    sh.own[r] = own;
+    sh.parent[r] = (int8_t)(known ? j : -2);
+    int bad = known ? 0 : VG_DEVERR_INDEX;
+    if (len < 0 || own < 0 || own > p.width || pages_of(len) > own) bad |= VG_DEVERR_LENGTH;
+    if (bad) atomicOr(&sh.bad[b], bad);
+    if (known && j >= 0) atomicOr(&sh.alive[b], 1 << j);
+    atomicMax(&sh.ends[b], own);
+    atomicMin(&sh.full[b], known && j >= 0 ? len / kPageSize : 0);
   }
   __syncthreads();
-  // -------- the requests' columns
-  int end = 0, columns;
+  // the page at the end of each new row: on its way during the sum
+  constexpr int kEarly = NT == kThreads ? kMaxRows / NT : 1;  // (fewer threads: at most a row each)
+  int tails[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const int r = tid + k * NT;
+    tails[k] = -1;
+    if (r >= rows) break;
+    const int b = r / p.beams, j = sh.parent[r];
+    if (j < 0 || sh.bad[b]) continue;
+    const int from = b * p.beams + j, len = sh.len[from];
+    if (len % kPageSize) tails[k] = p.page_table[(int64_t)from * p.width + len / kPageSize];
+  }
+  int columns = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
-    int cols = 0, alive = 0, bad = 0;
-    if (b < p.batch) {
-      for (int i = 0; i < p.beams; ++i) {
-        const int r = b * p.beams + i, j = sh.parent[r];
-        if (j == -2) bad |= VG_DEVERR_INDEX;
-        if (j >= 0) alive |= 1 << j;
-        if (sh.len[r] < 0 || sh.own[r] < 0 || sh.own[r] > p.width || pages_of(sh.len[r]) > sh.own[r])
-          bad |= VG_DEVERR_LENGTH;
-        cols = max(cols, sh.own[r]);
-      }
-      if (bad) {
-        if (cta == 0) flag_error(p.error_flag, bad);
-        cols = alive = 0;
-        for (int i = 0; i < p.beams; ++i) sh.parent[b * p.beams + i] = -2;
-      }
-      sh.alive[b] = alive;
+    int cols = 0, all;
+    const int bad = b < p.batch ? sh.bad[b] : 0;
+    if (b < p.batch && !bad) cols = sh.ends[b];
+    const int end = columns + sum(cols, &all);
+    if (b < p.batch) sh.ends[b] = end;
+    if (bad) {
+      if (cta == 0) flag_error(p.error_flag, bad);
+      sh.alive[b] = 0;
+      for (int i = 0; i < p.beams; ++i) sh.parent[b * p.beams + i] = -2;
     }
-    const int e = end + cta_inclusive_sum<NT>(cols, part, &columns);
-    if (b < p.batch) sh.ends[b] = e;
-    end += columns;
+    columns += all;
   }
-  columns = end;
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (tid + k * NT < rows) sh.tail[tid + k * NT] = tails[k];
   __syncthreads();
   // -------- who asks for a copy of its last page
-  for (int r = tid; r < rows; r += NT) {
-    const int j = sh.parent[r];
-    int tail = -1;
-    if (j >= 0) {
-      const int from = r - r % p.beams + j, len = sh.len[from];
-      if (len % kPageSize) tail = p.page_table[(int64_t)from * p.width + len / kPageSize];
-    }
-    sh.tail[r] = tail;
-  }
-  __syncthreads();
   int asked = 0;
   for (int r0 = 0; r0 < rows; r0 += NT) {
     const int r = r0 + tid;
@@ -205,21 +265,73 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
       for (int k = first; k < r && !ask; ++k)
         ask = sh.tail[k] == sh.tail[r] && sh.len[first + sh.parent[k]] / kPageSize == full;
     }
-    const int at = asked + cta_inclusive_sum<NT>(ask, part, &all) - ask;
+    const int at = asked + sum(ask, &all) - ask;
     if (r < rows) sh.rank[r] = ask ? at : -1;
     asked += all;
   }
-  // -------- pages that go back: counted, by CTA
-  const int share = (columns + ctas - 1) / ctas, x0 = cta * share, x1 = min(columns, x0 + share);
-  const bool once = share <= NT;
-  Column col = {0, 0};
-  int mine = 0, total;
-  for (int x = x0 + tid; x < x1; x += NT) {
-    col = load_column<NT>(p, sh, x);
-    for_returned<NT>(p, sh, col, true, [&](int) { ++mine; });
+  // -------- the columns that change, and the pages that go back: counted
+  const int step = 32 >> p.row_bits, sub = lane >> p.row_bits;  // columns of a pass, and this lane's
+  const int warps = ctas * (NT / 32), w = cta * (NT / 32) + warp;
+  // few columns: all are gone through, in one pass of every warp.  Else a warp has a
+  // run of tiles of 32, and looks which of their columns change
+  const bool direct = columns <= warps * step;
+  const int tiles = (columns + 31) / 32, share = (tiles + warps - 1) / warps;
+  const int tile0 = w * share, tile1 = min(tiles, tile0 + share);
+  Column* list = lists[warp];
+  int k_begin = 0, k_end = 0;
+  uint32_t has_work = 0;  // tiles with columns that change; those past kTiles share a bit
+  bool spread = true;
+  if (!direct) {
+    int found = 0, listed;
+    bool fits = true;
+    for (int t = tile0; t < tile1; ++t) {
+      fits &= found <= kListed - 32;  // past its room the list is made again
+      const int n = list_columns(p, sh, t * 32 + lane, columns, list + (fits ? found : 0));
+      if (n > 0) has_work |= 1u << min(t - tile0, kTiles);
+      found += n;
+    }
+    // where a warp has several passes: one list of the CTA, if every warp's has
+    // fitted, cut anew in warps' shares
+    constexpr int kMany = 1 << 16, kNotAll = 1 << 24;
+    const int at = sum(lane > 0 ? 0 : !fits ? kNotAll : found > step ? found + kMany : found, &listed);
+    spread = listed < kNotAll;
+    k_end = found;
+    if (spread && listed >= kMany) {
+      listed %= kMany;
+      const int first = __shfl_sync(0xffffffffu, at, 0) % kMany - found;
+      for (int k = lane; k < found; k += 32) spread_list[first + k] = list[k];
+      const int each = ((listed + step - 1) / step + NT / 32 - 1) / (NT / 32) * step;
+      k_begin = min(listed, warp * each);
+      k_end = min(listed, k_begin + each);
+      list = spread_list;
+      __syncthreads();
+    }
   }
-  cta_inclusive_sum<NT>(mine, part, &total);
-  int base = top0, back = total;
+  if (direct) {
+    k_begin = min(columns, w * step);
+    k_end = min(columns, k_begin + step);
+  }
+  // entry of column k of the list
+  auto entry = [&](int k) {
+    Column col = {-1, 0};
+    if (k + sub < k_end) col = direct ? column_of(p, sh, k + sub) : list[k + sub];
+    return load_entry(p, sh, col);
+  };
+  int mine = 0, passes = 0;
+  Entry e = {-1, 0, 0, -1, false, false, false};
+  for (int t = tile0; t < tile1 || (spread && t == tile0); ++t) {
+    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_columns(p, sh, t * 32 + lane, columns, list) : 0;
+    Entry next = entry(k_begin);
+    for (int k0 = k_begin; k0 < k_end; k0 += step, ++passes) {
+      e = next;
+      next = entry(k0 + step);
+      mine += __popc(find_returned(p, e, true));
+    }
+    if (spread) break;
+  }
+  int total;
+  const int before = sum(lane == 0 ? mine : 0, &total) - (lane == 0 ? mine : 0);
+  int base = top0 + __shfl_sync(0xffffffffu, before, 0), back = total;
   if (ctas > 1) {
     if (tid < ctas) {
       const uint32_t to = mapa_shared(smem_u32(&counts[cta]), tid);
@@ -228,11 +340,9 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
     __syncwarp();
     cluster_arrive_release();
     cluster_wait_acquire();
-    back = 0;
-    for (int i = 0; i < ctas; ++i) {
-      if (i < cta) base += counts[i];
-      back += counts[i];
-    }
+    const int count = lane < ctas ? counts[lane] : 0;
+    back = __reduce_add_sync(0xffffffffu, count);
+    base += __reduce_add_sync(0xffffffffu, lane < cta ? count : 0);
   } else {
     __syncthreads();
   }
@@ -247,33 +357,43 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
   }
   const int top = top0 + back;
   // -------- pushed, and the new entries (those of copies come last)
-  for (int xa = x0; xa < x1; xa += NT) {
-    const int x = xa + tid;
-    int n = 0;
-    if (x < x1) {
-      if (!once) col = load_column<NT>(p, sh, x);
-      for_returned<NT>(p, sh, col, false, [&](int) { ++n; });
-    }
-    if (total > 0) {  // of this CTA
-      int all;
-      int at = base + cta_inclusive_sum<NT>(n, part, &all) - n;
-      if (n > 0) for_returned<NT>(p, sh, col, false, [&](int page) { p.free_pages[at++] = page; });
-      base += all;
-    }
-    if (x < x1) {
-      const int r0 = col.b * p.beams;
-      const int* old = sh.stage + tid;
-      for (int i = 0; i < p.beams; ++i) {
-        const int r = r0 + i, j = sh.parent[r];
-        int page = -1;
-        if (j >= 0 && sh.rank[r] < top) {
-          const int len = sh.len[r0 + j], full = len / kPageSize;
-          if (col.c == full && sh.rank[r] >= 0) continue;
-          if (col.c < full || (col.c == full && len % kPageSize)) page = old[j * NT];
-        }
-        const bool had = col.c < sh.own[r];
-        if (had ? page != old[i * NT] : page != -1) p.page_table[(int64_t)r * p.width + col.c] = page;
+  const bool once = passes == 1;  // the pass is still in the registers
+  for (int t = tile0; t < tile1 || (spread && t == tile0); ++t) {
+    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_columns(p, sh, t * 32 + lane, columns, list) : 0;
+    Entry next = once ? e : entry(k_begin);
+    for (int k0 = k_begin; k0 < k_end; k0 += step) {
+      if (!once) {
+        e = next;
+        next = entry(k0 + step);
+        find_returned(p, e, false);
       }
+      const uint32_t goes = __ballot_sync(0xffffffffu, e.back);
+      if (e.back) p.free_pages[base + __popc(goes & ((1u << lane) - 1u))] = e.page;
+      base += __popc(goes);
+      const int j = e.b >= 0 ? sh.parent[e.r] : -1, first = lane >> p.row_bits << p.row_bits;
+      const int from = __shfl_sync(0xffffffffu, e.page, first + max(j, 0));
+      if (e.b < 0) continue;
+      int page = -1;
+      const int rank = sh.rank[e.r];
+      if (j >= 0 && rank < top) {
+        const int len = sh.len[e.b * p.beams + j], full = len / kPageSize;
+        if (e.c == full && rank >= 0) continue;
+        if (e.c < full || (e.c == full && len % kPageSize)) page = from;
+      }
+      if (e.has ? page != e.page : page != -1) p.page_table[(int64_t)e.r * p.width + e.c] = page;
+    }
+    __syncwarp();
+    if (spread) break;
+  }
+  if (asked > top && !direct) {  // rows are emptied: their entries of columns that would stay, too
+    __syncthreads();
+    for (int t = tile0; t < tile1; ++t) {
+      const int x = t * 32 + lane;
+      if (x >= columns) break;
+      const Column col = column_of(p, sh, x);
+      if (!stays(p, sh, col)) continue;
+      for (int r = col.b * p.beams; r < (col.b + 1) * p.beams; ++r)
+        if (sh.rank[r] >= top) p.page_table[(int64_t)r * p.width + col.c] = -1;
     }
   }
   if (back > 0) {
@@ -326,7 +446,7 @@ cudaError_t launch(const BeamParams& p, int ctas, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev >= 64 || !set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(beam_tables_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(226 * 1024));
+                                         160 * 1024);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(beam_tables_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -342,7 +462,7 @@ cudaError_t launch(const BeamParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = shared_bytes(p.batch, p.beams, NT);
+  cfg.dynamicSmemBytes = shared_bytes(p.batch, p.beams);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
@@ -377,13 +497,14 @@ extern "C" vg_status vg_beam_tables(const int32_t* parents, int batch, int beams
   p.error_flag = error_flag;
   p.batch = batch;
   p.beams = beams;
+  while ((1 << p.row_bits) < beams) ++p.row_bits;
   p.width = max_pages_per_seq;
   p.num_pages = num_pages;
   p.free_capacity = free_capacity;
   const int64_t columns = (int64_t)batch * max_pages_per_seq;  // at most
   int ctas = 1;
   while (ctas < kMaxCluster && (int64_t)ctas * kThreads < columns) ctas *= 2;
-  const cudaError_t e = batch * beams <= kFewThreads && columns <= 4 * kFewThreads
+  const cudaError_t e = batch * beams <= kFewThreads && columns <= kFewThreads
                             ? launch<kFewThreads>(p, 1, stream)
                             : launch<kThreads>(p, ctas, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
