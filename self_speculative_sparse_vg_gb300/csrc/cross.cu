@@ -16,8 +16,13 @@
 //    a chained kernel merges.
 //  * Two softmax warpgroups, one row per thread, each with its own S (128 fp32
 //    columns of tensor memory, P written back over it in 16 bits) and O.  A unit
-//    of one row tile (single tokens, beams, verify rows) gives both the same
-//    rows and alternate state tiles.
+//    of one row tile gives both the same rows and alternate state tiles.
+//  * Units of at most 32 rows (single tokens, beams, verify rows) would leave a
+//    tile's 128 columns to the one warp that holds their lanes.  Their Q is
+//    laid four times into the row tile, so that each warp of a warpgroup finds
+//    the rows' scores in its own lanes and takes 32 columns; the warps exchange
+//    the rows' maxima and write P to shared memory, whence the product with V
+//    reads it.
 //  * States lie in rows of a projection, so a tile of K or V of one head is one
 //    TMA box of 128 rows (128-byte swizzle) into a ring of stages.
 //  * All rows of a unit attend the same states.  Tiles with states that are not
@@ -68,6 +73,7 @@ struct Unit {
   int h;
   int kt0, kt1;       // state tiles of this CTA; kt0 == kt1: no more units
   int two;            // two row tiles (else one, state tiles alternate)
+  int narrow;         // at most 32 rows, four times in the row tile
   int part;           // partial slot of the workspace, -1: writes its rows
 };
 
@@ -78,9 +84,17 @@ struct CrossLayout {
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kStageBytes = kBlocks * kBlockBytes;
   static constexpr int kStages = HD == 128 ? 5 : 10;
-  static constexpr int kRing = 2 * kStageBytes;        // behind two row tiles of Q
+  // P of units of few rows, [warpgroup][64-column block][32 rows][128 bytes], and the
+  // warps' exchange: in the place of the second row tile of Q, if that has room
+  static constexpr int kPBlockBytes = 32 * 128;
+  static constexpr int kPBytes = 2 * kPBlockBytes;
+  static constexpr int kP = HD == 128 ? kStageBytes : 2 * kStageBytes;
+  static constexpr int kExchange = kP + 2 * kPBytes;
+  // behind two row tiles of Q.  (The product reads 128 rows of P, of which 32 are
+  // there: what follows is the other P and the ring, and goes to unused lanes.)
+  static constexpr int kRing = HD == 128 ? 2 * kStageBytes : kExchange + 2048;
   static constexpr int kBars = kRing + kStages * kStageBytes;
-  static constexpr int kBarCount = 3 * kStages + 15;
+  static constexpr int kBarCount = 3 * kStages + 17;
   static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
   static constexpr int kTmemAt = kUnits + 2 * 48;
   static constexpr int kMl = kTmemAt + 16;
@@ -101,6 +115,7 @@ struct CrossBars {
   // `empty`: its products are done.
   uint64_t *full, *landed, *empty;         // [stages]
   uint64_t *sfull, *pfull, *ofull;         // [2]: S, P, all of O of a warpgroup
+  uint64_t *xmax;                          // [2]: the warps' maxima of a unit of few rows
   uint64_t *qfull, *qempty, *ufull, *uempty, *xfull, *xdone, *drain;
 };
 
@@ -115,11 +130,12 @@ __device__ __forceinline__ CrossBars cross_bars(uint64_t* b, int stages) {
   r.ofull = b + 4;
   r.ufull = b + 6;
   r.uempty = b + 8;
-  r.qfull = b + 10;
-  r.qempty = b + 11;
-  r.xfull = b + 12;
-  r.xdone = b + 13;
-  r.drain = b + 14;
+  r.xmax = b + 10;
+  r.qfull = b + 12;
+  r.qempty = b + 13;
+  r.xfull = b + 14;
+  r.xdone = b + 15;
+  r.drain = b + 16;
   return r;
 }
 
@@ -151,7 +167,7 @@ __device__ __forceinline__ long long unit_length(int ntok, int len, int tu) {
 // A unit's state tiles that end before offset y of its length; a CTA whose
 // share holds [y0, y1) of it takes tiles [tiles_before(y0), tiles_before(y1)).
 __device__ __forceinline__ int tiles_before(long long y, int cost) {
-  return y <= kUnitCost ? 0 : (int)((y - kUnitCost) / cost);
+  return y <= kUnitCost ? 0 : (int)quotient(y - kUnitCost, cost);
 }
 
 // Whether tile kt may hold states that are not attended.
@@ -180,7 +196,7 @@ __device__ __forceinline__ uint32_t mask_word(uint32_t bytes, int w) {
 // One warp of a warpgroup through all units of the CTA.
 template <int HD, bool F16>
 __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBars& bars, const Unit* units,
-                                             float2* ml_s, uint32_t tmem, int wg, int warp, int lane) {
+                                             float2* ml_s, uint8_t* smem, uint32_t tmem, int wg, int warp, int lane) {
   using Lay = CrossLayout<HD>;
   const int g = p.group, tt = kTile / g;
   const int r = (warp & 3) * 32 + lane;  // row within the tile
@@ -188,7 +204,10 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
   const uint32_t scol = trow + Lay::kSCol + wg * kTile;
   const uint32_t ocol = trow + Lay::kOCol + wg * HD;
   const int tok_r = r / g, head_r = r - tok_r * g;
-  uint32_t sc = 0, oc = 0, xc = 0;
+  uint32_t sc = 0, oc = 0, xc = 0, mc = 0;
+  const int quarter = warp & 3;  // of a tile's columns, for few rows
+  float* maxima = reinterpret_cast<float*>(smem + Lay::kExchange) + wg * 256 + lane;  // [2][4][32]
+  uint8_t* p_row = smem + Lay::kP + wg * Lay::kPBytes + (quarter >> 1) * Lay::kPBlockBytes + lane * 128;
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
     if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
@@ -201,7 +220,87 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
     const int step = un.two ? 1 : 2;
     const int end = un.kt1;
     float m_used = -INFINITY, lsum = 0.f;
-    for (int kt = first; kt < end; kt += step) {
+    // the four warps' values of this lane's row, joined
+    auto exchange = [&](float v, auto join, float& all) {
+      float* at = maxima + (mc & 1) * 128;
+      at[quarter * 32] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.xmax[wg]);
+      if (!wait_phase_warp(&bars.xmax[wg], mc & 1, p)) return false;
+      ++mc;
+      all = join(join(at[0], at[32]), join(at[64], at[96]));
+      return true;
+    };
+    for (int kt = first; un.narrow && kt < end; kt += 2) {
+      const bool partly = checked_tile(p, un.len, kt);
+      const uint32_t attended = partly ? mask_bytes(p, un.start, un.len, kt, lane) : 0x01010101u;
+      if (!wait_phase_warp(&bars.sfull[wg], sc & 1, p)) return;
+      ++sc;
+      tc_fence_after();
+      float s[32];
+      tmem_ld32(scol + quarter * 32, s);
+      if (partly) {
+        const uint32_t keep = mask_word(attended, quarter);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!((keep >> j) & 1u)) s[j] = -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx[j] = fmaxf(s[j], s[j + 4]);
+#pragma unroll
+      for (int j = 8; j < 32; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[j + k], s[j + k + 4]);
+      float m_tile;
+      if (!exchange(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2,
+                    [](float a, float b) { return fmaxf(a, b); }, m_tile))
+        return;
+      const bool need = m_tile > m_used + kRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        const float mn = need ? m_tile : m_used;
+        if (kt != first) {  // P(t - 1) V is done: S(t) was issued after it
+          const float corr = mn == -INFINITY ? 1.f : ex2(m_used - mn);
+          lsum *= corr;
+          if (quarter == 0) {  // O is in the first warp's lanes
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tmem_ld16(ocol + c, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= corr;
+              tmem_st16(ocol + c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        m_used = mn;
+      }
+      const float nref = -safe_ref(m_used);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = ex2(fmaf(s[8 * i + 2 * j], p.scale_log2, nref));
+          const float b = ex2(fmaf(s[8 * i + 2 * j + 1], p.scale_log2, nref));
+          w[j] = pack2<F16>(a, b);
+          sum += a + b;
+        }
+        const int ch = (4 * quarter + i) & 7;
+        *reinterpret_cast<uint4*>(p_row + ((ch ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pfull[wg]);
+      lsum += sum;
+    }
+    if (un.narrow && end > first &&
+        !exchange(lsum, [](float a, float b) { return a + b; }, lsum))
+      return;
+    for (int kt = un.narrow ? end : first; kt < end; kt += step) {
       // read before the wait, so that the mask is there with the scores
       const bool partly = checked_tile(p, un.len, kt);
       const uint32_t attended = rows && partly ? mask_bytes(p, un.start, un.len, kt, lane) : 0x01010101u;
@@ -387,7 +486,7 @@ template <int HD, bool F16>
 struct MmaIssuer {
   using Lay = CrossLayout<HD>;
   const CrossBars& bars;
-  uint32_t tmem, ring_lo, q_lo, v_lo;  // low descriptor words of stage 0 and of Q
+  uint32_t tmem, ring_lo, q_lo, v_lo, p_lo;  // low descriptor words of stage 0, Q and P
   static constexpr uint32_t kTypes = F16 ? (1u << 7) | (1u << 10) : 0u;  // fp16 operands: the bf16 bits off
   static constexpr uint32_t kIdQk = umma_idesc_bf16(kTile, kTile, 0, 0) ^ kTypes;
   static constexpr uint32_t kIdPv = umma_idesc_bf16(kTile, HD, 0, 1) ^ kTypes;
@@ -412,6 +511,14 @@ struct MmaIssuer {
       umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
                          v + ks * (16 * 128 >> 4), kHi, kIdPv, accumulate || ks > 0);
   }
+  // the same with P in shared memory
+  __device__ __forceinline__ void pv_few(int wg, uint32_t stage, bool accumulate) {
+    const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4), a = p_lo + wg * (Lay::kPBytes >> 4);
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)
+      umma_bf16_elect(tmem + Lay::kOCol + wg * HD, a + (((ks >> 2) * Lay::kPBlockBytes + (ks & 3) * 32) >> 4), kHi,
+                      v + ks * (16 * 128 >> 4), kHi, kIdPv, accumulate || ks > 0);
+  }
 };
 
 template <int HD, bool F16>
@@ -420,7 +527,7 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
   using Lay = CrossLayout<HD>;
   constexpr uint32_t NST = Lay::kStages;
   MmaIssuer<HD, F16> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
-                         umma_desc_lo(ring, Lay::kBlockBytes)};
+                         umma_desc_lo(ring, Lay::kBlockBytes), umma_desc_lo(q + Lay::kP, 16)};
   uint32_t pc = 0;            // parities of the warpgroups' next P
   // next K's and V's ring stage and parity; entries are K(0), V(0), K(1) ...
   uint32_t sk = 0, pk = 0, sv = 1, pv = 0;
@@ -434,18 +541,22 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
     }
   };
   // O(wg) (+)= P V
-  auto pv_product = [&](int wg, uint32_t st, bool accumulate) {
+  auto pv_product = [&](int wg, uint32_t st, bool accumulate, bool few = false) {
     const uint32_t par = (pc >> wg) & 1;
     pc ^= 1u << wg;
     if (!wait_phase_warp(&bars.pfull[wg], par, p)) return false;
     tc_fence_after();
-    mma.pv(wg, st, accumulate);
+    if (few)
+      mma.pv_few(wg, st, accumulate);
+    else
+      mma.pv(wg, st, accumulate);
     return true;
   };
   for (uint32_t u = 0;; ++u) {
     const int slot = u & 1;
     if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return false;
     const int kt0 = same(units[slot].kt0), kt1 = same(units[slot].kt1), two = same(units[slot].two);
+    const bool few = same(units[slot].narrow) != 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.uempty[slot]);
     if (kt0 == kt1) return true;
@@ -492,7 +603,7 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
       if (n <= 2) umma_commit_elect(bars.qempty);
       for (int j = 0; j < n; ++j) {
         const int wg = j & 1;
-        if (!wait(&bars.full[sv], pv) || !pv_product(wg, sv, j > 1)) return false;
+        if (!wait(&bars.full[sv], pv) || !pv_product(wg, sv, j > 1, few)) return false;
         if (j >= n - 2) umma_commit_elect(&bars.ofull[wg]);
         umma_commit_elect(&bars.empty[sv]);
         next(sv, pv);
@@ -652,116 +763,159 @@ __device__ __forceinline__ Share find_share(const CrossParams& p, const Sequence
 
 // ----------------------------------------------------------------- producer
 // Walks the CTA's units, publishes them and streams their Q, K and V; one lane.
-// On a wait that was given up it stops, then waits (bounded) for its own copies.
+// K and V do not wait for room for Q: it is looked for before each of them and
+// while they wait for a stage.  On a wait that was given up the lane stops, then
+// waits (bounded) for its own copies.
 template <int HD>
-__device__ __forceinline__ void producer_role(const CrossParams& p, const CrossBars& bars, const Share& s,
-                                              const CUtensorMap& tmq, const CUtensorMap& tmk,
-                                              const CUtensorMap& tmv, Unit* units, uint8_t* smem) {
+struct Producer {
   using Lay = CrossLayout<HD>;
-  constexpr int NST = Lay::kStages;
-  const int g = p.group, tt = kTile / g, tu = 2 * tt;
-  uint8_t* ring = smem + Lay::kRing;
-  int e = s.e, h = s.h, rt = s.rt, kt0 = s.kt0;
-  long long at = s.unit_at;  // line position of the current unit's first tile
-  Sequence seq = s.seq;
-  uint32_t ri = 0, u = 0, on_landed = 0, landed = 0;  // bits: last load of a stage, its parity
-  bool live = true, q_armed = false;
-  MergeUnit cut = {};
-  while (live) {
-    const int ntok = min(tu, seq.n - rt * tu), cost = tile_cost(ntok, tu);
-    // its next state tile ends in the share
-    const bool more = e >= 0 && at + kUnitCost + (long long)cost * (kt0 + 1) <= s.x1;
-    const int slot = u & 1;
-    if (u >= 2 && !wait_phase(&bars.uempty[slot], ((u >> 1) - 1) & 1, p)) {
-      live = false;
-      break;
-    }
-    Unit un = {};
-    if (more) {
-      un.tok0 = seq.q0 + rt * tu;
-      un.ntok = ntok;
-      un.start = seq.start;
-      un.len = seq.len;
-      un.h = h;
-      un.two = un.ntok > tt;
-      const int tiles = state_tiles(seq.len);
-      un.kt0 = kt0;
-      un.kt1 = min(tiles, tiles_before(s.x1 - at, cost));
-      un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
-      at += kUnitCost + (long long)cost * tiles;  // the next unit's
-      if (kt0 == 0 && un.kt1 < tiles) {
-        cut.parts = (int)quotient(at - 1, s.share) - (int)blockIdx.x + 1;
-        cut.tok0 = un.tok0;
-        cut.ntok = un.ntok;
-        cut.h = h;
+  const CrossParams& p;
+  const CrossBars& bars;
+  const CUtensorMap &tmq, &tmf, &tmk, &tmv;
+  uint8_t* smem;
+  Unit q_unit = {};       // whose Q is to come, if
+  bool q_wanted = false;
+  bool q_all = false;     // once the unit before is done with, P too (else with its Q)
+  uint32_t q_sent = 0;    // units whose Q was sent
+
+  __device__ __forceinline__ bool q_has_room() const {
+    if (q_sent == 0) return true;
+    const uint32_t before = q_sent - 1;
+    return q_all ? mbar_test_wait(&bars.uempty[before & 1], (before >> 1) & 1) : mbar_test_wait(bars.qempty, before & 1);
+  }
+  __device__ __forceinline__ void send_q() {
+    const int g = p.group, tt = kTile / g;
+    const int copies = q_unit.narrow ? 4 : q_unit.two ? 2 : 1, tokens = q_unit.narrow ? 32 / g : tt;
+    mbar_arrive_expect_tx(bars.qfull, copies * Lay::kBlocks * tokens * g * 128);
+    for (int t = 0; t < copies; ++t)
+      for (int x = 0; x < Lay::kBlocks; ++x) {
+        uint8_t* dst = smem + x * Lay::kBlockBytes + t * (q_unit.narrow ? 32 * 128 : Lay::kStageBytes);
+        tma_load_3d(dst, q_unit.narrow ? &tmf : &tmq, bars.qfull, x * 64, q_unit.h * g,
+                    q_unit.tok0 + (q_unit.narrow ? 0 : t * tt));
       }
-    }
-    q_armed = false;
-    units[slot] = un;
-    mbar_arrive(&bars.ufull[slot]);
-    if (!more) break;
-    for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
+    q_wanted = false;
+    ++q_sent;
+  }
+  // Waits for the phase of `bar` (a stage, or null), or for Q's room if that is
+  // wanted and `q_too`; sends Q when there is room.  Bounded as wait_phase.
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, bool q_too) {
+    uint64_t t0 = 0;
+    while (true) {
 #pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        if (v == 1 && kt == un.kt0) {  // Q, once the unit before has made its scores
-          if (u >= 1 && !wait_phase(bars.qempty, (u - 1) & 1, p)) {
+      for (int i = 0; i < p.polls; ++i) {
+        if (q_wanted && q_has_room()) send_q();
+        const bool there = bar == nullptr || (q_wanted || p.polls == 1 ? mbar_test_wait(bar, parity)
+                                                                       : mbar_try_wait(bar, parity));
+        if (there && !(q_too && q_wanted)) return true;
+      }
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > p.wait_ns) flag_error(p.error_flag, VG_DEVERR_TIMEOUT);
+      if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+
+  __device__ __forceinline__ void run(const Share& s, Unit* units) {
+    constexpr int NST = Lay::kStages;
+    const int tt = kTile / p.group, tu = 2 * tt;
+    uint8_t* ring = smem + Lay::kRing;
+    int e = s.e, h = s.h, rt = s.rt, kt0 = s.kt0;
+    long long at = s.unit_at;  // line position of the current unit's first tile
+    Sequence seq = s.seq;
+    uint32_t ri = 0, u = 0, on_landed = 0, landed = 0;  // bits: last load of a stage, its parity
+    bool live = true, last_narrow = false;
+    MergeUnit cut = {};
+    while (true) {
+      const int ntok = min(tu, seq.n - rt * tu), cost = tile_cost(ntok, tu);
+      // its next state tile ends in the share
+      const bool more = e >= 0 && at + kUnitCost + (long long)cost * (kt0 + 1) <= s.x1;
+      const int slot = u & 1;
+      if (u >= 2 && !wait(&bars.uempty[slot], ((u >> 1) - 1) & 1, false)) {
+        live = false;
+        break;
+      }
+      Unit un = {};
+      if (more) {
+        un.tok0 = seq.q0 + rt * tu;
+        un.ntok = ntok;
+        un.start = seq.start;
+        un.len = seq.len;
+        un.h = h;
+        un.two = un.ntok > tt;
+        un.narrow = un.ntok * p.group <= 32;
+        const int tiles = state_tiles(seq.len);
+        un.kt0 = kt0;
+        un.kt1 = min(tiles, tiles_before(s.x1 - at, cost));
+        un.part = kt0 > 0 ? 2 * (int)blockIdx.x : un.kt1 < tiles ? 2 * (int)blockIdx.x + 1 : -1;
+        at += kUnitCost + (long long)cost * tiles;  // the next unit's
+        if (kt0 == 0 && un.kt1 < tiles) {
+          cut.parts = (int)quotient(at - 1, s.share) - (int)blockIdx.x + 1;
+          cut.tok0 = un.tok0;
+          cut.ntok = un.ntok;
+          cut.h = h;
+        }
+      }
+      units[slot] = un;
+      mbar_arrive(&bars.ufull[slot]);
+      if (!more) break;
+      q_wanted = true;
+      q_unit = un;
+      q_all = un.two && last_narrow && Lay::kP < 2 * Lay::kStageBytes;
+      last_narrow = un.narrow;
+      for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t st = ri % NST;
+          if (!wait(ri >= NST ? &bars.empty[st] : nullptr, ((ri / NST) - 1) & 1, false)) {
             live = false;
             break;
           }
-          q_armed = true;
-          mbar_arrive_expect_tx(bars.qfull, (un.two ? 2 : 1) * Lay::kBlocks * tt * g * 128);
-          for (int t = 0; t < (un.two ? 2 : 1); ++t)
-            for (int x = 0; x < Lay::kBlocks; ++x)
-              tma_load_3d(smem + t * Lay::kStageBytes + x * Lay::kBlockBytes, &tmq, bars.qfull, x * 64,
-                          h * g, un.tok0 + t * tt);
+          uint64_t* bar = &(v && checked_tile(p, un.len, kt) ? bars.landed : bars.full)[st];
+          if (bar == &bars.full[st]) mbar_arrive(bar);  // for the second checker
+          mbar_arrive_expect_tx(bar, Lay::kStageBytes);
+          tma_load_4d(ring + st * Lay::kStageBytes, v ? &tmv : &tmk, bar, 0, un.start + kt * kTile, 0, h);
+          on_landed &= ~(1u << st);
+          if (bar == &bars.landed[st]) {
+            on_landed |= 1u << st;
+            landed ^= 1u << st;
+          }
+          ++ri;
         }
-        const uint32_t st = ri % NST;
-        if (ri >= NST && !wait_phase(&bars.empty[st], ((ri / NST) - 1) & 1, p)) {
-          live = false;
-          break;
+      }
+      if (live && !wait(nullptr, 0, true)) live = false;
+      if (!live) break;
+      ++u;
+      kt0 = 0;
+      if (++rt * tu >= seq.n) {
+        rt = 0;
+        if (++h == p.num_kv_heads) {
+          h = 0;
+          do {
+            if (++e >= p.batch) break;
+            sequence_of(p, e, seq);
+          } while (seq.n == 0);
         }
-        uint64_t* bar = &(v && checked_tile(p, un.len, kt) ? bars.landed : bars.full)[st];
-        if (bar == &bars.full[st]) mbar_arrive(bar);  // for the second checker
-        mbar_arrive_expect_tx(bar, Lay::kStageBytes);
-        tma_load_4d(ring + st * Lay::kStageBytes, v ? &tmv : &tmk, bar, 0, un.start + kt * kTile, 0, h);
-        on_landed &= ~(1u << st);
-        if (bar == &bars.landed[st]) {
-          on_landed |= 1u << st;
-          landed ^= 1u << st;
-        }
-        ++ri;
       }
     }
-    ++u;
-    kt0 = 0;
-    if (++rt * tu >= seq.n) {
-      rt = 0;
-      if (++h == p.num_kv_heads) {
-        h = 0;
-        do {
-          if (++e >= p.batch) break;
-          sequence_of(p, e, seq);
-        } while (seq.n == 0);
+    p.merge[blockIdx.x] = cut;
+    if (!live) {
+      for (uint32_t i = ri > NST ? ri - NST : 0; i < ri; ++i) {
+        const uint32_t st = i % NST;
+        if ((on_landed >> st) & 1)
+          mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
+        else
+          mbar_wait(&bars.full[st], (i / NST) & 1);
       }
+      if (q_sent > 0) mbar_wait(bars.qfull, (q_sent - 1) & 1);
     }
   }
-  p.merge[blockIdx.x] = cut;
-  if (!live) {
-    for (uint32_t i = ri > NST ? ri - NST : 0; i < ri; ++i) {
-      const uint32_t st = i % NST;
-      if ((on_landed >> st) & 1)
-        mbar_wait(&bars.landed[st], ((landed >> st) & 1) ^ 1);
-      else
-        mbar_wait(&bars.full[st], (i / NST) & 1);
-    }
-    if (u > 0 && q_armed) mbar_wait(bars.qfull, (u - 1) & 1);
-  }
-}
+};
 
 template <int HD, bool F16>
 __global__ void __launch_bounds__(kCrossThreads, 1)
-    cross_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                 const __grid_constant__ CUtensorMap tmv, const CrossParams p) {
+    cross_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmf,
+                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                 const CrossParams p) {
   using Lay = CrossLayout<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -772,6 +926,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
   // what needs no input comes before the wait for the previous kernel
   if (warp == kProducer && lane == 0) {
     tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmf);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
     for (int i = 0; i < Lay::kStages; ++i) {
@@ -783,6 +938,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
       mbar_init(&bars.sfull[i], 1);
       mbar_init(&bars.pfull[i], 4);
       mbar_init(&bars.ofull[i], 1);
+      mbar_init(&bars.xmax[i], 4);
       mbar_init(&bars.ufull[i], 1);
       mbar_init(&bars.uempty[i], 8 + 1 + 2);
     }
@@ -813,12 +969,15 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   }
   if (warp < 8) {
-    softmax_role<HD, F16>(p, bars, units, ml, tmem, warp >> 2, warp, lane);
+    softmax_role<HD, F16>(p, bars, units, ml, smem, tmem, warp >> 2, warp, lane);
   } else if (warp == kProducer) {
     const Share share = find_share(p, tab, lane);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) producer_role<HD>(p, bars, share, tmq, tmk, tmv, units, smem);
+    if (lane == 0) {
+      Producer<HD> producer{p, bars, tmq, tmf, tmk, tmv, smem};
+      producer.run(share, units);
+    }
   } else if (warp == kMma) {
     const uint32_t base = smem_u32(smem);
     if (!mma_role<HD, F16>(p, bars, units, tmem, base + Lay::kRing, base, lane)) {
@@ -855,7 +1014,7 @@ CrossPlan make_cross_plan(int num_tokens, int group, int head_dim) {
 }
 
 template <int HD, bool F16>
-cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk,
+cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUtensorMap& tf, const CUtensorMap& tk,
                          const CUtensorMap& tv, const CrossParams& p, cudaStream_t stream) {
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -876,7 +1035,7 @@ cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUten
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_kernel<HD, F16>, tq, tk, tv, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_kernel<HD, F16>, tq, tf, tk, tv, p);
   if (e != cudaSuccess) return e;
   const MergeParams m = {p.out,        p.lse,         p.part_o, p.part_ml, p.merge,
                          p.out_stride, p.num_q_heads, p.group,  p.rows};
@@ -931,12 +1090,14 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   // without states there is nothing to map: Q stands in (a tile that is loaded
   // for rows without states is never used)
   const bool none = num_states == 0;
-  CUtensorMap tq, tk, tv;
+  // (Q of few rows: as many tokens as have 32)
+  CUtensorMap tq, tf, tk, tv;
   if (!head_tile_tensor_map(none ? q : k, none ? num_tokens : num_states, none ? num_q_heads : num_kv_heads,
                             head_dim, none ? q_stride : k_stride, kTile, &tk) ||
       !head_tile_tensor_map(none ? q : v, none ? num_tokens : num_states, none ? num_q_heads : num_kv_heads,
                             head_dim, none ? q_stride : v_stride, kTile, &tv) ||
-      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, kTile / g, &tq))
+      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, kTile / g, &tq) ||
+      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, g > 32 ? 1 : 32 / g, &tf))
     return VG_ERR_LAUNCH;
   CrossParams p = {};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -962,9 +1123,9 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   p.group = g;
   p.rows = pl.rows;
   const bool f16 = type == VG_TYPE_FP16;
-  const cudaError_t e = head_dim == 128 ? (f16 ? launch_cross<128, true>(pl, tq, tk, tv, p, stream)
-                                               : launch_cross<128, false>(pl, tq, tk, tv, p, stream))
-                                        : (f16 ? launch_cross<64, true>(pl, tq, tk, tv, p, stream)
-                                               : launch_cross<64, false>(pl, tq, tk, tv, p, stream));
+  const cudaError_t e = head_dim == 128 ? (f16 ? launch_cross<128, true>(pl, tq, tf, tk, tv, p, stream)
+                                               : launch_cross<128, false>(pl, tq, tf, tk, tv, p, stream))
+                                        : (f16 ? launch_cross<64, true>(pl, tq, tf, tk, tv, p, stream)
+                                               : launch_cross<64, false>(pl, tq, tf, tk, tv, p, stream));
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }
