@@ -23,6 +23,10 @@
 //    the rows' scores in its own lanes and takes 32 columns; the warps exchange
 //    the rows' maxima and write P to shared memory, whence the product with V
 //    reads it.
+//  * Where most sequences have so few rows and heads are 64 wide, a unit is a pair
+//    of neighbouring KV heads, one for each warpgroup: a state's 128 bytes of one
+//    head come from HBM at 4.5 TB/s, 256 bytes of two at 6.5 (16 heads, 6144
+//    states of 64 requests).
 //  * States lie in rows of a projection, so a tile of K or V of one head is one
 //    TMA box of 128 rows (128-byte swizzle) into a ring of stages.
 //  * All rows of a unit attend the same states.  Tiles with states that are not
@@ -64,6 +68,9 @@ struct CrossParams {
   int polls;           // polls of a wait between two looks at the timer
   float scale_log2;
   int batch, num_tokens, num_states, num_q_heads, num_kv_heads, group, rows;
+  int heads;          // of the line: KV heads, or pairs of them
+  int tile_tokens, few_tokens, unit_tokens;  // tokens of a row tile, of 32 rows, and of a unit
+  uint32_t by_unit_tokens;       // ceil(2^32 / unit_tokens), 0 for 1
 };
 
 // A unit of work as the CTA's roles see it.
@@ -77,22 +84,22 @@ struct Unit {
   int part;           // partial slot of the workspace, -1: writes its rows
 };
 
-template <int HD>
+template <int HD, bool PAIR>
 struct CrossLayout {
-  static constexpr int kBlocks = HD / 64;              // 64-dim blocks of a row
+  static constexpr int kBlocks = PAIR ? 2 : HD / 64;   // 64-dim blocks of a row (of a pair: its heads)
   // Q, K and V tiles: [block][row][128 bytes], as one TMA box brings them
   static constexpr int kBlockBytes = kTile * 128;
   static constexpr int kStageBytes = kBlocks * kBlockBytes;
-  static constexpr int kStages = HD == 128 ? 5 : 10;
+  static constexpr int kStages = kBlocks == 2 ? 5 : 10;
   // P of units of few rows, [warpgroup][64-column block][32 rows][128 bytes], and the
   // warps' exchange: in the place of the second row tile of Q, if that has room
   static constexpr int kPBlockBytes = 32 * 128;
   static constexpr int kPBytes = 2 * kPBlockBytes;
-  static constexpr int kP = HD == 128 ? kStageBytes : 2 * kStageBytes;
+  static constexpr int kP = kBlocks == 2 ? kStageBytes : 2 * kStageBytes;
   static constexpr int kExchange = kP + 2 * kPBytes;
   // behind two row tiles of Q.  (The product reads 128 rows of P, of which 32 are
   // there: what follows is the other P and the ring, and goes to unused lanes.)
-  static constexpr int kRing = HD == 128 ? 2 * kStageBytes : kExchange + 2048;
+  static constexpr int kRing = kBlocks == 2 ? 2 * kStageBytes : kExchange + 2048;
   static constexpr int kBars = kRing + kStages * kStageBytes;
   static constexpr int kBarCount = 3 * kStages + 17;
   static constexpr int kUnits = kBars + (kBarCount + 1) / 2 * 16;
@@ -106,7 +113,9 @@ struct CrossLayout {
     return (ch >> 3) * kBlockBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
   }
 };
-static_assert(CrossLayout<128>::kBytes <= 227 * 1024 && CrossLayout<64>::kBytes <= 227 * 1024, "");
+static_assert(CrossLayout<128, false>::kBytes <= 227 * 1024 && CrossLayout<64, false>::kBytes <= 227 * 1024 &&
+                  CrossLayout<64, true>::kBytes <= 227 * 1024,
+              "");
 static_assert(sizeof(Unit) <= 48, "");
 
 struct CrossBars {
@@ -157,17 +166,22 @@ __device__ __forceinline__ bool sequence_of(const CrossParams& p, int e, Sequenc
   return ok;
 }
 
-__device__ __forceinline__ int tile_cost(int ntok, int tu) { return 2 * ntok > tu ? kTwoCost : kOneCost; }
+__device__ __forceinline__ int tile_cost(const CrossParams& p, int ntok) {
+  return ntok > p.tile_tokens ? kTwoCost : kOneCost;
+}
 
 // Length on the line of a unit of ntok tokens: its overhead, then its tiles.
-__device__ __forceinline__ long long unit_length(int ntok, int len, int tu) {
-  return kUnitCost + (long long)tile_cost(ntok, tu) * state_tiles(len);
+__device__ __forceinline__ long long unit_length(const CrossParams& p, int ntok, int len) {
+  return kUnitCost + (long long)tile_cost(p, ntok) * state_tiles(len);
 }
 
 // A unit's state tiles that end before offset y of its length; a CTA whose
 // share holds [y0, y1) of it takes tiles [tiles_before(y0), tiles_before(y1)).
 __device__ __forceinline__ int tiles_before(long long y, int cost) {
-  return y <= kUnitCost ? 0 : (int)quotient(y - kUnitCost, cost);
+  if (y <= kUnitCost) return 0;
+  const long long z = y - kUnitCost;
+  if (z >> 32) return (int)(z / cost);
+  return cost == kTwoCost ? (int)((uint32_t)z / kTwoCost) : (int)((uint32_t)z / kOneCost);
 }
 
 // Whether tile kt may hold states that are not attended.
@@ -194,11 +208,11 @@ __device__ __forceinline__ uint32_t mask_word(uint32_t bytes, int w) {
 
 // ---------------------------------------------------------------- softmax
 // One warp of a warpgroup through all units of the CTA.
-template <int HD, bool F16>
+template <int HD, bool F16, bool PAIR>
 __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBars& bars, const Unit* units,
                                              float2* ml_s, uint8_t* smem, uint32_t tmem, int wg, int warp, int lane) {
-  using Lay = CrossLayout<HD>;
-  const int g = p.group, tt = kTile / g;
+  using Lay = CrossLayout<HD, PAIR>;
+  const int g = p.group, tt = p.tile_tokens;
   const int r = (warp & 3) * 32 + lane;  // row within the tile
   const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t scol = trow + Lay::kSCol + wg * kTile;
@@ -213,7 +227,7 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
     if (!wait_phase_warp(&bars.ufull[slot], (u >> 1) & 1, p)) return;
     const Unit un = units[slot];
     if (un.kt0 == un.kt1) return;
-    const int tok = un.two ? wg * tt + tok_r : tok_r;       // token within the unit
+    const int tok = un.two && !PAIR ? wg * tt + tok_r : tok_r;  // token within the unit
     const bool valid = tok_r < tt && tok < un.ntok;
     const bool rows = __any_sync(0xffffffffu, valid);       // a warp without rows only keeps step
     const int first = un.two ? un.kt0 : un.kt0 + wg;
@@ -231,7 +245,7 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
       all = join(join(at[0], at[32]), join(at[64], at[96]));
       return true;
     };
-    for (int kt = first; un.narrow && kt < end; kt += 2) {
+    for (int kt = first; un.narrow && kt < end; kt += step) {
       const bool partly = checked_tile(p, un.len, kt);
       const uint32_t attended = partly ? mask_bytes(p, un.start, un.len, kt, lane) : 0x01010101u;
       if (!wait_phase_warp(&bars.sfull[wg], sc & 1, p)) return;
@@ -411,8 +425,9 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
     }
     if (rows && (un.two || wg == 0)) {
       const bool direct = un.part < 0;
-      const int t = un.tok0 + tok, qh = un.h * g + head_r;
-      const int prow = (un.two ? wg * kTile : 0) + r;       // row of the partial
+      const int t = un.tok0 + tok, qh = (PAIR ? 2 * un.h + wg : un.h) * g + head_r;
+      // row of the partial
+      const int prow = PAIR ? tok_r * 2 * g + wg * g + head_r : (un.two ? wg * kTile : 0) + r;
       const float inv = direct ? (l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN) : 1.f;
       const float f_own = has ? w_own * inv : 0.f, f_other = w_other * inv;
       const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
@@ -482,9 +497,9 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
 // ------------------------------------------------------- tensor-core issue
 // The warp runs in step (every value it uses is the same in all lanes) and an
 // elected lane issues.
-template <int HD, bool F16>
+template <int HD, bool F16, bool PAIR>
 struct MmaIssuer {
-  using Lay = CrossLayout<HD>;
+  using Lay = CrossLayout<HD, PAIR>;
   const CrossBars& bars;
   uint32_t tmem, ring_lo, q_lo, v_lo, p_lo;  // low descriptor words of stage 0, Q and P
   static constexpr uint32_t kTypes = F16 ? (1u << 7) | (1u << 10) : 0u;  // fp16 operands: the bf16 bits off
@@ -495,10 +510,10 @@ struct MmaIssuer {
   // S of warpgroup `wg` = Q (row tile qt) K^T of the stage
   __device__ __forceinline__ void qk(int wg, int qt, uint32_t stage) {
     const uint32_t k = ring_lo + stage * (Lay::kStageBytes >> 4);
-    const uint32_t q = q_lo + qt * (Lay::kStageBytes >> 4);
+    const uint32_t q = q_lo + (PAIR ? 0 : qt) * (Lay::kStageBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < HD / 16; ++ks) {
-      const uint32_t at = ((ks >> 2) * Lay::kBlockBytes + (ks & 3) * 32) >> 4;
+      const uint32_t at = ((PAIR ? wg : ks >> 2) * Lay::kBlockBytes + (ks & 3) * 32) >> 4;
       umma_bf16_elect(tmem + Lay::kSCol + wg * kTile, q + at, kHi, k + at, kHi, kIdQk, ks > 0);
     }
     umma_commit_elect(&bars.sfull[wg]);
@@ -513,7 +528,8 @@ struct MmaIssuer {
   }
   // the same with P in shared memory
   __device__ __forceinline__ void pv_few(int wg, uint32_t stage, bool accumulate) {
-    const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4), a = p_lo + wg * (Lay::kPBytes >> 4);
+    const uint32_t v = v_lo + (stage * Lay::kStageBytes + (PAIR ? wg * Lay::kBlockBytes : 0) >> 4);
+    const uint32_t a = p_lo + wg * (Lay::kPBytes >> 4);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
       umma_bf16_elect(tmem + Lay::kOCol + wg * HD, a + (((ks >> 2) * Lay::kPBlockBytes + (ks & 3) * 32) >> 4), kHi,
@@ -521,12 +537,12 @@ struct MmaIssuer {
   }
 };
 
-template <int HD, bool F16>
+template <int HD, bool F16, bool PAIR>
 __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& bars, const Unit* units,
                                          uint32_t tmem, uint32_t ring, uint32_t q, int lane) {
-  using Lay = CrossLayout<HD>;
+  using Lay = CrossLayout<HD, PAIR>;
   constexpr uint32_t NST = Lay::kStages;
-  MmaIssuer<HD, F16> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
+  MmaIssuer<HD, F16, PAIR> mma{bars, tmem, umma_desc_lo(ring, 16), umma_desc_lo(q, 16),
                          umma_desc_lo(ring, Lay::kBlockBytes), umma_desc_lo(q + Lay::kP, 16)};
   uint32_t pc = 0;            // parities of the warpgroups' next P
   // next K's and V's ring stage and parity; entries are K(0), V(0), K(1) ...
@@ -546,7 +562,7 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
     pc ^= 1u << wg;
     if (!wait_phase_warp(&bars.pfull[wg], par, p)) return false;
     tc_fence_after();
-    if (few)
+    if (PAIR || few)
       mma.pv_few(wg, st, accumulate);
     else
       mma.pv(wg, st, accumulate);
@@ -578,7 +594,7 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
         // instruction cache)
 #pragma unroll 1
         for (int wg = 0; wg < 2; ++wg) {
-          if (!pv_product(wg, sv, j > 0)) return false;
+          if (!pv_product(wg, sv, j > 0, few)) return false;
           if (more)
             mma.qk(wg, wg, sk);
           else
@@ -623,13 +639,13 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
 
 // ------------------------------------------------- V rows that nobody attends
 // Warp `half` of two owns half of the dimensions of every such V tile.
-template <int HD>
+template <int HD, bool PAIR>
 __device__ __forceinline__ void check_role(const CrossParams& p, const CrossBars& bars, const Unit* units,
                                            uint8_t* ring, int half, int lane) {
-  using Lay = CrossLayout<HD>;
+  using Lay = CrossLayout<HD, PAIR>;
   constexpr int NST = Lay::kStages;
-  constexpr int CPW = HD / 16;       // 16-byte pieces of a row per warp
-  constexpr int RPI = 32 / CPW;      // rows per pass
+  constexpr int CPW = Lay::kBlocks * 4;  // 16-byte pieces of a row per warp
+  constexpr int RPI = 32 / CPW;          // rows per pass
   uint32_t tiles = 0, landed = 0;
   const int ch = half * CPW + lane % CPW, r = lane / CPW;  // piece of the row, row of the pass
   for (uint32_t u = 0;; ++u) {
@@ -673,22 +689,28 @@ struct Share {
   Sequence seq;       // the first unit's
 };
 
-__device__ __forceinline__ int row_tiles(int n, int tu) {
-  return (int)(((unsigned)n + (unsigned)tu - 1u) / (unsigned)tu);
+// Units of n tokens (a product's upper half for the quotient, put right by one).
+__device__ __forceinline__ int row_units(const CrossParams& p, int n) {
+  const uint32_t a = (uint32_t)n + (uint32_t)p.unit_tokens - 1u;
+  if (p.by_unit_tokens == 0) return (int)a;
+  uint32_t q = __umulhi(a, p.by_unit_tokens);
+  if (q * (uint32_t)p.unit_tokens > a) --q;
+  return (int)q;
 }
 
-// Length on the line of one KV head of a sequence: full units, then the last.
-__device__ __forceinline__ long long head_length(const Sequence& s, int tu) {
-  const int nrt = row_tiles(s.n, tu);
-  if (nrt == 0) return 0;
-  return (nrt - 1) * unit_length(tu, s.len, tu) + unit_length(s.n - (nrt - 1) * tu, s.len, tu);
+// Length on the line of one head of a sequence: full units, then the last.
+__device__ __forceinline__ long long head_length(const CrossParams& p, const Sequence& s) {
+  const int units = row_units(p, s.n);
+  if (units == 0) return 0;
+  return (units - 1) * unit_length(p, p.unit_tokens, s.len) +
+         unit_length(p, s.n - (units - 1) * p.unit_tokens, s.len);
 }
 
 // The sequence of this lane among the 32 from e0 on, and its length on the line.
-__device__ __forceinline__ long long sequence_length(const CrossParams& p, int e, int tu, Sequence& s) {
+__device__ __forceinline__ long long sequence_length(const CrossParams& p, int e, Sequence& s) {
   s = {};
   if (e < p.batch && !sequence_of(p, e, s) && blockIdx.x == 0) flag_error(p.error_flag, VG_DEVERR_LENGTH);
-  return head_length(s, tu) * p.num_kv_heads;
+  return head_length(p, s) * p.heads;
 }
 
 // Batches of more than 32 sequences: the CTA's warps put every sequence's
@@ -699,22 +721,20 @@ struct SequenceTable {
 };
 
 __device__ __forceinline__ void fill_sequence_table(const CrossParams& p, const SequenceTable& tab) {
-  const int tu = 2 * (kTile / p.group);
   for (int e = threadIdx.x; e < p.batch; e += kCrossThreads) {
     Sequence s;
-    tab.length[e] = sequence_length(p, e, tu, s);
+    tab.length[e] = sequence_length(p, e, s);
     tab.seq[e] = s;
   }
 }
 
 // Where the CTA's share of the line begins; found by one warp.  e < 0: no work.
 __device__ __forceinline__ Share find_share(const CrossParams& p, const SequenceTable& tab, int lane) {
-  const int tu = 2 * (kTile / p.group);
   const bool small = p.batch <= 32;
   Sequence seq = {};
   long long sum = 0, total = 0;  // running sum over the line, this lane's sequence included
   if (small) {
-    sum = warp_inclusive_sum(sequence_length(p, lane, tu, seq), lane);
+    sum = warp_inclusive_sum(sequence_length(p, lane, seq), lane);
     total = __shfl_sync(0xffffffffu, sum, 31);
   } else {
     for (int e0 = 0; e0 < p.batch; e0 += 32) {
@@ -751,12 +771,12 @@ __device__ __forceinline__ Share find_share(const CrossParams& p, const Sequence
     base = s.e > 0 ? tab.length[s.e - 1] : 0;
     s.seq = tab.seq[s.e];
   }
-  const long long per_head = head_length(s.seq, tu), full = unit_length(tu, s.seq.len, tu);
+  const long long per_head = head_length(p, s.seq), full = unit_length(p, p.unit_tokens, s.seq.len);
   s.h = (int)quotient(x0 - base, per_head);
   const long long y = x0 - base - s.h * per_head;
-  s.rt = min((int)quotient(y, full), row_tiles(s.seq.n, tu) - 1);
+  s.rt = y < full ? 0 : min((int)quotient(y, full), row_units(p, s.seq.n) - 1);
   const long long in = y - s.rt * full;
-  s.kt0 = tiles_before(in, tile_cost(min(tu, s.seq.n - s.rt * tu), tu));
+  s.kt0 = tiles_before(in, tile_cost(p, min(p.unit_tokens, s.seq.n - s.rt * p.unit_tokens)));
   s.unit_at = x0 - in;
   return s;
 }
@@ -766,9 +786,9 @@ __device__ __forceinline__ Share find_share(const CrossParams& p, const Sequence
 // K and V do not wait for room for Q: it is looked for before each of them and
 // while they wait for a stage.  On a wait that was given up the lane stops, then
 // waits (bounded) for its own copies.
-template <int HD>
+template <int HD, bool PAIR>
 struct Producer {
-  using Lay = CrossLayout<HD>;
+  using Lay = CrossLayout<HD, PAIR>;
   const CrossParams& p;
   const CrossBars& bars;
   const CUtensorMap &tmq, &tmf, &tmk, &tmv;
@@ -784,14 +804,15 @@ struct Producer {
     return q_all ? mbar_test_wait(&bars.uempty[before & 1], (before >> 1) & 1) : mbar_test_wait(bars.qempty, before & 1);
   }
   __device__ __forceinline__ void send_q() {
-    const int g = p.group, tt = kTile / g;
-    const int copies = q_unit.narrow ? 4 : q_unit.two ? 2 : 1, tokens = q_unit.narrow ? 32 / g : tt;
+    const int g = p.group, tt = p.tile_tokens;
+    const bool narrow = PAIR || q_unit.narrow;
+    const int copies = narrow ? 4 : q_unit.two ? 2 : 1, tokens = narrow ? p.few_tokens : tt;
     mbar_arrive_expect_tx(bars.qfull, copies * Lay::kBlocks * tokens * g * 128);
     for (int t = 0; t < copies; ++t)
       for (int x = 0; x < Lay::kBlocks; ++x) {
-        uint8_t* dst = smem + x * Lay::kBlockBytes + t * (q_unit.narrow ? 32 * 128 : Lay::kStageBytes);
-        tma_load_3d(dst, q_unit.narrow ? &tmf : &tmq, bars.qfull, x * 64, q_unit.h * g,
-                    q_unit.tok0 + (q_unit.narrow ? 0 : t * tt));
+        uint8_t* dst = smem + x * Lay::kBlockBytes + t * (narrow ? 32 * 128 : Lay::kStageBytes);
+        tma_load_3d(dst, narrow ? &tmf : &tmq, bars.qfull, PAIR ? 0 : x * 64,
+                    (PAIR ? 2 * q_unit.h + x : q_unit.h) * g, q_unit.tok0 + (narrow ? 0 : t * tt));
       }
     q_wanted = false;
     ++q_sent;
@@ -817,7 +838,7 @@ struct Producer {
 
   __device__ __forceinline__ void run(const Share& s, Unit* units) {
     constexpr int NST = Lay::kStages;
-    const int tt = kTile / p.group, tu = 2 * tt;
+    const int tt = p.tile_tokens, tu = p.unit_tokens;
     uint8_t* ring = smem + Lay::kRing;
     int e = s.e, h = s.h, rt = s.rt, kt0 = s.kt0;
     long long at = s.unit_at;  // line position of the current unit's first tile
@@ -826,7 +847,7 @@ struct Producer {
     bool live = true, last_narrow = false;
     MergeUnit cut = {};
     while (true) {
-      const int ntok = min(tu, seq.n - rt * tu), cost = tile_cost(ntok, tu);
+      const int ntok = min(tu, seq.n - rt * tu), cost = tile_cost(p, ntok);
       // its next state tile ends in the share
       const bool more = e >= 0 && at + kUnitCost + (long long)cost * (kt0 + 1) <= s.x1;
       const int slot = u & 1;
@@ -841,8 +862,8 @@ struct Producer {
         un.start = seq.start;
         un.len = seq.len;
         un.h = h;
-        un.two = un.ntok > tt;
-        un.narrow = un.ntok * p.group <= 32;
+        un.two = PAIR || un.ntok > tt;
+        un.narrow = PAIR || un.ntok <= p.few_tokens;
         const int tiles = state_tiles(seq.len);
         un.kt0 = kt0;
         un.kt1 = min(tiles, tiles_before(s.x1 - at, cost));
@@ -860,7 +881,7 @@ struct Producer {
       if (!more) break;
       q_wanted = true;
       q_unit = un;
-      q_all = un.two && last_narrow && Lay::kP < 2 * Lay::kStageBytes;
+      q_all = !PAIR && un.two && last_narrow && Lay::kP < 2 * Lay::kStageBytes;
       last_narrow = un.narrow;
       for (int kt = un.kt0; kt < un.kt1 && live; ++kt) {
 #pragma unroll 1
@@ -888,7 +909,7 @@ struct Producer {
       kt0 = 0;
       if (++rt * tu >= seq.n) {
         rt = 0;
-        if (++h == p.num_kv_heads) {
+        if (++h == p.heads) {
           h = 0;
           do {
             if (++e >= p.batch) break;
@@ -911,12 +932,12 @@ struct Producer {
   }
 };
 
-template <int HD, bool F16>
+template <int HD, bool F16, bool PAIR>
 __global__ void __launch_bounds__(kCrossThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmf,
                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const CrossParams p) {
-  using Lay = CrossLayout<HD>;
+  using Lay = CrossLayout<HD, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CrossBars bars = cross_bars(reinterpret_cast<uint64_t*>(smem + Lay::kBars), Lay::kStages);
@@ -969,24 +990,24 @@ __global__ void __launch_bounds__(kCrossThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   }
   if (warp < 8) {
-    softmax_role<HD, F16>(p, bars, units, ml, smem, tmem, warp >> 2, warp, lane);
+    softmax_role<HD, F16, PAIR>(p, bars, units, ml, smem, tmem, warp >> 2, warp, lane);
   } else if (warp == kProducer) {
     const Share share = find_share(p, tab, lane);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      Producer<HD> producer{p, bars, tmq, tmf, tmk, tmv, smem};
+      Producer<HD, PAIR> producer{p, bars, tmq, tmf, tmk, tmv, smem};
       producer.run(share, units);
     }
   } else if (warp == kMma) {
     const uint32_t base = smem_u32(smem);
-    if (!mma_role<HD, F16>(p, bars, units, tmem, base + Lay::kRing, base, lane)) {
+    if (!mma_role<HD, F16, PAIR>(p, bars, units, tmem, base + Lay::kRing, base, lane)) {
       // abandoned: wait (bounded) for every tensor-core operation issued
       umma_commit_elect(bars.drain);
       if (lane == 0) mbar_wait(bars.drain, 0);
     }
   } else {
-    check_role<HD>(p, bars, units, smem + Lay::kRing, warp - kChecker, lane);
+    check_role<HD, PAIR>(p, bars, units, smem + Lay::kRing, warp - kChecker, lane);
   }
   __syncwarp();
   tc_fence_before();
@@ -1013,7 +1034,7 @@ CrossPlan make_cross_plan(int num_tokens, int group, int head_dim) {
   return pl;
 }
 
-template <int HD, bool F16>
+template <int HD, bool F16, bool PAIR>
 cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUtensorMap& tf, const CUtensorMap& tk,
                          const CUtensorMap& tv, const CrossParams& p, cudaStream_t stream) {
   static bool attr_set[64] = {false};
@@ -1021,7 +1042,7 @@ cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUten
   cudaGetDevice(&dev);
   if (dev >= 64 || !attr_set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        cross_kernel<HD, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, CrossLayout<HD>::kBytes);
+        cross_kernel<HD, F16, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, CrossLayout<HD, PAIR>::kBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev] = true;
   }
@@ -1031,15 +1052,17 @@ cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUten
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid);
   cfg.blockDim = dim3(kCrossThreads);
-  cfg.dynamicSmemBytes = CrossLayout<HD>::kBytes;
+  cfg.dynamicSmemBytes = CrossLayout<HD, PAIR>::kBytes;
   cfg.stream = stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_kernel<HD, F16>, tq, tf, tk, tv, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_kernel<HD, F16, PAIR>, tq, tf, tk, tv, p);
   if (e != cudaSuccess) return e;
+  const int group = PAIR ? 2 * p.group : p.group;  // (as the rows of a partial lie)
   const MergeParams m = {p.out,        p.lse,         p.part_o, p.part_ml, p.merge,
-                         p.out_stride, p.num_q_heads, p.group,  p.rows};
-  return launch_unit_merge<HD, F16>(cfg, pl.grid, (long long)p.num_tokens * p.group, m);
+                         p.out_stride, p.num_q_heads, group,    p.rows};
+  const long long rows = (long long)(PAIR ? min(p.num_tokens, p.unit_tokens) : p.num_tokens) * group;
+  return launch_unit_merge<HD, F16>(cfg, pl.grid, rows, m);
 }
 
 bool known_shape(int num_q_heads, int num_kv_heads, int head_dim) {
@@ -1092,12 +1115,17 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   const bool none = num_states == 0;
   // (Q of few rows: as many tokens as have 32)
   CUtensorMap tq, tf, tk, tv;
-  if (!head_tile_tensor_map(none ? q : k, none ? num_tokens : num_states, none ? num_q_heads : num_kv_heads,
-                            head_dim, none ? q_stride : k_stride, kTile, &tk) ||
-      !head_tile_tensor_map(none ? q : v, none ? num_tokens : num_states, none ? num_q_heads : num_kv_heads,
-                            head_dim, none ? q_stride : v_stride, kTile, &tv) ||
+  // Pairs of heads: where sequences have at most 32 rows of a head on average.  (A
+  // longer one is cut into units of 32 rows, whose products fill a quarter of the
+  // tensor cores' rows: 2048 rows of one sequence took twice the time.)
+  const bool pairs = head_dim == 64 && num_kv_heads % 2 == 0 && g <= 32 && (int64_t)num_tokens * g <= (int64_t)32 * batch;
+  const int few = g > 32 ? 0 : 32 / g, wide = pairs ? 128 : head_dim;
+  const int heads = pairs ? num_kv_heads / 2 : num_kv_heads;
+  const int there = none ? num_tokens : num_states, mapped = none ? (pairs ? num_q_heads / 2 : num_q_heads) : heads;
+  if (!head_tile_tensor_map(none ? q : k, there, mapped, wide, none ? q_stride : k_stride, kTile, &tk) ||
+      !head_tile_tensor_map(none ? q : v, there, mapped, wide, none ? q_stride : v_stride, kTile, &tv) ||
       !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, kTile / g, &tq) ||
-      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, g > 32 ? 1 : 32 / g, &tf))
+      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, few ? few : 1, &tf))
     return VG_ERR_LAUNCH;
   CrossParams p = {};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1122,10 +1150,15 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   p.num_kv_heads = num_kv_heads;
   p.group = g;
   p.rows = pl.rows;
+  p.heads = heads;
+  p.tile_tokens = pairs ? few : kTile / g;
+  p.few_tokens = few;
+  p.unit_tokens = pairs ? few : 2 * (kTile / g);
+  p.by_unit_tokens = p.unit_tokens == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.unit_tokens - 1) / p.unit_tokens);
   const bool f16 = type == VG_TYPE_FP16;
-  const cudaError_t e = head_dim == 128 ? (f16 ? launch_cross<128, true>(pl, tq, tf, tk, tv, p, stream)
-                                               : launch_cross<128, false>(pl, tq, tf, tk, tv, p, stream))
-                                        : (f16 ? launch_cross<64, true>(pl, tq, tf, tk, tv, p, stream)
-                                               : launch_cross<64, false>(pl, tq, tf, tk, tv, p, stream));
+  auto launch = [&](auto kernel_of_type) { return kernel_of_type(pl, tq, tf, tk, tv, p, stream); };
+  const cudaError_t e = head_dim == 128 ? launch(f16 ? launch_cross<128, true, false> : launch_cross<128, false, false>)
+                        : pairs         ? launch(f16 ? launch_cross<64, true, true> : launch_cross<64, false, true>)
+                                        : launch(f16 ? launch_cross<64, true, false> : launch_cross<64, false, false>);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;
 }

@@ -42,6 +42,22 @@ def test_ragged_batch(masked, dtype, d):
     check_cross(States(lens, 2, d, dtype, seed=4, gap=1, masked=masked, fused=True), new, 8, strided=True)
 
 
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 4, 64), (16, 2, 64), (6, 2, 64), (34, 2, 64), (64, 2, 64), (66, 2, 64),
+                                      (10, 10, 64), (8, 2, 128), (9, 3, 64)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_few_rows(Hq, Hkv, d, dtype, masked):
+    """Sequences of at most 32 rows of a head, with one that has more: heads of 64
+    go in pairs where their number is even."""
+    rng = np.random.default_rng(Hq)
+    lens = [1, 128, 700, 0, 129, 2000, 5, 300, 1111, 40]
+    few = max(1, 32 * Hkv // Hq)
+    new = rng.integers(0, few + 1, 10)
+    new[:4] = [few, 1, few, min(few, 2)]
+    new[7] = min(5 * few + 1, int(10 * few - new.sum() + new[7]))
+    check_cross(States(lens, Hkv, d, dtype, seed=Hq, gap=2, masked=masked, fused=True), new, Hq, rows_after=1)
+
+
 @pytest.mark.parametrize("batch", [31, 32, 33, 100, 400, 4096])
 def test_many_sequences(batch):
     rng = np.random.default_rng(batch)
