@@ -1051,7 +1051,8 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   if (e != cudaSuccess) return e;
   const MergeParams m = {reinterpret_cast<uint16_t*>(p.out), p.lse,          p.part_o,  p.part_ml, p.merge,
                          p.out_stride,                       p.num_q_heads, p.group,   p.rows};
-  return launch_unit_merge<HD, false>(cfg, pl.grid, (long long)p.num_tokens * p.group, m);
+  const long long rows = (long long)p.num_tokens * p.group;
+  return launch_unit_merge<HD, false>(cfg, pl.grid, rows, rows, m);
 }
 
 }  // namespace

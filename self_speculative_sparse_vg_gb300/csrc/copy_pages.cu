@@ -11,7 +11,7 @@
 namespace vg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPoolsPerLaunch = 128;  // K and V of 64 layers
 constexpr int kBatch = 8;             // 16-byte pieces of a thread in flight
 

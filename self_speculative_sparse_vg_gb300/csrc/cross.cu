@@ -728,6 +728,48 @@ __device__ __forceinline__ void fill_sequence_table(const CrossParams& p, const 
   }
 }
 
+// Where the CTA's share of a line of `total` begins, in the numbers that it needs (a
+// division of 64 bits takes 1000 cycles, and its code is fetched for it).  sum: the
+// line up to and with this lane's sequence, where they are at most 32.
+template <typename N>
+__device__ __forceinline__ Share locate_share(const CrossParams& p, const SequenceTable& tab, const Sequence& seq,
+                                              long long sum, long long total, int lane) {
+  // at least one tile, so that every CTA inside a divided unit has a part of it
+  const N share = max((N)((N)(total + gridDim.x - 1) / (N)gridDim.x), (N)(p.rows == kTile ? kOneCost : kTwoCost));
+  const long long x0 = (long long)share * blockIdx.x;
+  Share s = {};
+  s.share = share;
+  s.x1 = min(total, x0 + (long long)share);
+  s.e = -1;
+  if (x0 >= total) return s;
+  long long base = 0;  // where the sequence's part of the line begins
+  if (p.batch <= 32) {
+    s.e = __ffs(__ballot_sync(0xffffffffu, sum > x0)) - 1;
+    base = __shfl_sync(0xffffffffu, sum, max(s.e - 1, 0));
+    if (s.e == 0) base = 0;
+    s.seq.q0 = __shfl_sync(0xffffffffu, seq.q0, s.e);
+    s.seq.n = __shfl_sync(0xffffffffu, seq.n, s.e);
+    s.seq.start = __shfl_sync(0xffffffffu, seq.start, s.e);
+    s.seq.len = __shfl_sync(0xffffffffu, seq.len, s.e);
+  } else {
+    for (int e0 = 0; e0 < p.batch && s.e < 0; e0 += 32) {
+      const uint32_t past = __ballot_sync(0xffffffffu, e0 + lane < p.batch && tab.length[e0 + lane] > x0);
+      if (past) s.e = e0 + __ffs(past) - 1;
+    }
+    base = s.e > 0 ? tab.length[s.e - 1] : 0;
+    s.seq = tab.seq[s.e];
+  }
+  const N per_head = (N)head_length(p, s.seq), full = (N)unit_length(p, p.unit_tokens, s.seq.len);
+  const N in_seq = (N)(x0 - base);
+  s.h = in_seq < per_head ? 0 : (int)(in_seq / per_head);
+  const N y = in_seq - (N)s.h * per_head;
+  s.rt = y < full ? 0 : min((int)(y / full), row_units(p, s.seq.n) - 1);
+  const N in = y - (N)s.rt * full;
+  s.kt0 = tiles_before((long long)in, tile_cost(p, min(p.unit_tokens, s.seq.n - s.rt * p.unit_tokens)));
+  s.unit_at = x0 - (long long)in;
+  return s;
+}
+
 // Where the CTA's share of the line begins; found by one warp.  e < 0: no work.
 __device__ __forceinline__ Share find_share(const CrossParams& p, const SequenceTable& tab, int lane) {
   const bool small = p.batch <= 32;
@@ -745,40 +787,8 @@ __device__ __forceinline__ Share find_share(const CrossParams& p, const Sequence
     }
     __syncwarp();
   }
-  // at least one tile, so that every CTA inside a divided unit has a part of it
-  const long long share = max(quotient(total + gridDim.x - 1, gridDim.x),
-                              (long long)(p.rows == kTile ? kOneCost : kTwoCost));
-  const long long x0 = share * blockIdx.x;
-  Share s = {};
-  s.share = share;
-  s.x1 = min(total, x0 + share);
-  s.e = -1;
-  if (x0 >= total) return s;
-  long long base = 0;  // where the sequence's part of the line begins
-  if (small) {
-    s.e = __ffs(__ballot_sync(0xffffffffu, sum > x0)) - 1;
-    base = __shfl_sync(0xffffffffu, sum, max(s.e - 1, 0));
-    if (s.e == 0) base = 0;
-    s.seq.q0 = __shfl_sync(0xffffffffu, seq.q0, s.e);
-    s.seq.n = __shfl_sync(0xffffffffu, seq.n, s.e);
-    s.seq.start = __shfl_sync(0xffffffffu, seq.start, s.e);
-    s.seq.len = __shfl_sync(0xffffffffu, seq.len, s.e);
-  } else {
-    for (int e0 = 0; e0 < p.batch && s.e < 0; e0 += 32) {
-      const uint32_t past = __ballot_sync(0xffffffffu, e0 + lane < p.batch && tab.length[e0 + lane] > x0);
-      if (past) s.e = e0 + __ffs(past) - 1;
-    }
-    base = s.e > 0 ? tab.length[s.e - 1] : 0;
-    s.seq = tab.seq[s.e];
-  }
-  const long long per_head = head_length(p, s.seq), full = unit_length(p, p.unit_tokens, s.seq.len);
-  s.h = (int)quotient(x0 - base, per_head);
-  const long long y = x0 - base - s.h * per_head;
-  s.rt = y < full ? 0 : min((int)quotient(y, full), row_units(p, s.seq.n) - 1);
-  const long long in = y - s.rt * full;
-  s.kt0 = tiles_before(in, tile_cost(p, min(p.unit_tokens, s.seq.n - s.rt * p.unit_tokens)));
-  s.unit_at = x0 - in;
-  return s;
+  if (total >> 31 == 0) return locate_share<uint32_t>(p, tab, seq, sum, total, lane);
+  return locate_share<long long>(p, tab, seq, sum, total, lane);
 }
 
 // ----------------------------------------------------------------- producer
@@ -1062,7 +1072,8 @@ cudaError_t launch_cross(const CrossPlan& pl, const CUtensorMap& tq, const CUten
   const MergeParams m = {p.out,        p.lse,         p.part_o, p.part_ml, p.merge,
                          p.out_stride, p.num_q_heads, group,    p.rows};
   const long long rows = (long long)(PAIR ? min(p.num_tokens, p.unit_tokens) : p.num_tokens) * group;
-  return launch_unit_merge<HD, F16>(cfg, pl.grid, rows, m);
+  const long long usual = 2 * ((long long)p.num_tokens * group / p.batch) + 1;
+  return launch_unit_merge<HD, F16>(cfg, pl.grid, rows, usual, m);
 }
 
 bool known_shape(int num_q_heads, int num_kv_heads, int head_dim) {

@@ -110,6 +110,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // not attend is zero, and a NaN or an infinity of one whose weight underflows
 // still has to show (as NaN), as it does where no cut falls.
 constexpr int kMergeWarps = 8, kMergeRows = 32;
+constexpr int kMergeBatch = 2;  // parts whose loads are in flight together (most units have two)
 
 template <int HD, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32) unit_merge_kernel(const MergeParams p) {
@@ -119,57 +120,68 @@ __global__ void __launch_bounds__(kMergeWarps * 32) unit_merge_kernel(const Merg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.y * kMergeRows, row = row0 + lane;  // row of the partial
   const MergeUnit mu = p.merge[c];
+  if (mu.parts == 0) return;
   const int g = p.group, tt = kUnitTile / g;
   const int rows = mu.ntok > tt ? kUnitTile + (mu.ntok - tt) * g : mu.ntok * g;
-  if (mu.parts == 0 || row0 >= rows) return;
-  const int tr = row % kUnitTile, tok = row / kUnitTile * tt + tr / g;
-  const bool mine = tr < tt * g && tok < mu.ntok;  // else no token's row
-  auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)(warp * NP) * p.rows + row;
-  float m = -INFINITY, l = 0.f, acc[NP][4];
+  for (int row0 = blockIdx.y * kMergeRows; row0 < rows; row0 += gridDim.y * kMergeRows) {
+    const int row = row0 + lane;  // row of the partial
+    const int tr = row % kUnitTile, tok = row / kUnitTile * tt + tr / g;
+    const bool mine = tr < tt * g && tok < mu.ntok;  // else no token's row
+    auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)(warp * NP) * p.rows + row;
+    float m = -INFINITY, l = 0.f, acc[NP][4];
 #pragma unroll
-  for (int k = 0; k < NP; ++k)
+    for (int k = 0; k < NP; ++k)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
-  if (mine) {
-#pragma unroll 4
-    for (int i = 0; i < mu.parts; ++i) {
-      const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
-      float4 v[NP];
+      for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
+    if (mine) {
+      for (int i0 = 0; i0 < mu.parts; i0 += kMergeBatch) {
+        float2 x[kMergeBatch];
+        float4 v[kMergeBatch][NP];
 #pragma unroll
-      for (int k = 0; k < NP; ++k) v[k] = __ldcg(po + (slot(i) * (HD / 4) + k) * p.rows);
-      const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-      const float f = ex2(m - ref), w = ex2(x.x - ref);
-      l = fmaf(l, f, w * x.y);
+        for (int i = 0; i < kMergeBatch; ++i)
+          if (i0 + i < mu.parts) {
+            x[i] = __ldcg(&ml[slot(i0 + i) * p.rows + row]);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const float y[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            for (int k = 0; k < NP; ++k) v[i][k] = __ldcg(po + (slot(i0 + i) * (HD / 4) + k) * p.rows);
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(w, y[e], acc[k][e] * f);
+        for (int i = 0; i < kMergeBatch; ++i) {
+          if (i0 + i >= mu.parts) break;
+          const float mn = fmaxf(m, x[i].x), ref = safe_ref(mn);
+          const float f = ex2(m - ref), w = ex2(x[i].x - ref);
+          l = fmaf(l, f, w * x[i].y);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            const float y[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[k][e] = fmaf(w, y[e], acc[k][e] * f);
+          }
+          m = mn;
+        }
       }
-      m = mn;
     }
-  }
-  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
+    const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : NAN;
+    if (row0 >= gridDim.y * kMergeRows) __syncthreads();  // the rows before are read
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    out_s[lane][(warp * NP + k) * 2] = pack2<F16>(acc[k][0] * inv, acc[k][1] * inv);
-    out_s[lane][(warp * NP + k) * 2 + 1] = pack2<F16>(acc[k][2] * inv, acc[k][3] * inv);
-  }
-  if (mine && warp == 0 && p.lse)
-    p.lse[(int64_t)(mu.tok0 + tok) * p.num_q_heads + mu.h * g + tr % g] =
-        (m + log2f(l)) * 0.6931471805599453f;
-  __syncthreads();
-  constexpr int kPieces = HD / 8;  // 16-byte pieces of a row
-  for (int i = threadIdx.x; i < kMergeRows * kPieces; i += kMergeWarps * 32) {
-    const int r = row0 + i / kPieces, rr = r % kUnitTile, tk = r / kUnitTile * tt + rr / g;
-    if (rr >= tt * g || tk >= mu.ntok) continue;
-    *reinterpret_cast<uint4*>(p.out + (int64_t)(mu.tok0 + tk) * p.out_stride +
-                              (int64_t)(mu.h * g + rr % g) * HD + (i % kPieces) * 8) =
-        *reinterpret_cast<const uint4*>(&out_s[i / kPieces][(i % kPieces) * 4]);
+    for (int k = 0; k < NP; ++k) {
+      out_s[lane][(warp * NP + k) * 2] = pack2<F16>(acc[k][0] * inv, acc[k][1] * inv);
+      out_s[lane][(warp * NP + k) * 2 + 1] = pack2<F16>(acc[k][2] * inv, acc[k][3] * inv);
+    }
+    if (mine && warp == 0 && p.lse)
+      p.lse[(int64_t)(mu.tok0 + tok) * p.num_q_heads + mu.h * g + tr % g] =
+          (m + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();
+    constexpr int kPieces = HD / 8;  // 16-byte pieces of a row
+    for (int i = threadIdx.x; i < kMergeRows * kPieces; i += kMergeWarps * 32) {
+      const int r = row0 + i / kPieces, rr = r % kUnitTile, tk = r / kUnitTile * tt + rr / g;
+      if (rr >= tt * g || tk >= mu.ntok) continue;
+      *reinterpret_cast<uint4*>(p.out + (int64_t)(mu.tok0 + tk) * p.out_stride +
+                                (int64_t)(mu.h * g + rr % g) * HD + (i % kPieces) * 8) =
+          *reinterpret_cast<const uint4*>(&out_s[i / kPieces][(i % kPieces) * 4]);
+    }
   }
 }
 
@@ -248,9 +260,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) unit_merge_row_kernel(const 
 }
 
 // Launches the merge behind a kernel whose calls have at most `rows` rows of a
-// unit to merge (all of the call's rows of a KV head).
+// unit to merge (all of the call's rows of a KV head), of which a unit is expected
+// to have `usual` (a CTA takes 32, and more where a unit has them).
 template <int HD, bool F16>
-cudaError_t launch_unit_merge(cudaLaunchConfig_t cfg, int grid, long long rows, const MergeParams& p) {
+cudaError_t launch_unit_merge(cudaLaunchConfig_t cfg, int grid, long long rows, long long usual,
+                              const MergeParams& p) {
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   // Up to 32 rows: a CTA per row, whose units have many parts (one token of 8
@@ -260,7 +274,8 @@ cudaError_t launch_unit_merge(cudaLaunchConfig_t cfg, int grid, long long rows, 
     cfg.gridDim = dim3(grid, (int)rows);
     return cudaLaunchKernelEx(&cfg, unit_merge_row_kernel<HD, F16>, p);
   }
-  cfg.gridDim = dim3(grid, ((p.rows == kUnitTile ? (int)rows : p.rows) + kMergeRows - 1) / kMergeRows);
+  const int most = p.rows == kUnitTile ? (int)rows : p.rows;
+  cfg.gridDim = dim3(grid, ((usual < most ? (int)usual : most) + kMergeRows - 1) / kMergeRows);
   return cudaLaunchKernelEx(&cfg, unit_merge_kernel<HD, F16>, p);
 }
 
