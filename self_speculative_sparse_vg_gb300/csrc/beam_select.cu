@@ -96,6 +96,15 @@ struct Word {
       x[1] = f.y;
     }
   }
+  // two floats, of a word or of two
+  static __device__ __forceinline__ void two(const uint32_t* w, float (&x)[2]) {
+    if constexpr (kPer == 2) {
+      get(w[0], x);
+    } else {
+      x[0] = __uint_as_float(w[0]);
+      x[1] = __uint_as_float(w[1]);
+    }
+  }
   // maximum by element (a NaN gives way)
   static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -353,30 +362,51 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
   const float least = kth, floor = fmaxf(least, -FLT_MAX);
   const float base = safe_ref(m_warp);
   const bool plain = fabsf(base) < 1e30f;
-  const float r = plain ? base * kLog2e : 0.f, shift = plain ? 0.f : -base;
-  const uint64_t c2 = pair(kLog2e, kLog2e), r2 = pair(-r, -r);
+  const float r = plain ? base * kLog2e : 0.f;
   uint64_t acc = 0;
-#pragma unroll 2
-  for (int q = tid; q < pieces; q += kSliceThreads) {
-    const uint4 v = data[q];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; i += 2 / PER) {
-      float x[2];
-      if constexpr (PER == 2) {
-        W::get(w[i], x);
-      } else {
-        x[0] = __uint_as_float(w[i]);
-        x[1] = __uint_as_float(w[i + 1]);
-      }
-      uint64_t x2 = pair(x[0], x[1]);
-      if (!plain) x2 = add2(x2, pair(shift, shift));
-      const float2 y = unpair(fma2(x2, c2, r2));
-      acc = add2(acc, pair(ex2(y.x), ex2(y.y)));
-    }
+  auto reached = [&](const uint4& v, int q) {
     if (W::top(piece_top(v)) >= floor) {
       const int at = atomicAdd(&counter, 1);
       if (at < kListed) piece_list[at] = q;
+    }
+  };
+  if (plain) {
+    const uint64_t c2 = pair(kLog2e, kLog2e), r2 = pair(-r, -r);
+    auto add = [&](const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; i += 2 / PER) {
+        float x[2];
+        W::two(w + i, x);
+        const float2 y = unpair(fma2(pair(x[0], x[1]), c2, r2));
+        acc = add2(acc, pair(ex2(y.x), ex2(y.y)));
+      }
+    };
+    int q = tid;
+    for (; q + kSliceThreads < pieces; q += 2 * kSliceThreads) {  // two pieces, one look at both
+      const uint4 v0 = data[q], v1 = data[q + kSliceThreads];
+      add(v0);
+      add(v1);
+      if (W::top(W::most(piece_top(v0), piece_top(v1))) >= floor) {
+        reached(v0, q);
+        reached(v1, q + kSliceThreads);
+      }
+    }
+    if (q < pieces) {
+      add(data[q]);
+      reached(data[q], q);
+    }
+  } else {
+    for (int q = tid; q < pieces; q += kSliceThreads) {
+      const uint4 v = data[q];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+      for (int i = 0; i < 4; i += 2 / PER) {
+        float x[2];
+        W::two(w + i, x);
+        acc = add2(acc, pair(ex2((x[0] - base) * kLog2e), ex2((x[1] - base) * kLog2e)));
+      }
+      reached(v, q);
     }
   }
   const float2 a = unpair(acc);
