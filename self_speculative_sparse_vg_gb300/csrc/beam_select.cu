@@ -5,19 +5,20 @@
 // the lower token.  Every logit is read once, so the call is bound by HBM.
 //
 //  * A row of logits is cut into slices, a CTA each, that lie in shared memory
-//    (one bulk copy; several CTAs share an SM, so that copies and arithmetic of
-//    different slices overlap).  A slice leaves its maximum m, its
-//    sum of exp(x - m) and its best num_out logits in order: nothing else of a row
-//    can be among a request's best.
-//  * The best of a slice: threads are dealt to at least num_out groups; the
-//    least of the groups' maxima has num_out logits at or above it, and few more
-//    (num_out times the harmonic number of num_out, for logits in any order).  Those
-//    are listed and ordered by counting.  Where more are listed than there is
-//    room for (a row of equal values, most of it set to the type's lowest), the
-//    num_out-th largest value is found by bisection and its ties in order.
-//  * A second kernel, a CTA per request, merges the slices' lists per row and
-//    the rows' lists by score, the front entries of up to 32 lists in the lanes
-//    of a warp.
+//    (one bulk copy; six CTAs share an SM, so that copies and arithmetic of
+//    different slices overlap: fewer CTAs that load ahead of what they compute, in
+//    two buffers of 32 KB or a ring of 16 KB stages, were slower, 512 rows of 128K
+//    51 and 58 us against 42).  A slice leaves its maximum m, its sum of exp(x - m)
+//    and its best num_out logits in order: nothing else of a row can be among a
+//    request's best.
+//  * The best of a slice: threads are dealt to groups, twice num_out at least; the
+//    num_out-th largest of the groups' maxima has num_out logits at or above it, and
+//    few more (1.4 num_out in all, for logits in any order).  Those are listed and
+//    ordered by counting.  Where more are listed than there is room for (a row of
+//    equal values, most of it set to the type's lowest), the num_out-th largest
+//    value is found by bisection and its ties in order.
+//  * A second kernel, a CTA per request, merges the slices' lists: of their front
+//    entries it finds a bound as the slices do, and orders by counting what reaches it.
 //
 // A score decides between candidates that may lie close together, so it is held
 // as an unevaluated pair of floats: s - m - log l by error-free sums, the
@@ -40,7 +41,8 @@ constexpr int kSliceWarps = kSliceThreads / 32;
 constexpr int kMaxSlices = 96;           // of a row
 constexpr int kMaxBeams = 32;
 constexpr int kMaxOut = 64;
-constexpr int kListed = 512;             // candidates that a slice, or a request, has room for
+constexpr int kListed = 256;             // candidates that a slice, or a request, has room for (more cost a
+                                         // slice's shared memory the sixth CTA of an SM)
 constexpr int kSliceBytes = 32 * 1024;   // of a slice, at most
 constexpr int kLeastSliceBytes = 4 * 1024;
 
@@ -210,20 +212,32 @@ __device__ __forceinline__ int cta_sum(int v, int* part) {
   return sum;
 }
 
-// Of 32 or 64 values in shared memory the num_out-th largest: the least of those
-// that fewer than num_out exceed.  One warp.
-__device__ __forceinline__ float kth_of_groups(const float* group, int groups, int num_out) {
-  const int lane = threadIdx.x & 31;
-  const float a = group[lane], b = groups > 32 ? group[32 + lane] : a;
-  int over_a = 0, over_b = 0;
-#pragma unroll 4
-  for (int j = 0; j < groups; j += 4) {
-    const float4 o = *reinterpret_cast<const float4*>(group + j);
-    over_a += (o.x > a) + (o.y > a) + (o.z > a) + (o.w > a);
-    if (groups > 32) over_b += (o.x > b) + (o.y > b) + (o.z > b) + (o.w > b);
+// Groups that the threads are dealt to: twice num_out at least, so that some 1.4
+// num_out elements reach the num_out-th largest of their maxima.
+constexpr int kGroups = 2 * kMaxOut;
+__device__ __forceinline__ int groups_for(int num_out) { return num_out <= 16 ? 32 : num_out <= 32 ? 64 : kGroups; }
+
+// The num_out-th largest of the groups' maxima: the least of those that fewer than
+// num_out exceed.  One warp; group[]: its room.
+__device__ __forceinline__ float kth_of_groups(const float* thread_max, float* group, int num_out) {
+  const int lane = threadIdx.x & 31, groups = groups_for(num_out);
+  for (int g = lane; g < groups; g += 32) {
+    float v = thread_max[g];
+    for (int t = g + groups; t < kSliceThreads; t += groups) v = fmaxf(v, thread_max[t]);
+    group[g] = v;
   }
-  uint32_t least = over_a < num_out ? ordered(a) : 0xffffffffu;
-  if (groups > 32 && over_b < num_out) least = min(least, ordered(b));
+  __syncwarp();
+  uint32_t least = 0xffffffffu;
+  for (int g = lane; g < groups; g += 32) {
+    const float v = group[g];
+    int over = 0;
+#pragma unroll 4
+    for (int j = 0; j < groups; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(group + j);
+      over += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+    }
+    if (over < num_out) least = min(least, ordered(v));
+  }
   return from_ordered(__reduce_min_sync(0xffffffffu, least));
 }
 
@@ -292,10 +306,11 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
   extern __shared__ __align__(16) uint4 data[];
   __shared__ __align__(8) uint64_t bar;
   __shared__ float2 list[kListed];
-  __shared__ __align__(16) float group_max[64];
+  __shared__ __align__(16) float group_max[kGroups];
   __shared__ float thread_max[kSliceThreads];
   __shared__ float warp_max[kSliceWarps], warp_sum[kSliceWarps], kth;
-  __shared__ int counter, elements, dead, piece_list[kListed], part[kSliceWarps];
+  __shared__ uint16_t piece_list[kListed];
+  __shared__ int counter, elements, dead, part[kSliceWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.slices, s = blockIdx.x - row * p.slices;
   if (tid == 0) {
@@ -342,17 +357,7 @@ __global__ void __launch_bounds__(kSliceThreads, 6) beam_slice_kernel(const Sele
   __syncthreads();
   // -------- a value that at least num_out elements reach, and few more
   if (warp == 0) {
-    const int groups = p.num_out <= 16 ? 32 : 64;
-    float even = -INFINITY, odd = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kSliceWarps; i += 2) {
-      even = fmaxf(even, thread_max[i * 32 + lane]);
-      odd = fmaxf(odd, thread_max[i * 32 + 32 + lane]);
-    }
-    group_max[lane] = groups == 32 ? fmaxf(even, odd) : even;
-    group_max[32 + lane] = odd;
-    __syncwarp();
-    const float v = kth_of_groups(group_max, groups, p.num_out);
+    const float v = kth_of_groups(thread_max, group_max, p.num_out);
     if (lane == 0) kth = v;
   }
   __syncthreads();
