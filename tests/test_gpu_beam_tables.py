@@ -99,6 +99,24 @@ def test_the_list_runs_out(spare):
     check_beam_tables(**c)
 
 
+@pytest.mark.parametrize("spare", [0, 2, 7])
+@pytest.mark.parametrize("B", [2, 12])
+def test_the_list_runs_out_of_long_tables(B, spare):
+    """The rows that are emptied lose their entries of columns that would stay."""
+    rng = np.random.default_rng(10 * B + spare)
+    W, width = 8, 600
+    lens = np.repeat(rng.integers(8000, 9001, B), W)
+    owned = -(-lens // PAGE)
+    table = np.full((B * W, width), -1)
+    for b in range(B):                                      # all rows were given one row's table
+        rows = slice(b * W, (b + 1) * W)
+        table[rows, :owned[b * W]] = 600 * b + rng.permutation(600)[:owned[b * W]]
+    parents = rng.integers(0, W, (B, W))
+    free = np.concatenate([600 * B + np.arange(spare), np.full(50, -1)])
+    got = check_beam_tables(parents, lens, table, 600 * B + spare, owned, free, spare)
+    assert got["flag"] == 32 and (got["owned"] == 0).any()
+
+
 def test_refused_requests_stay_as_they_were():
     rng = np.random.default_rng(1)
     for edit in (("parents", (1, 2), 4), ("parents", (1, 0), -2), ("parents", (0, 0), 2 ** 31 - 1),
