@@ -855,6 +855,7 @@ struct Producer {
     Sequence seq = s.seq;
     uint32_t ri = 0, u = 0, on_landed = 0, landed = 0;  // bits: last load of a stage, its parity
     bool live = true, last_narrow = false;
+    const uint64_t once = l2_policy_evict_first();
     MergeUnit cut = {};
     while (true) {
       const int ntok = min(tu, seq.n - rt * tu), cost = tile_cost(p, ntok);
@@ -904,7 +905,12 @@ struct Producer {
           uint64_t* bar = &(v && checked_tile(p, un.len, kt) ? bars.landed : bars.full)[st];
           if (bar == &bars.full[st]) mbar_arrive(bar);  // for the second checker
           mbar_arrive_expect_tx(bar, Lay::kStageBytes);
-          tma_load_4d(ring + st * Lay::kStageBytes, v ? &tmv : &tmk, bar, 0, un.start + kt * kTile, 0, h);
+          // (states that no other unit reads leave L2 first: verify rows 31.0 us, 32.1
+          // without; prompts, whose units share them, 273 with and 262 without)
+          if (seq.n <= tu)
+            tma_load_4d(ring + st * Lay::kStageBytes, v ? &tmv : &tmk, bar, 0, un.start + kt * kTile, 0, h, once);
+          else
+            tma_load_4d(ring + st * Lay::kStageBytes, v ? &tmv : &tmk, bar, 0, un.start + kt * kTile, 0, h);
           on_landed &= ~(1u << st);
           if (bar == &bars.landed[st]) {
             on_landed |= 1u << st;
