@@ -3,25 +3,34 @@
 // Row j of a request becomes a continuation of its row parents[j].  The rows of
 // a request share the pages that are full: a page stands in several of its rows,
 // always at the column of its positions, so the rows themselves say who holds
-// it and no counter is kept.  A column is one thread's: it reads the request's old
-// entries there, finds the pages that no new row holds (they go on the free
-// list), and writes the new entries.  A partly filled last page is written to by
-// its row, so it stays with one row; each other one that takes it gets a page
-// from the list's end, and the copy is left to vg_copy_pages.
+// it and no counter is kept.  A column's old entries say which pages no new row
+// holds (they go on the free list); then the new entries are written.  A partly
+// filled last page is written to by its row, so it stays with one row; each other
+// one that takes it gets a page from the list's end, and the copy is left to
+// vg_copy_pages.
 //
-// The call is bound by latency (lengths, entries, list: dependent round trips).
-// The columns of all requests form one line that the CTAs of one cluster share;
-// the places of the returned pages are in line order, so the CTAs exchange their
-// counts through distributed shared memory, and a second cluster barrier lies
-// between what is pushed and what is popped.
+// The call is bound by latency (lengths, entries, list: dependent round trips, and
+// barriers between them).  The columns of all requests, in tiles of 32, form one
+// line that the CTAs of one cluster share; the places of the returned pages are in
+// line order, so the CTAs exchange their counts through distributed shared memory,
+// and a second cluster barrier lies between what is pushed and what is popped.
 //
-// Most columns hold one page in all rows and go on doing so: a thread looks at
-// one, all its loads in flight, and leaves it.  The others are gone through by
-// lanes, one per row, several columns of a warp at a time: who holds the same page
-// is one `match` (a thread per column took 4000 cycles for eight rows, in loops
-// over shared memory).  Rows part at neighbouring columns, so a CTA's warps share
-// what each of them has found (32 requests of eight beams 14.7 us with a warp's
-// columns left to it).
+// Three kinds of columns.  Most hold one full page in all rows and go on doing so:
+// a tile of such is looked at, a thread per column and all its loads in flight,
+// and left.  Where no column of a tile holds several pages (a prompt that one
+// row holds, a request that ends), the tile is one item of the list: one page a
+// column is read again and the rows' entries follow from their lengths.  Other
+// columns are items of their own, gone through by lanes, one per row, several
+// columns of a warp at a time: who holds the same page is one `match` (a thread
+// per column took 4000 cycles for eight rows).  Rows part at neighbouring
+// columns and a long request's tiles lie side by side, so a CTA's warps share what
+// each of them has found.
+//
+// Measured, calls in a row: 4 beams of 2100 positions 5.3 us, a launch's latency
+// and five round trips.  32 requests of eight beams with up to 32768 positions 10.5 us
+// when rows go on as they were, 15.7 us when a fifth of the requests begins or ends
+// in the call (35.6 us with every column by lanes, 24.4 us with all rows of such a tile
+// read again).
 #include <limits.h>
 
 #include "vg_device.cuh"
@@ -37,7 +46,7 @@ constexpr int kMaxRows = 4096;
 constexpr int kMaxBeams = 32;
 constexpr int kBatch = 8;             // entries of a thread whose loads are in flight together
 constexpr int kTiles = 31;            // tiles of 32 columns of a warp that are remembered
-constexpr int kListed = 64;           // columns of a warp that the CTA's warps can share
+constexpr int kListed = 96;           // items of a warp that the CTA's warps can share
 
 struct BeamParams {
   const int32_t* parents;
@@ -56,7 +65,8 @@ struct BeamParams {
 struct BeamShared {
   int *len, *own, *tail, *rank;  // [rows]; tail: page of a new row's partly filled last page, -1: none;
                                  // rank: which of the pages asked for is its copy's, -1: none
-  int *ends, *alive, *full;      // [batch]: columns up to the request's end; mask of rows that go on (after
+  int *kept, *held;              // [rows]; columns of an old row that a new one takes, and of a new row
+  int *ends, *alive, *full;      // [batch]: tiles up to the request's end; mask of rows that go on (after
                                  // its check); columns that are full pages in every row, 0 if one ends
   int *bad;                      // [batch]: error bits
   int8_t* parent;                // [rows]; -1: the row is emptied, -2: the request is refused
@@ -64,7 +74,7 @@ struct BeamShared {
 
 __host__ __device__ inline size_t shared_bytes(int batch, int beams) {
   const size_t rows = (size_t)batch * beams;
-  return (4 * rows + 4 * (size_t)batch) * sizeof(int) + rows;
+  return (6 * rows + 4 * (size_t)batch) * sizeof(int) + rows;
 }
 
 __device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p) {
@@ -74,7 +84,9 @@ __device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p) {
   sh.own = s + rows;
   sh.tail = s + 2 * rows;
   sh.rank = s + 3 * rows;
-  sh.ends = s + 4 * rows;
+  sh.kept = s + 4 * rows;
+  sh.held = s + 5 * rows;
+  sh.ends = s + 6 * rows;
   sh.alive = sh.ends + p.batch;
   sh.full = sh.alive + p.batch;
   sh.bad = sh.full + p.batch;
@@ -85,7 +97,7 @@ __device__ __forceinline__ BeamShared carve(int* s, const BeamParams& p) {
 // Inclusive sum of v over the CTA's threads in order; `all` is the total.  One
 // barrier; `part` is used again two sums later at the earliest.
 template <int NT>
-__device__ __noinline__ int cta_inclusive_sum(int v, int* part, int* all) {
+__device__ __forceinline__ int cta_inclusive_sum(int v, int* part, int* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -103,74 +115,128 @@ __device__ __noinline__ int cta_inclusive_sum(int v, int* part, int* all) {
 
 __device__ __forceinline__ int pages_of(int len) { return (int)(((unsigned)len + kPageSize - 1) / kPageSize); }
 
-// A column of the line: its request and number.  b < 0: none.
+// What a warp's list holds: a column (its request and number), or a tile of 32 columns
+// of which each holds one page at most: b = -2 - request, c = 2 * its first column
+// + how many pages go back.  b = -1: nothing.
 struct Column {
   int b, c;
 };
 
-__device__ __forceinline__ Column column_of(const BeamParams& p, const BeamShared& sh, int x) {
-  int lo = 0, hi = p.batch - 1;  // the first request that ends past x
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (sh.ends[mid] > x)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return {lo, x - (lo > 0 ? sh.ends[lo - 1] : 0)};
+// Whether the page that a column's rows hold goes back: no new row takes it (kept: the
+// columns that any takes).  A foreign one is flagged and dropped.
+__device__ __forceinline__ bool goes_back(const BeamParams& p, int c, int kept, int page) {
+  if (c < kept) return false;
+  if (page >= 0 && page < p.num_pages) return true;
+  flag_error(p.error_flag, VG_DEVERR_PAGE);
+  return false;
 }
 
-// Whether the column is one full page in every row and stays that.
-__device__ __forceinline__ bool stays(const BeamParams& p, const BeamShared& sh, const Column& col) {
-  if (col.c >= sh.full[col.b]) return false;
-  const int32_t* at = p.page_table + (int64_t)col.b * p.beams * p.width + col.c;
-  const int first = at[0];
-  bool same = true;
-  for (int i0 = 1; i0 < p.beams; i0 += kBatch) {
-    int page[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) page[k] = i0 + k < p.beams ? at[(int64_t)(i0 + k) * p.width] : first;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) same &= page[k] == first;
-  }
-  return same;
+// The columns of request b that new rows take.
+__device__ __forceinline__ int columns_kept(const BeamParams& p, const BeamShared& sh, int b) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_max_sync(0xffffffffu, lane < p.beams ? sh.kept[b * p.beams + lane] : 0);
 }
 
-// The columns of a tile that change (x: this lane's), listed in order.  Returns how
-// many.
-__device__ __forceinline__ int list_columns(const BeamParams& p, const BeamShared& sh, int x, int end,
-                                            Column* list) {
-  Column col = {-1, 0};
-  bool works = false;
-  if (x < end) {
-    col = column_of(p, sh, x);
-    works = !stays(p, sh, col);
+// What changes of the tile at column c0 of request b, listed in order: its columns, or
+// the tile if no column holds several pages.  Returns how many.
+__device__ __forceinline__ int list_tile(const BeamParams& p, const BeamShared& sh, int b, int c0, Column* list) {
+  const int lane = threadIdx.x & 31, c = c0 + lane;
+  bool works = false, many = false, back = false;
+  if (c0 + 32 <= sh.full[b]) {  // full pages, in every row
+    const int32_t* at = p.page_table + (int64_t)b * p.beams * p.width + c;
+    const int first = at[0];
+    for (int i0 = 1; i0 < p.beams; i0 += kBatch) {
+      int page[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) page[k] = i0 + k < p.beams ? at[(int64_t)(i0 + k) * p.width] : first;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) many |= page[k] != first;
+    }
+    works = many;
+  } else {
+    const int own = lane < p.beams ? sh.own[b * p.beams + lane] : 0, kept = columns_kept(p, sh, b);
+    const int32_t* at = p.page_table + (int64_t)b * p.beams * p.width + c;
+    int lo = INT_MAX, hi = INT_MIN;
+    for (int i0 = 0; i0 < p.beams; i0 += kBatch) {
+      int page[kBatch];  // (entries past a row's pages are loaded, too, and not looked at)
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        page[k] = i0 + k < p.beams && c < p.width ? at[(int64_t)(i0 + k) * p.width] : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool has = c < __shfl_sync(0xffffffffu, own, i0 + k);
+        lo = has ? min(lo, page[k]) : lo;
+        hi = has ? max(hi, page[k]) : hi;
+      }
+    }
+    works = lo <= hi;
+    many = lo < hi;
+    if (lo == hi) back = goes_back(p, c, kept, lo);
   }
   const uint32_t mask = __ballot_sync(0xffffffffu, works);
-  const int lane = threadIdx.x & 31;
+  if (!mask) return 0;
+  const bool columns = __any_sync(0xffffffffu, many);
+  const int goes = __popc(__ballot_sync(0xffffffffu, back));
   __syncwarp();
-  if (works) list[__popc(mask & ((1u << lane) - 1u))] = col;
+  if (columns) {
+    if (works) list[__popc(mask & ((1u << lane) - 1u))] = {b, c};
+  } else if (lane == 0) {
+    list[0] = {-2 - b, 2 * c0 + goes};
+  }
   __syncwarp();
-  return __popc(mask);
+  return columns ? __popc(mask) : 1;
+}
+
+// A listed tile: its pages that go back to the free list from `place` on, and its
+// new entries.  A row's copy is written last, by another thread.
+__device__ __forceinline__ void write_tile(const BeamParams& p, const BeamShared& sh, int b, int c0, int place,
+                                           int top) {
+  const int lane = threadIdx.x & 31, c = c0 + lane, r0 = b * p.beams;
+  int own = 0, held = 0, copied = -1;  // row `lane`: its columns before and after, and its copy's
+  if (lane < p.beams) {
+    const int rank = sh.rank[r0 + lane];
+    own = sh.own[r0 + lane];
+    held = rank < top ? sh.held[r0 + lane] : 0;
+    copied = rank >= 0 ? held - 1 : -1;
+  }
+  const int most = __reduce_max_sync(0xffffffffu, own), kept = columns_kept(p, sh, b);
+  const int row = __ffs(__ballot_sync(0xffffffffu, own == most)) - 1;  // it holds what any row does
+  int32_t* at = p.page_table + (int64_t)r0 * p.width + c;
+  const int page = c < most ? at[(int64_t)row * p.width] : -1;
+  const bool differs = min(max(own, c0), c0 + 32) != min(max(held, c0), c0 + 32);
+  const uint32_t rows = __ballot_sync(0xffffffffu, differs);
+  const bool back = c < most && goes_back(p, c, kept, page);
+  const uint32_t goes = __ballot_sync(0xffffffffu, back);
+  if (back) p.free_pages[place + __popc(goes & ((1u << lane) - 1u))] = page;
+  for (int i0 = 0; i0 < p.beams; i0 += kBatch) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k;
+      const bool had = c < __shfl_sync(0xffffffffu, own, i), has = c < __shfl_sync(0xffffffffu, held, i);
+      const bool copy = c == __shfl_sync(0xffffffffu, copied, i);
+      if ((rows >> i & 1) && had != has && !copy) at[(int64_t)i * p.width] = has ? page : -1;
+    }
+  }
 }
 
 // One row of a column, in a lane: its old entry, and whether the page goes back
 // (no new row holds it; the first of the rows that did).
 struct Entry {
-  int b, c, r, page;
+  int b, c, r, page;  // b <= -2, in its first lane: a tile
   bool has, keeps, back;
 };
 
 __device__ __forceinline__ Entry load_entry(const BeamParams& p, const BeamShared& sh, const Column& col) {
   const int i = threadIdx.x & ((1 << p.row_bits) - 1);
   Entry e = {-1, 0, 0, -1, false, false, false};
-  if (col.b < 0 || i >= p.beams) return e;
+  if (col.b < 0 ? i > 0 : i >= p.beams) return e;  // a tile is its first lane's
   e.b = col.b;
   e.c = col.c;
+  if (col.b < 0) return e;
   e.r = col.b * p.beams + i;
   e.has = col.c < sh.own[e.r];
   if (e.has) e.page = p.page_table[(int64_t)e.r * p.width + col.c];
-  e.keeps = e.has && (sh.alive[col.b] >> i & 1) && col.c < pages_of(sh.len[e.r]);
+  e.keeps = e.has && col.c < sh.kept[e.r];
   return e;
 }
 
@@ -232,24 +298,26 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
     tails[k] = -1;
     if (r >= rows) break;
     const int b = r / p.beams, j = sh.parent[r];
-    if (j < 0 || sh.bad[b]) continue;
-    const int from = b * p.beams + j, len = sh.len[from];
+    sh.kept[r] = sh.alive[b] >> (r - b * p.beams) & 1 ? pages_of(sh.len[r]) : 0;
+    const int from = b * p.beams + j, len = j >= 0 ? sh.len[from] : 0;
+    sh.held[r] = pages_of(len);
+    if (sh.bad[b]) continue;
     if (len % kPageSize) tails[k] = p.page_table[(int64_t)from * p.width + len / kPageSize];
   }
-  int columns = 0;
+  int tiles = 0;  // of the line
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
-    int cols = 0, all;
+    int n = 0, all;
     const int bad = b < p.batch ? sh.bad[b] : 0;
-    if (b < p.batch && !bad) cols = sh.ends[b];
-    const int end = columns + sum(cols, &all);
+    if (b < p.batch && !bad) n = (sh.ends[b] + 31) / 32;
+    const int end = tiles + sum(n, &all);
     if (b < p.batch) sh.ends[b] = end;
     if (bad) {
       if (cta == 0) flag_error(p.error_flag, bad);
       sh.alive[b] = 0;
       for (int i = 0; i < p.beams; ++i) sh.parent[b * p.beams + i] = -2;
     }
-    columns += all;
+    tiles += all;
   }
 #pragma unroll
   for (int k = 0; k < kEarly; ++k)
@@ -272,60 +340,63 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
   // -------- the columns that change, and the pages that go back: counted
   const int step = 32 >> p.row_bits, sub = lane >> p.row_bits;  // columns of a pass, and this lane's
   const int warps = ctas * (NT / 32), w = cta * (NT / 32) + warp;
-  // few columns: all are gone through, in one pass of every warp.  Else a warp has a
-  // run of tiles of 32, and looks which of their columns change
-  const bool direct = columns <= warps * step;
-  const int tiles = (columns + 31) / 32, share = (tiles + warps - 1) / warps;
-  const int tile0 = w * share, tile1 = min(tiles, tile0 + share);
+  // a warp has a run of tiles, and lists what changes of them
+  const int share = (tiles + warps - 1) / warps;
+  const int tile0 = min(tiles, w * share), tile1 = min(tiles, tile0 + share);
+  int first_b = 0;  // the request of the first: the one that ends past it
+  for (int hi = p.batch - 1; first_b < hi;) {
+    const int mid = (first_b + hi) >> 1;
+    if (sh.ends[mid] > tile0)
+      hi = mid;
+    else
+      first_b = mid + 1;
+  }
+  auto list_next = [&](int t, int* b, Column* to) {  // tile t; *b: a request no later than its own
+    while (sh.ends[*b] <= t) ++*b;
+    return list_tile(p, sh, *b, (t - (*b > 0 ? sh.ends[*b - 1] : 0)) * 32, to);
+  };
   Column* list = lists[warp];
   int k_begin = 0, k_end = 0;
   uint32_t has_work = 0;  // tiles with columns that change; those past kTiles share a bit
-  bool spread = true;
-  if (!direct) {
-    int found = 0, listed;
-    bool fits = true;
-    for (int t = tile0; t < tile1; ++t) {
-      fits &= found <= kListed - 32;  // past its room the list is made again
-      const int n = list_columns(p, sh, t * 32 + lane, columns, list + (fits ? found : 0));
-      if (n > 0) has_work |= 1u << min(t - tile0, kTiles);
-      found += n;
-    }
-    // where a warp has several passes: one list of the CTA, if every warp's has
-    // fitted, cut anew in warps' shares
-    constexpr int kMany = 1 << 16, kNotAll = 1 << 24;
-    const int at = sum(lane > 0 ? 0 : !fits ? kNotAll : found > step ? found + kMany : found, &listed);
-    spread = listed < kNotAll;
-    k_end = found;
-    if (spread && listed >= kMany) {
-      listed %= kMany;
-      const int first = __shfl_sync(0xffffffffu, at, 0) % kMany - found;
-      for (int k = lane; k < found; k += 32) spread_list[first + k] = list[k];
-      const int each = ((listed + step - 1) / step + NT / 32 - 1) / (NT / 32) * step;
-      k_begin = min(listed, warp * each);
-      k_end = min(listed, k_begin + each);
-      list = spread_list;
-      __syncthreads();
-    }
+  int found = 0, listed;
+  bool fits = true;
+  for (int t = tile0, b = first_b; t < tile1; ++t) {
+    fits &= found <= kListed - 32;  // past its room the list is made again
+    const int n = list_next(t, &b, list + (fits ? found : 0));
+    if (n > 0) has_work |= 1u << min(t - tile0, kTiles);
+    found += n;
   }
-  if (direct) {
-    k_begin = min(columns, w * step);
-    k_end = min(columns, k_begin + step);
+  // where a warp has several passes: one list of the CTA, if every warp's has
+  // fitted, cut anew in warps' shares
+  constexpr int kMany = 1 << 16, kNotAll = 1 << 24;
+  const int at = sum(lane > 0 ? 0 : !fits ? kNotAll : found > step ? found + kMany : found, &listed);
+  const bool spread = listed < kNotAll;
+  k_end = found;
+  if (spread && listed >= kMany) {
+    listed %= kMany;
+    const int first = __shfl_sync(0xffffffffu, at, 0) % kMany - found;
+    for (int k = lane; k < found; k += 32) spread_list[first + k] = list[k];
+    const int each = (listed + NT / 32 - 1) / (NT / 32);
+    k_begin = min(listed, warp * each);
+    k_end = min(listed, k_begin + each);
+    list = spread_list;
+    __syncthreads();
   }
   // entry of column k of the list
   auto entry = [&](int k) {
     Column col = {-1, 0};
-    if (k + sub < k_end) col = direct ? column_of(p, sh, k + sub) : list[k + sub];
+    if (k + sub < k_end) col = list[k + sub];
     return load_entry(p, sh, col);
   };
   int mine = 0, passes = 0;
   Entry e = {-1, 0, 0, -1, false, false, false};
-  for (int t = tile0; t < tile1 || (spread && t == tile0); ++t) {
-    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_columns(p, sh, t * 32 + lane, columns, list) : 0;
+  for (int t = tile0, b = first_b; t < tile1 || (spread && t == tile0); ++t) {
+    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_next(t, &b, list) : 0;
     Entry next = entry(k_begin);
     for (int k0 = k_begin; k0 < k_end; k0 += step, ++passes) {
       e = next;
       next = entry(k0 + step);
-      mine += __popc(find_returned(p, e, true));
+      mine += __popc(find_returned(p, e, true)) + __reduce_add_sync(0xffffffffu, e.b <= -2 ? e.c & 63 : 0);
     }
     if (spread) break;
   }
@@ -358,8 +429,8 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
   const int top = top0 + back;
   // -------- pushed, and the new entries (those of copies come last)
   const bool once = passes == 1;  // the pass is still in the registers
-  for (int t = tile0; t < tile1 || (spread && t == tile0); ++t) {
-    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_columns(p, sh, t * 32 + lane, columns, list) : 0;
+  for (int t = tile0, b = first_b; t < tile1 || (spread && t == tile0); ++t) {
+    if (!spread) k_end = has_work >> min(t - tile0, kTiles) & 1 ? list_next(t, &b, list) : 0;
     Entry next = once ? e : entry(k_begin);
     for (int k0 = k_begin; k0 < k_end; k0 += step) {
       if (!once) {
@@ -368,35 +439,29 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
         find_returned(p, e, false);
       }
       const uint32_t goes = __ballot_sync(0xffffffffu, e.back);
-      if (e.back) p.free_pages[base + __popc(goes & ((1u << lane) - 1u))] = e.page;
+      int place = base + __popc(goes & ((1u << lane) - 1u));
       base += __popc(goes);
+      for (uint32_t marks = __ballot_sync(0xffffffffu, e.b <= -2); marks; marks &= marks - 1) {
+        const int at = __ffs(marks) - 1, c = __shfl_sync(0xffffffffu, e.c, at), n = c & 63;
+        write_tile(p, sh, -2 - __shfl_sync(0xffffffffu, e.b, at), (c & ~63) / 2,
+                   __shfl_sync(0xffffffffu, place, at), top);
+        __syncwarp();
+        if (lane > at) place += n;
+        base += n;
+      }
+      if (e.back) p.free_pages[place] = e.page;
       const int j = e.b >= 0 ? sh.parent[e.r] : -1, first = lane >> p.row_bits << p.row_bits;
       const int from = __shfl_sync(0xffffffffu, e.page, first + max(j, 0));
       if (e.b < 0) continue;
-      int page = -1;
-      const int rank = sh.rank[e.r];
-      if (j >= 0 && rank < top) {
-        const int len = sh.len[e.b * p.beams + j], full = len / kPageSize;
-        if (e.c == full && rank >= 0) continue;
-        if (e.c < full || (e.c == full && len % kPageSize)) page = from;
-      }
+      const int rank = sh.rank[e.r], held = rank < top ? sh.held[e.r] : 0;
+      if (rank >= 0 && e.c == held - 1) continue;  // a copy's, written last
+      const int page = e.c < held ? from : -1;
       if (e.has ? page != e.page : page != -1) p.page_table[(int64_t)e.r * p.width + e.c] = page;
     }
     __syncwarp();
     if (spread) break;
   }
-  if (asked > top && !direct) {  // rows are emptied: their entries of columns that would stay, too
-    __syncthreads();
-    for (int t = tile0; t < tile1; ++t) {
-      const int x = t * 32 + lane;
-      if (x >= columns) break;
-      const Column col = column_of(p, sh, x);
-      if (!stays(p, sh, col)) continue;
-      for (int r = col.b * p.beams; r < (col.b + 1) * p.beams; ++r)
-        if (sh.rank[r] >= top) p.page_table[(int64_t)r * p.width + col.c] = -1;
-    }
-  }
-  if (back > 0) {
+  if (back > 0 || asked > top) {
     __syncwarp();
     if (ctas > 1) {
       cluster_arrive_release();
@@ -404,6 +469,11 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
     } else {
       __syncthreads();
     }
+  }
+  if (asked > top) {  // rows are emptied: their entries of columns that would stay, too
+    for (int r = cta; r < rows; r += ctas)
+      if (sh.rank[r] >= top)
+        for (int c = tid; c < sh.own[r]; c += NT) p.page_table[(int64_t)r * p.width + c] = -1;
   }
   // -------- rows, and the pages for copies from the list's end
   for (int r = cta * NT + tid; r < rows; r += ctas * NT) {
@@ -446,7 +516,7 @@ cudaError_t launch(const BeamParams& p, int ctas, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev >= 64 || !set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(beam_tables_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         160 * 1024);
+                                         170 * 1024);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(beam_tables_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -482,9 +552,9 @@ extern "C" vg_status vg_beam_tables(const int32_t* parents, int batch, int beams
   if (!parents || !lens || !page_table || !owned || !free_pages || !free_count || !copies || batch <= 0 ||
       beams <= 0 || max_pages_per_seq <= 0 || num_pages <= 0 || free_capacity <= 0)
     return VG_ERR_INVALID_ARGUMENT;
-  // a column's number on the line has to fit an int32
+  // twice a column's number, and the tiles of all requests, have to fit an int32
   if (beams > kMaxBeams || (int64_t)batch * beams > kMaxRows || num_pages > INT_MAX / kPageSize ||
-      max_pages_per_seq > INT_MAX / kPageSize || (int64_t)batch * max_pages_per_seq > INT_MAX - kThreads * kMaxCluster)
+      max_pages_per_seq > INT_MAX / kPageSize || (int64_t)batch * max_pages_per_seq > INT_MAX)
     return VG_ERR_UNSUPPORTED;
   BeamParams p = {};
   p.parents = parents;
@@ -501,10 +571,10 @@ extern "C" vg_status vg_beam_tables(const int32_t* parents, int batch, int beams
   p.width = max_pages_per_seq;
   p.num_pages = num_pages;
   p.free_capacity = free_capacity;
-  const int64_t columns = (int64_t)batch * max_pages_per_seq;  // at most
+  const int64_t tiles = (int64_t)batch * ((max_pages_per_seq + 31) / 32);  // at most
   int ctas = 1;
-  while (ctas < kMaxCluster && (int64_t)ctas * kThreads < columns) ctas *= 2;
-  const cudaError_t e = batch * beams <= kFewThreads && columns <= kFewThreads
+  while (ctas < kMaxCluster && (int64_t)ctas * kThreads / 32 < tiles) ctas *= 2;
+  const cudaError_t e = batch * beams <= kFewThreads && tiles <= kFewThreads / 32
                             ? launch<kFewThreads>(p, 1, stream)
                             : launch<kThreads>(p, ctas, stream);
   return e == cudaSuccess ? VG_OK : VG_ERR_LAUNCH;

@@ -117,6 +117,38 @@ def test_the_list_runs_out_of_long_tables(B, spare):
     assert got["flag"] == 32 and (got["owned"] == 0).any()
 
 
+@pytest.mark.parametrize("W", [1, 3, 8, 17, 32])
+@pytest.mark.parametrize("B,hi,apart", [(6, 33000, 30), (40, 33000, 3), (3, 9000, 560), (300, 1500, 2)])
+def test_requests_that_begin_and_end_among_others(B, W, hi, apart):
+    """Long runs of columns with one page at most, of which all, some or none go
+    back, between columns where the rows part; foreign ids among the returned."""
+    if B * W > 4096:
+        B = 4096 // W
+    rng = np.random.default_rng(1000 * B + W)
+    c = make(rng, B, W, 1, hi, apart)
+    rows = lambda b: slice(b * W, (b + 1) * W)              # noqa: E731
+    for b in range(B):
+        kind = b % 6
+        if kind == 0:                                       # finished
+            c["parents"][b] = -1
+        elif kind == 1:                                     # a prompt that one row holds, not always the first
+            one = int(rng.integers(W))
+            for r in range(b * W, (b + 1) * W):
+                if r != b * W + one:
+                    c["lens"][r] = c["owned"][r] = 0
+                    c["table"][r] = -1
+            c["parents"][b] = one
+        elif kind == 2:                                     # one row goes on, the others are emptied
+            c["parents"][b] = -1
+            c["parents"][b, rng.integers(W)] = rng.integers(W)
+        elif kind == 3:                                     # rows cut back to a part of their pages
+            c["lens"][rows(b)] //= 2
+        elif kind == 4:
+            c["parents"][b] = -1
+            c["table"][rows(b), 5:9] = [-3, 2 ** 30, c["num_pages"], -1]
+    check_beam_tables(**c)
+
+
 def test_refused_requests_stay_as_they_were():
     rng = np.random.default_rng(1)
     for edit in (("parents", (1, 2), 4), ("parents", (1, 0), -2), ("parents", (0, 0), 2 ** 31 - 1),
