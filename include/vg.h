@@ -518,7 +518,8 @@ vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, int64_t q_str
  * -infinity) is zero.  What lies in states that a row does not attend does not
  * reach it, whatever it holds.  A sequence whose rows or states are not a range
  * inside [0, num_tokens) or [0, num_states) is flagged VG_DEVERR_LENGTH and its
- * rows are left as they were.
+ * rows are left as they were.  (Rows that offsets out of order give to two
+ * sequences hold either's.)
  * Results are the same on every run; what else is in the batch changes them by
  * rounding alone: it decides where a long sequence is cut, and a softmax weight
  * is rounded to the call's type (half a step) against the largest score since

@@ -1,4 +1,5 @@
-"""Calls one case of operators.py four times: a program to profile.
+"""Calls one case of operators.py or more_operators.py four times: a program to
+profile.
 
     python perf/run_case.py NAME [SEED]
 """
@@ -8,14 +9,15 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from perf import operators  # noqa: E402
+from perf import more_operators, operators  # noqa: E402
 
 
 def main(name, seed=1):
-    operators.own = True
-    state = operators.prepare(next(c for c in operators.listed() if c["name"] == name), int(seed))
+    of, case = next((m, c) for m in (operators, more_operators) for c in m.listed() if c["name"] == name)
+    of.own = True
+    state = of.prepare(case, int(seed))
     for _ in range(4):
-        operators.run(state)
+        of.run(state)
     torch.cuda.synchronize()
     print("ok", name)
 

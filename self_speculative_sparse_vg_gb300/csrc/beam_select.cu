@@ -24,6 +24,13 @@
 // as an unevaluated pair of floats: s - m - log l by error-free sums, the
 // logarithm split in exponent and mantissa.  What is left is the rounding of the
 // sum of exponentials, about 2^-23 relative.
+//
+// Measured, calls in a row.  One request of four beams, 32K bf16 logits: 6.9 us, two
+// launches' latency.  8 of four beams, 151936 float32 logits: 10.2 us.  16 of five,
+// 50257 fp16 logits from odd addresses: 11.3 us.  64 of eight, 128256 bf16 logits: 41.8
+// us (117 MB: 17.3 at the rate of a copy); there the slices take 34 us, of which the
+// load and the maxima 20.5, the exponentials 4.7, the candidates and their order 9:
+// issue is active 63 % of the time, and the short phases wait at barriers.
 #include <float.h>
 #include <limits.h>
 #include <math.h>

@@ -33,6 +33,15 @@
 //    attended (masked, or past the end, where another sequence's lie) pass
 //    through two warps that zero those rows of V: a weight of zero times a NaN
 //    or an infinity would still spoil the row.  Their scores become -inf.
+//
+// Measured, calls in a row, merge included.  One token to 1500 states, 16 heads of
+// 64: 9.8 us, latency (share, first loads, partials, merge).  Five beams of 24
+// requests to 200 - 1500 states of them: 28 us for 105 MB; six verify rows of 8
+// requests to up to 6404 masked states, 32/8 heads of 128: 30 us for 121 MB, both
+// HBM between a start of 4 us and a merge of 4 (64 requests of 6144 states stream at
+// 6.5 - 6.8 TB/s).  4777 tokens of five prompts to 129 - 6404 states, 32/8 heads of
+// 128: 262 us, 1300 TFLOP/s; the tensor pipe is active 62 % of the time, since S,
+// P and O fill tensor memory and a warpgroup's softmax and products alternate.
 #include <limits.h>
 #include <math.h>
 
@@ -728,8 +737,8 @@ __device__ __forceinline__ void fill_sequence_table(const CrossParams& p, const 
   }
 }
 
-// Where the CTA's share of a line of `total` begins, in the numbers that it needs (a
-// division of 64 bits takes 1000 cycles, and its code is fetched for it).  sum: the
+// Where the CTA's share of a line of `total` begins, in the numbers that it needs (one
+// division of 64 bits is a call of its own on the way to the first load).  sum: the
 // line up to and with this lane's sequence, where they are at most 32.
 template <typename N>
 __device__ __forceinline__ Share locate_share(const CrossParams& p, const SequenceTable& tab, const Sequence& seq,
@@ -1134,7 +1143,9 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   CUtensorMap tq, tf, tk, tv;
   // Pairs of heads: where sequences have at most 32 rows of a head on average.  (A
   // longer one is cut into units of 32 rows, whose products fill a quarter of the
-  // tensor cores' rows: 2048 rows of one sequence took twice the time.)
+  // tensor cores' rows.  64 sequences of 1500 states, 16 heads, us in pairs and one
+  // by one: 4 rows 72 and 101, 32 rows 75 and 99, 48 rows 134 and 105, 128 rows 247
+  // and 106; 2048 rows of one sequence of 2048 states 78 and 33.)
   const bool pairs = head_dim == 64 && num_kv_heads % 2 == 0 && g <= 32 && (int64_t)num_tokens * g <= (int64_t)32 * batch;
   const int few = g > 32 ? 0 : 32 / g, wide = pairs ? 128 : head_dim;
   const int heads = pairs ? num_kv_heads / 2 : num_kv_heads;
