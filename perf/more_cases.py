@@ -1,6 +1,7 @@
-"""Device times that operators.py does not show: block tables in steps whose
-pages move (there a state's second pass finds them moved already), and chunk
-attention over hundreds of sequences.
+"""Device times that operators.py and more_operators.py do not show: block tables
+in steps whose pages move (there a state's second pass finds them moved
+already), chunk attention over hundreds of sequences, cross attention to long
+states.
 
     python perf/more_cases.py
 
@@ -14,6 +15,7 @@ import numpy as np
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from perf import more_operators  # noqa: E402
 from self_speculative_sparse_vg_gb300 import vg  # noqa: E402
 
 PAGE = 16
@@ -111,6 +113,39 @@ class Chunks:
         pass
 
 
+class Case:
+    """A case of more_operators.py; what a call changes of a state is put back."""
+    def __init__(self, name, seed, **changes):
+        case = next(c for c in more_operators.listed() if c["name"] == name)
+        self.state = more_operators.prepare({**case, **changes}, seed)
+        self.kept = {k: self.state[k].clone() for k in ("table", "lens", "owned", "free", "count") if k in self.state}
+
+    def call(self):
+        more_operators.run(self.state)
+
+    def restore(self):
+        for k, v in self.kept.items():
+            self.state[k].copy_(v)
+
+
+class Cross:
+    """`rows` rows of each of `batch` sequences to `states` states."""
+
+    def __init__(self, batch, rows, states, Hq, Hkv, d):
+        new = lambda n, h: torch.randn(n, h, d, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+        self.q, self.k, self.v = new(batch * rows, Hq), new(batch * states, Hkv), new(batch * states, Hkv)
+        self.out = torch.empty_like(self.q)
+        self.where = i32(np.arange(batch + 1) * rows), i32(np.arange(batch) * states), i32([states] * batch)
+        self.ws = torch.empty(vg.cross_workspace_bytes(batch, batch * rows, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+        self.bytes = 2 * (2 * self.k.numel() + 2 * self.q.numel())
+
+    def call(self):
+        vg.cross_attention(self.q, self.k, self.v, *self.where, self.q.shape[2] ** -0.5, self.out, workspace=self.ws)
+
+    def restore(self):
+        pass
+
+
 def measure(states):
     for s in states:
         s.call()
@@ -142,6 +177,18 @@ def main():
         us = measure(states)
         rate = np.mean([s.bytes for s in states]) / us * 1e-3
         print(f"chunk  {single} tokens + {chunk:4d}   {us:7.1f} us   {rate:6.0f} GB/s", flush=True)
+    more_operators.own = True
+    for name, changes in (("tables_b32", {}), ("tables_b32", dict(fresh=0.0, finished=0.0)), ("tables_one", {}),
+                          ("select_one_32k", {}), ("select_b64_128k", {}), ("copy_layer", {}), ("copy_32_layers", {}),
+                          ("cross_one_1500", {}), ("cross_beams_b24", {}), ("cross_verify_b8", {}),
+                          ("cross_prompts_b5", {})):
+        us = measure([Case(name, i, **changes) for i in range(STATES)])
+        print(f"{name:16s} {str(changes or ''):36s} {us:7.2f} us", flush=True)
+    for shape in ((64, 4, 1500, 16, 16, 64), (64, 64, 1500, 16, 16, 64), (64, 6, 6144, 16, 16, 64),
+                  (64, 6, 6144, 32, 8, 128)):
+        states = [Cross(*shape) for _ in range(2)]
+        us = measure(states)
+        print(f"cross  {shape} {us:7.1f} us   {states[0].bytes / us * 1e-3:6.0f} GB/s", flush=True)
 
 
 if __name__ == "__main__":
