@@ -23,7 +23,7 @@
 //    the rows' scores in its own lanes and takes 32 columns; the warps exchange
 //    the rows' maxima and write P to shared memory, whence the product with V
 //    reads it.
-//  * Where most sequences have so few rows and heads are 64 wide, a unit is a pair
+//  * Where most sequences have one row tile and heads are 64 wide, a unit is a pair
 //    of neighbouring KV heads, one for each warpgroup: a state's 128 bytes of one
 //    head come from HBM at 4.5 TB/s, 256 bytes of two at 6.5 (16 heads, 6144
 //    states of 64 requests).
@@ -436,7 +436,8 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
       const bool direct = un.part < 0;
       const int t = un.tok0 + tok, qh = (PAIR ? 2 * un.h + wg : un.h) * g + head_r;
       // row of the partial
-      const int prow = PAIR ? tok_r * 2 * g + wg * g + head_r : (un.two ? wg * kTile : 0) + r;
+      const int half = tt / 2;  // (of a pair: as many tokens have 128 rows of both heads)
+      const int prow = PAIR ? tok_r / half * kTile + (tok_r % half * 2 + wg) * g + head_r : (un.two ? wg * kTile : 0) + r;
       const float inv = direct ? (l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN) : 1.f;
       const float f_own = has ? w_own * inv : 0.f, f_other = w_other * inv;
       const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * 2)) & 31) == 0;
@@ -529,7 +530,7 @@ struct MmaIssuer {
   }
   // O of warpgroup `wg` (+)= P V of the stage
   __device__ __forceinline__ void pv(int wg, uint32_t stage, bool accumulate) {
-    const uint32_t v = v_lo + stage * (Lay::kStageBytes >> 4);
+    const uint32_t v = v_lo + (stage * Lay::kStageBytes + (PAIR ? wg * Lay::kBlockBytes : 0) >> 4);
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks)
       umma_bf16_ts_elect(tmem + Lay::kOCol + wg * HD, tmem + Lay::kSCol + wg * kTile + ks * 8,
@@ -571,7 +572,7 @@ __device__ __forceinline__ bool mma_role(const CrossParams& p, const CrossBars& 
     pc ^= 1u << wg;
     if (!wait_phase_warp(&bars.pfull[wg], par, p)) return false;
     tc_fence_after();
-    if (PAIR || few)
+    if (few)
       mma.pv_few(wg, st, accumulate);
     else
       mma.pv(wg, st, accumulate);
@@ -824,8 +825,8 @@ struct Producer {
   }
   __device__ __forceinline__ void send_q() {
     const int g = p.group, tt = p.tile_tokens;
-    const bool narrow = PAIR || q_unit.narrow;
-    const int copies = narrow ? 4 : q_unit.two ? 2 : 1, tokens = narrow ? p.few_tokens : tt;
+    const bool narrow = q_unit.narrow;
+    const int copies = narrow ? 4 : q_unit.two && !PAIR ? 2 : 1, tokens = narrow ? p.few_tokens : tt;
     mbar_arrive_expect_tx(bars.qfull, copies * Lay::kBlocks * tokens * g * 128);
     for (int t = 0; t < copies; ++t)
       for (int x = 0; x < Lay::kBlocks; ++x) {
@@ -883,7 +884,7 @@ struct Producer {
         un.len = seq.len;
         un.h = h;
         un.two = PAIR || un.ntok > tt;
-        un.narrow = PAIR || un.ntok <= p.few_tokens;
+        un.narrow = un.ntok <= p.few_tokens;
         const int tiles = state_tiles(seq.len);
         un.kt0 = kt0;
         un.kt1 = min(tiles, tiles_before(s.x1 - at, cost));
@@ -1048,10 +1049,18 @@ struct CrossPlan {
   size_t off_ml, off_merge, bytes;
 };
 
-CrossPlan make_cross_plan(int num_tokens, int group, int head_dim) {
+// Whether heads may be taken in pairs: then a token has 2 group rows, of which the
+// merge finds kTile / (2 group) tokens' in a tile.
+bool may_pair(int group, int num_kv_heads, int head_dim) {
+  return head_dim == 64 && num_kv_heads % 2 == 0 && 2 * group <= kTile;
+}
+
+CrossPlan make_cross_plan(int num_tokens, int group, int num_kv_heads, int head_dim) {
   CrossPlan pl;
   pl.grid = device_sm_count();
-  pl.rows = num_tokens > kTile / group ? kRowsMax : kTile;  // one row tile holds every unit
+  // one row tile holds every unit
+  const bool one = num_tokens <= kTile / (may_pair(group, num_kv_heads, head_dim) ? 2 * group : group);
+  pl.rows = one ? kTile : kRowsMax;
   const size_t rows = (size_t)pl.grid * 2 * pl.rows;
   pl.off_ml = align_up(rows * head_dim * sizeof(float), 256);
   pl.off_merge = align_up(pl.off_ml + rows * 2 * sizeof(float), 256);
@@ -1105,7 +1114,7 @@ extern "C" size_t vg_cross_workspace_bytes(int batch, int num_tokens, int num_q_
   if (batch <= 0 || num_tokens <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_q_heads % num_kv_heads || !known_shape(num_q_heads, num_kv_heads, head_dim))
     return 0;
-  return make_cross_plan(num_tokens, num_q_heads / num_kv_heads, head_dim).bytes;
+  return make_cross_plan(num_tokens, num_q_heads / num_kv_heads, num_kv_heads, head_dim).bytes;
 }
 
 extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -1133,7 +1142,7 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
       (num_states > 0 && (bad(k, k_stride, kv_row) || bad(v, v_stride, kv_row))))
     return VG_ERR_INVALID_ARGUMENT;
   const int g = num_q_heads / num_kv_heads;
-  const CrossPlan pl = make_cross_plan(num_tokens, g, head_dim);
+  const CrossPlan pl = make_cross_plan(num_tokens, g, num_kv_heads, head_dim);
   if (!workspace || workspace_bytes < pl.bytes) return VG_ERR_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return VG_ERR_INVALID_ARGUMENT;
   // without states there is nothing to map: Q stands in (a tile that is loaded
@@ -1141,18 +1150,24 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   const bool none = num_states == 0;
   // (Q of few rows: as many tokens as have 32)
   CUtensorMap tq, tf, tk, tv;
-  // Pairs of heads: where sequences have at most 32 rows of a head on average.  (A
-  // longer one is cut into units of 32 rows, whose products fill a quarter of the
-  // tensor cores' rows.  64 sequences of 1500 states, 16 heads, us in pairs and one
-  // by one: 4 rows 72 and 101, 32 rows 75 and 99, 48 rows 134 and 105, 128 rows 247
-  // and 106; 2048 rows of one sequence of 2048 states 78 and 33.)
-  const bool pairs = head_dim == 64 && num_kv_heads % 2 == 0 && g <= 32 && (int64_t)num_tokens * g <= (int64_t)32 * batch;
+  // Pairs of heads: where sequences have at most 128 rows of a head on average (a
+  // pair's unit has one row tile of each, so longer ones load K and V twice as
+  // often), and past 32 only where a CTA has several tiles (a pair's divided units have
+  // twice the rows to merge).  us in pairs and one by one, 16 heads, 1500 states:
+  // 64 sequences of 4 rows 72 and 101, 32 rows 75 and 100, 33 rows 78 and 107, 128 rows
+  // 83 and 106, 160 rows 154 and 133; 6 sequences of 64 rows 19.6 and 20.6, of 128 rows
+  // 20.7 both; 2 of 128 rows 16.7 and 14.3; 1, 2 and 6 of 1 row 10.0, 11.6 and 16.6 against
+  // 10.3, 12.0 and 18.0.
+  const int64_t rows = (int64_t)num_tokens * g;
+  const bool many = (int64_t)num_states * num_kv_heads >= (int64_t)7 * kTile * pl.grid;
+  const bool pairs = may_pair(g, num_kv_heads, head_dim) && rows <= (int64_t)(many ? kTile : 32) * batch;
   const int few = g > 32 ? 0 : 32 / g, wide = pairs ? 128 : head_dim;
+  const int tile_tokens = pairs ? 2 * (kTile / (2 * g)) : kTile / g;
   const int heads = pairs ? num_kv_heads / 2 : num_kv_heads;
   const int there = none ? num_tokens : num_states, mapped = none ? (pairs ? num_q_heads / 2 : num_q_heads) : heads;
   if (!head_tile_tensor_map(none ? q : k, there, mapped, wide, none ? q_stride : k_stride, kTile, &tk) ||
       !head_tile_tensor_map(none ? q : v, there, mapped, wide, none ? q_stride : v_stride, kTile, &tv) ||
-      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, kTile / g, &tq) ||
+      !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, tile_tokens, &tq) ||
       !token_rows_tensor_map(q, num_tokens, num_q_heads, head_dim, q_stride, g, few ? few : 1, &tf))
     return VG_ERR_LAUNCH;
   CrossParams p = {};
@@ -1179,9 +1194,9 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   p.group = g;
   p.rows = pl.rows;
   p.heads = heads;
-  p.tile_tokens = pairs ? few : kTile / g;
+  p.tile_tokens = tile_tokens;
   p.few_tokens = few;
-  p.unit_tokens = pairs ? few : 2 * (kTile / g);
+  p.unit_tokens = pairs ? tile_tokens : 2 * tile_tokens;
   p.by_unit_tokens = p.unit_tokens == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + p.unit_tokens - 1) / p.unit_tokens);
   const bool f16 = type == VG_TYPE_FP16;
   auto launch = [&](auto kernel_of_type) { return kernel_of_type(pl, tq, tf, tk, tv, p, stream); };

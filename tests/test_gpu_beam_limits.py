@@ -151,3 +151,19 @@ def test_every_row_asks_for_a_copy_of_one_page():
 def test_the_longest_group_of_heads():
     check_cross(States([300, 77], 1, 64, seed=4), [3, 1], 128)
     check_cross(States([300, 77], 1, 128, seed=5, masked=0.2), [2, 300], 128)
+
+
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("Hq,Hkv", [(16, 16), (6, 2), (10, 2), (48, 4), (66, 2), (128, 2), (80, 80)])
+def test_pairs_of_heads_with_full_row_tiles(Hq, Hkv, dtype, masked):
+    """Up to 128 rows of a head on average, among many states: single tokens, full
+    tiles and sequences of several units in one call."""
+    lens = [700, 1, 2500, 128, 0, 129, 1111, 40, 1300]
+    gap = 7 * 128 * 160 // Hkv // len(lens)                 # the buffer's states decide
+    tile = 128 * Hkv // Hq
+    new = [tile, 1, tile // 2 + 1, max(1, tile // 4), tile, 0, tile + tile // 2, 2, 2 * tile + 1]
+    new[4] -= max(0, sum(new) - len(lens) * tile)
+    assert 0 <= new[4] and sum(new) <= len(lens) * tile
+    check_cross(States(lens, Hkv, 64, dtype, seed=Hq, gap=gap, masked=masked, fused=Hkv < 16), new, Hq, rows_after=1,
+                strided=dtype == torch.float16)
