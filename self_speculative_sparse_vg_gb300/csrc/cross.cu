@@ -35,7 +35,7 @@
 //    or an infinity would still spoil the row.  Their scores become -inf.
 //
 // Measured, calls in a row, merge included.  One token to 1500 states, 16 heads of
-// 64: 9.8 us, latency (share, first loads, partials, merge).  Five beams of 24
+// 64: 10 us, latency (share, first loads, partials, merge).  Five beams of 24
 // requests to 200 - 1500 states of them: 28 us for 105 MB; six verify rows of 8
 // requests to up to 6404 masked states, 32/8 heads of 128: 30 us for 121 MB, both
 // HBM between a start of 4 us and a merge of 4 (64 requests of 6144 states stream at
