@@ -1052,7 +1052,8 @@ cudaError_t launch_chunk(const ChunkPlan& pl, const CUtensorMap& tq, const CUten
   const MergeParams m = {reinterpret_cast<uint16_t*>(p.out), p.lse,          p.part_o,  p.part_ml, p.merge,
                          p.out_stride,                       p.num_q_heads, p.group,   p.rows};
   const long long rows = (long long)p.num_tokens * p.group;
-  return launch_unit_merge<HD, false>(cfg, pl.grid, rows, rows, m);
+  const long long usual = rows <= 32 ? 2 * (rows / p.batch) + 1 : rows;
+  return launch_unit_merge<HD, false>(cfg, pl.grid, rows, usual, m);
 }
 
 }  // namespace

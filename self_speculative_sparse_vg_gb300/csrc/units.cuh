@@ -186,77 +186,81 @@ __global__ void __launch_bounds__(kMergeWarps * 32) unit_merge_kernel(const Merg
 }
 
 // The same for calls of few rows (single tokens), whose units have many parts:
-// a CTA per row, its warps over the parts, every load in flight at once.
+// a CTA per row at a time, its warps over the parts, every load in flight at once.
 template <int HD, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32) unit_merge_row_kernel(const MergeParams p) {
   constexpr int E = HD / 32;
   __shared__ float acc_s[kMergeWarps][HD], l_s[kMergeWarps], m_s[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const MergeUnit mu = p.merge[c];
   const int g = p.group;
-  if (mu.parts == 0 || row >= mu.ntok * g) return;
+  if (mu.parts == 0) return;
   auto slot = [&](int part) { return (size_t)(part == 0 ? 2 * c + 1 : 2 * (c + part)); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float m = -INFINITY, l = 0.f, acc[E];
+  for (int row = blockIdx.y; row < mu.ntok * g; row += gridDim.y) {
+    if (row >= gridDim.y) __syncthreads();  // the row before is read
+    float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < mu.parts; i += kMergeWarps) {
-    const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
-    const float* src = p.part_o + ((slot(i) * (HD / 4) + lane * E / 4) * p.rows + row) * 4 + lane * E % 4;
-    float v[E];
-    if (E == 4) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-      v[0] = y.x, v[1] = y.y, v[E - 2] = y.z, v[E - 1] = y.w;
-    } else {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-      v[0] = y.x, v[1] = y.y;
+    for (int i = warp; i < mu.parts; i += kMergeWarps) {
+      const float2 x = __ldcg(&ml[slot(i) * p.rows + row]);
+      const float* src = p.part_o + ((slot(i) * (HD / 4) + lane * E / 4) * p.rows + row) * 4 + lane * E % 4;
+      float v[E];
+      if (E == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+        v[0] = y.x, v[1] = y.y, v[E - 2] = y.z, v[E - 1] = y.w;
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+        v[0] = y.x, v[1] = y.y;
+      }
+      const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
+      const float f = ex2(m - ref), w = ex2(x.x - ref);
+      // a part without weight is passed over if all of it is finite (one token of
+      // 8 heads over 2K: 9.9 us for the call, 10.4 when none is)
+      bool finite = fabsf(x.y) < INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) finite &= fabsf(v[e]) < INFINITY;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f;
+      if (w != 0.f || !finite) {
+        l += w * x.y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+      }
+      m = mn;
     }
-    const float mn = fmaxf(m, x.x), ref = safe_ref(mn);
-    const float f = ex2(m - ref), w = ex2(x.x - ref);
-    // a part without weight is passed over if all of it is finite (one token of
-    // 8 heads over 2K: 9.9 us for the call, 10.4 when none is)
-    bool finite = fabsf(x.y) < INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) finite &= fabsf(v[e]) < INFINITY;
-    l *= f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= f;
-    if (w != 0.f || !finite) {
-      l += w * x.y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      l_s[warp] = l;
+      m_s[warp] = m;
     }
-    m = mn;
-  }
+    __syncthreads();
+    if (threadIdx.x < HD / 2) {
+      float m_all = m_s[0];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    l_s[warp] = l;
-    m_s[warp] = m;
-  }
-  __syncthreads();
-  if (threadIdx.x >= HD / 2) return;
-  float m_all = m_s[0];
+      for (int i = 1; i < kMergeWarps; ++i) m_all = fmaxf(m_all, m_s[i]);
+      const float ref = safe_ref(m_all);
+      float l_all = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-  for (int i = 1; i < kMergeWarps; ++i) m_all = fmaxf(m_all, m_s[i]);
-  const float ref = safe_ref(m_all);
-  float l_all = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMergeWarps; ++i) {
-    const float w = ex2(m_s[i] - ref);
-    l_all += w * l_s[i];
-    o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
-    o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
+      for (int i = 0; i < kMergeWarps; ++i) {
+        const float w = ex2(m_s[i] - ref);
+        l_all += w * l_s[i];
+        o0 = fmaf(w, acc_s[i][2 * threadIdx.x], o0);
+        o1 = fmaf(w, acc_s[i][2 * threadIdx.x + 1], o1);
+      }
+      const float inv = l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN;
+      const int t = mu.tok0 + row / g, qh = mu.h * g + row % g;
+      *reinterpret_cast<uint32_t*>(p.out + t * p.out_stride + (int64_t)qh * HD + 2 * threadIdx.x) =
+          pack2<F16>(o0 * inv, o1 * inv);
+      if (p.lse && threadIdx.x == 0)
+        p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
+    }
   }
-  const float inv = l_all > 0.f ? 1.f / l_all : l_all == l_all ? 0.f : NAN;
-  const int t = mu.tok0 + row / g, qh = mu.h * g + row % g;
-  *reinterpret_cast<uint32_t*>(p.out + t * p.out_stride + (int64_t)qh * HD + 2 * threadIdx.x) =
-      pack2<F16>(o0 * inv, o1 * inv);
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(int64_t)t * p.num_q_heads + qh] = (m_all + log2f(l_all)) * 0.6931471805599453f;
 }
 
 // Launches the merge behind a kernel whose calls have at most `rows` rows of a
@@ -269,9 +273,14 @@ cudaError_t launch_unit_merge(cudaLaunchConfig_t cfg, int grid, long long rows, 
   cfg.dynamicSmemBytes = 0;
   // Up to 32 rows: a CTA per row, whose units have many parts (one token of 8
   // heads over 2K: 9.9 us for the call, 12.7 with the other merge; eight tokens
-  // over 16K - 64K: the same).  More rows mean fewer parts, and a CTA takes 32.
+  // over 16K - 64K: the same).  Units of several sequences have fewer, so that most of
+  // 32 CTAs a unit would find no row: 16, or as many as expected, take two where one
+  // sequence has them all (a token each of 8 sequences to 6404 states, 32/8 heads:
+  // 30.6 us, 33.0 with 32; eight tokens of one 19.6 and 19.2).  More rows mean fewer parts,
+  // and a CTA takes 32.
   if (rows <= 32) {
-    cfg.gridDim = dim3(grid, (int)rows);
+    const long long some = usual > 16 ? usual : 16;
+    cfg.gridDim = dim3(grid, (int)(some < rows ? some : rows));
     return cudaLaunchKernelEx(&cfg, unit_merge_row_kernel<HD, F16>, p);
   }
   const int most = p.rows == kUnitTile ? (int)rows : p.rows;

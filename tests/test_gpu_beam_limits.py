@@ -167,3 +167,14 @@ def test_pairs_of_heads_with_full_row_tiles(Hq, Hkv, dtype, masked):
     assert 0 <= new[4] and sum(new) <= len(lens) * tile
     check_cross(States(lens, Hkv, 64, dtype, seed=Hq, gap=gap, masked=masked, fused=Hkv < 16), new, Hq, rows_after=1,
                 strided=dtype == torch.float16)
+
+
+@pytest.mark.parametrize("Hkv,g,d", [(8, 4, 128), (2, 4, 64), (1, 3, 128)])
+@pytest.mark.parametrize("new", [[8, 0, 0, 0, 0, 0, 0, 0], [0, 0, 6, 0, 0, 1, 0, 1], [1] * 8])
+def test_the_rows_of_a_padded_batch_are_one_sequences(Hkv, g, d, new):
+    """Few rows, whose units have many parts: more rows of one unit than a sequence has
+    on average, for both attentions that divide their units."""
+    from tests.fill_util import Cache, check_chunk
+    lens = [6000, 300, 9000, 40, 0, 2000, 1, 500]
+    check_cross(States(lens, Hkv, d, seed=g), new, Hkv * g)
+    check_chunk(Cache([n + m for n, m in zip(lens, new)], Hkv, d, seed=g), new, Hkv * g)
