@@ -1154,10 +1154,10 @@ extern "C" vg_status vg_cross_attention(const void* q, int64_t q_stride, const v
   // pair's unit has one row tile of each, so longer ones load K and V twice as
   // often), and past 32 only where a CTA has several tiles (a pair's divided units have
   // twice the rows to merge; the buffer's states decide, as lengths are on the device).
-  // us in pairs and one by one, 16 heads, 1500 states: 64 sequences of 4 rows 72 and 101, 32 rows 75 and 100, 33 rows 78 and 107, 128 rows
-  // 83 and 106, 160 rows 154 and 133; 6 sequences of 64 rows 19.6 and 20.6, of 128 rows
-  // 20.7 both; 2 of 128 rows 16.7 and 14.3; 1, 2 and 6 of 1 row 10.0, 11.6 and 16.6 against
-  // 10.3, 12.0 and 18.0.
+  // us in pairs and one by one, 16 heads, 1500 states: 64 sequences of 4 rows 72 and
+  // 101, 32 rows 75 and 100, 33 rows 78 and 107, 128 rows 83 and 106, 160 rows 154 and
+  // 133; 6 sequences of 64 rows 19.6 and 20.6, of 128 rows 20.7 both; 2 of 128 rows 16.7
+  // and 14.3; 1, 2 and 6 of 1 row 10.0, 11.6 and 16.6 against 10.3, 12.0 and 18.0.
   const int64_t rows = (int64_t)num_tokens * g;
   const bool many = (int64_t)num_states * num_kv_heads >= (int64_t)7 * kTile * pl.grid;
   const bool pairs = may_pair(g, num_kv_heads, head_dim) && rows <= (int64_t)(many ? kTile : 32) * batch;
