@@ -13,7 +13,8 @@
 // barriers between them).  The columns of all requests, in tiles of 32, form one
 // line that the CTAs of one cluster share; the places of the returned pages are in
 // line order, so the CTAs exchange their counts through distributed shared memory,
-// and a second cluster barrier lies between what is pushed and what is popped.
+// and a second cluster barrier lies between the columns (old entries read, pages
+// pushed) and the copies (pages popped, their entries written).
 //
 // Three kinds of columns.  Most hold one full page in all rows and go on doing so:
 // a tile of such is looked at, a thread per column and all its loads in flight,
@@ -461,7 +462,10 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
     __syncwarp();
     if (spread) break;
   }
-  if (back > 0 || asked > top) {
+  // before an entry of a copy is written every warp has read the old ones (a row that
+  // takes its own last page as a copy is another row's source), and what was pushed is
+  // there to be popped; the same decision in all CTAs
+  if (back > 0 || asked > 0) {
     __syncwarp();
     if (ctas > 1) {
       cluster_arrive_release();
