@@ -270,6 +270,11 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
     sh.alive[b] = sh.bad[b] = sh.ends[b] = 0;
     sh.full[b] = INT_MAX;
   }
+  // another CTA's shared memory is there once that CTA has begun
+  if (ctas > 1) {
+    __syncwarp();
+    cluster_arrive_relaxed();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int top0 = *p.free_count;
@@ -405,6 +410,8 @@ __global__ void __launch_bounds__(NT) beam_tables_kernel(const BeamParams p) {
   const int before = sum(lane == 0 ? mine : 0, &total) - (lane == 0 ? mine : 0);
   int base = top0 + __shfl_sync(0xffffffffu, before, 0), back = total;
   if (ctas > 1) {
+    __syncwarp();
+    cluster_wait_acquire();  // of the arrival at the beginning
     if (tid < ctas) {
       const uint32_t to = mapa_shared(smem_u32(&counts[cta]), tid);
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(total) : "memory");
