@@ -561,7 +561,8 @@ vg_status vg_cross_attention(const void* q, int64_t q_stride, const void* k, int
  * outputs must not overlap inputs.
  *   workspace    vg_beam_select_workspace_bytes() bytes, 16-byte aligned.
  * Scores are compared to about 2^-23 of the row's sum of exponentials, and rounded
- * to float32 once; candidates of one beam compare as their logits do.  A beam
+ * to float32 once; candidates of one beam compare as their logits do (logits
+ * apart by less than 2^-46 of their score may come in either order).  A beam
  * with a NaN or +infinity as its score or among its logits is flagged
  * VG_DEVERR_VALUE and offers nothing.  Two kernels.
  * Supported: beams <= 32, num_out <= 64, rows of at most 3 MB.

@@ -518,9 +518,12 @@ struct alignas(16) Row {
 
 struct Pick {
   uint64_t key;  // order of the score (hi, then lo); 0: none
-  int at;        // list * num_out + depth: beam, then token, among equal scores
-  int token;
+  uint64_t tie;  // order among equal keys: beam, logit (largest first), where it stands in
+                 // the lists.  (A key does not tell logits of a beam apart that differ
+                 // by less than 2^-47 of its offset: 1e-20 and 2e-20 beside -10.)
 };
+constexpr int kAtBits = 18;  // list * num_out + depth
+static_assert(kMaxBeams * kMaxSlices * kMaxOut <= 1 << kAtBits, "");
 
 __device__ __forceinline__ uint64_t score_key(float2 y) {
   return y.x > -INFINITY ? (uint64_t)ordered(y.x) << 32 | ordered(y.y) : 0;  // past float's range: none
@@ -530,28 +533,31 @@ __device__ __forceinline__ uint64_t score_key(float2 y) {
 // n d < 2^32.
 __device__ __forceinline__ int quotient(int n, uint32_t m) { return m == 0 ? n : (int)__umulhi((uint32_t)n, m); }
 
-// Entry `depth` of list `list` (a slice of a row), given what lies there.
-__device__ __forceinline__ Pick pick_of(const SelectParams& p, const Row* rows, int list, int depth, float2 raw) {
+// Key of entry `depth` of list `list` (a slice of a row), given what lies there.
+__device__ __forceinline__ uint64_t key_of(const SelectParams& p, const Row* rows, int list, int depth, float2 raw) {
   const int w = quotient(list, p.by_slices);
   const Row r = rows[w];
-  Pick k = {0, list * p.num_out + depth, __float_as_int(raw.y)};
-  if (r.kind == 1) {
-    if (k.token >= 0) k.key = score_key(pair_add(r.offset, raw.x));
-  } else if (r.kind == 2 && depth == 0 && list == w * p.slices) {
-    k.key = score_key(make_float2(r.score, 0.f));
-    k.token = p.end_token;
-  }
-  return k;
+  if (r.kind == 1 && __float_as_int(raw.y) >= 0) return score_key(pair_add(r.offset, raw.x));
+  if (r.kind == 2 && depth == 0 && list == w * p.slices) return score_key(make_float2(r.score, 0.f));
+  return 0;
+}
+__device__ __forceinline__ uint64_t tie_of(const SelectParams& p, int list, int at, float logit) {
+  return (uint64_t)quotient(list, p.by_slices) << (32 + kAtBits) | (uint64_t)~ordered(logit) << kAtBits | (uint64_t)at;
+}
+__device__ __forceinline__ bool before(const Pick& a, const Pick& b) {
+  return a.key > b.key || (a.key == b.key && a.tie < b.tie);
 }
 
-__device__ __forceinline__ void write_place(const SelectParams& p, const Row* rows, int b, int place, const Pick& k) {
+__device__ __forceinline__ void write_place(const SelectParams& p, const Row* rows, int b, int place, const Pick& k,
+                                            int token) {
   const int64_t at = (int64_t)b * p.num_out + place;
   const bool none = k.key == 0;
-  const int w = none ? -1 : quotient(quotient(k.at, p.by_out), p.by_slices);
+  const int w = none ? -1 : (int)(k.tie >> (32 + kAtBits));
+  if (!none && rows[w].kind == 2) token = p.end_token;
   p.out_scores[at] = none ? -INFINITY : from_ordered((uint32_t)(k.key >> 32));
-  p.out_tokens[at] = none ? -1 : k.token;
+  p.out_tokens[at] = none ? -1 : token;
   p.out_parents[at] = w;
-  if (p.out_ended) p.out_ended[at] = !none && (rows[w].kind == 2 || k.token == p.end_token);
+  if (p.out_ended) p.out_ended[at] = !none && (rows[w].kind == 2 || token == p.end_token);
 }
 
 // Where more entries are level than there is room for: the best front entry of
@@ -561,22 +567,42 @@ __device__ __noinline__ void merge_one_by_one(const SelectParams& p, const Row* 
   const int lane = threadIdx.x & 31, lists = p.beams * p.slices;
   for (int l = lane; l < lists; l += 32) depth[l] = 0;
   for (int place = 0; place < p.num_out; ++place) {
-    Pick top = {0, INT_MAX, -1};
-    for (int l = lane; l < lists; l += 32) {
-      if (depth[l] >= p.num_out) continue;
-      const Pick k = pick_of(p, rows, l, depth[l], __ldcg(best + (int64_t)l * p.num_out + depth[l]));
-      if (k.key > top.key) top = k;  // equal: the lower list
+    Pick top = {0, ~0ull};
+    int token = -1;
+    constexpr int kAhead = 4;  // lists of a lane whose loads are in flight together
+    for (int l0 = lane; l0 < lists; l0 += 32 * kAhead) {
+      float2 raw[kAhead];
+      int d[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int l = l0 + 32 * i;
+        d[i] = l < lists ? depth[l] : p.num_out;
+        if (d[i] < p.num_out) raw[i] = __ldcg(best + l * p.num_out + d[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (d[i] >= p.num_out) continue;
+        const int l = l0 + 32 * i;
+        const uint64_t key = key_of(p, rows, l, d[i], raw[i]);
+        if (key == 0 || key < top.key) continue;
+        const Pick k = {key, tie_of(p, l, l * p.num_out + d[i], raw[i].x)};
+        if (before(k, top)) {
+          top = k;
+          token = __float_as_int(raw[i].y);
+        }
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      Pick k;
-      k.key = __shfl_xor_sync(0xffffffffu, top.key, o);
-      k.at = __shfl_xor_sync(0xffffffffu, top.at, o);
-      k.token = __shfl_xor_sync(0xffffffffu, top.token, o);
-      if (k.key > top.key || (k.key == top.key && k.at < top.at)) top = k;
+      const Pick k = {__shfl_xor_sync(0xffffffffu, top.key, o), __shfl_xor_sync(0xffffffffu, top.tie, o)};
+      const int other = __shfl_xor_sync(0xffffffffu, token, o);
+      if (before(k, top)) {
+        top = k;
+        token = other;
+      }
     }
-    if (lane == 0) write_place(p, rows, b, place, top);
-    const int l = top.at / p.num_out;
+    if (lane == 0) write_place(p, rows, b, place, top, token);
+    const int l = (int)(top.tie & ((1u << kAtBits) - 1u)) / p.num_out;
     if (top.key && l % 32 == lane) ++depth[l];
     __syncwarp();
   }
@@ -588,6 +614,7 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
   __shared__ Row rows[kMaxBeams];
   __shared__ __align__(16) float heads[kHeads];
   __shared__ Pick picks[kListed];
+  __shared__ int tokens[kListed];
   __shared__ uint32_t bound;
   __shared__ int counter;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
@@ -658,13 +685,13 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
   }
   __syncthreads();  // scores and marks have been read: the outputs may be the same arrays
   // -------- the bound: on scores rounded to floats, whose order is that of scores
-  auto rounded = [&](const Pick& k) { return k.key ? from_ordered((uint32_t)(k.key >> 32)) : -INFINITY; };
+  auto rounded = [&](uint64_t key) { return key ? from_ordered((uint32_t)(key >> 32)) : -INFINITY; };
   float front_score = -INFINITY;
-  if (tid < values) front_score = rounded(pick_of(p, rows, head_list, head_depth, head));
+  if (tid < values) front_score = rounded(key_of(p, rows, head_list, head_depth, head));
   int n = values;
   if (values > kHeads) {  // many lists: the best front entry of every four threads
     for (int l = tid + kRequestThreads; l < lists; l += kRequestThreads)
-      front_score = fmaxf(front_score, rounded(pick_of(p, rows, l, 0, __ldcg(best + (int64_t)l * p.num_out))));
+      front_score = fmaxf(front_score, rounded(key_of(p, rows, l, 0, __ldcg(best + (int64_t)l * p.num_out))));
     front_score = fmaxf(front_score, __shfl_xor_sync(0xffffffffu, front_score, 1));
     front_score = fmaxf(front_score, __shfl_xor_sync(0xffffffffu, front_score, 2));
     n = kRequestThreads / 4;
@@ -691,10 +718,13 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
     if (i >= entries) break;
     const float2 raw = k == 0 ? early[0] : k == 1 ? early[1] : k == 2 ? early[2] : k == 3 ? early[3] : __ldcg(best + i);
     const int list = quotient(i, p.by_out);
-    const Pick x = pick_of(p, rows, list, i - list * p.num_out, raw);
-    if (x.key >= least) {
+    const uint64_t key = key_of(p, rows, list, i - list * p.num_out, raw);
+    if (key >= least) {
       const int at = atomicAdd(&counter, 1);
-      if (at < kListed) picks[at] = x;
+      if (at < kListed) {
+        picks[at] = {key, tie_of(p, list, i, raw.x)};
+        tokens[at] = __float_as_int(raw.y);
+      }
     }
   }
   __syncthreads();
@@ -709,15 +739,14 @@ __global__ void __launch_bounds__(kRequestThreads) beam_merge_kernel(const Selec
     const Pick own = picks[c < listed ? c : 0];
     int rank = 0;
     for (int j = tid & 7; j < listed; j += 8) {
-      const Pick& o = picks[j];
-      rank += o.key > own.key || (o.key == own.key && o.at < own.at);
+      rank += before(picks[j], own);
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (c < listed && rank < p.num_out && (tid & 7) == 0) write_place(p, rows, b, rank, own);
+    if (c < listed && rank < p.num_out && (tid & 7) == 0) write_place(p, rows, b, rank, own, tokens[c]);
   }
   for (int place = listed + tid; place < p.num_out; place += kRequestThreads)
-    write_place(p, rows, b, place, Pick{0, 0, -1});
+    write_place(p, rows, b, place, Pick{0, 0}, -1);
 }
 
 struct SelectPlan {
