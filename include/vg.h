@@ -522,8 +522,9 @@ vg_status vg_chunk_attention(const vg_paged_kv* kv, const void* q, int64_t q_str
  * sequences hold either's.)
  * Results are the same on every run; what else is in the batch changes them by
  * rounding alone: it decides where a long sequence is cut, and a softmax weight
- * is rounded to the call's type (half a step) against the largest score since
- * the cut, or one up to 8 powers of two below it; sums are float32.
+ * is rounded to the call's type against the largest score since the cut, or one up
+ * to 8 powers of two below it, by half a step, in fp16 by 2^-32 of the row's largest
+ * weight if that is more; sums are float32.
  * Supported: head_dim 64/128, num_q_heads / num_kv_heads <= 128, batch <= 4096,
  * num_states <= 2^30.
  * ------------------------------------------------------------------------- */

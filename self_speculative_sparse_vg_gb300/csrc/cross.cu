@@ -55,11 +55,21 @@ constexpr int kTile = kUnitTile;       // states of a K or V tile, rows of a row
 constexpr int kCrossThreads = 384;
 constexpr int kProducer = 8, kMma = 9, kChecker = 10;  // warps (0..7: softmax; two checkers)
 constexpr int kMaxBatch = 4096;
-constexpr float kRescale = 8.f;        // log2 growth of a row maximum that moves the reference
 constexpr int kRowsMax = 2 * kTile;    // rows of a unit
 // Costs on the line that the CTAs share: a state tile of a unit with two row
 // tiles or with one, and what a unit costs beside its tiles.
 constexpr int kTwoCost = 5, kOneCost = 4, kUnitCost = 15;
+
+// The reference m of a row's weights 2^(score - m), in powers of two: it is set kBelow
+// below the row's maximum, and again when that outgrows it by kLimit.  fp16 weights
+// reach 2^15 so (of 2^16), and what a weight loses below fp16's normal range is at
+// most 2^-32 of the row's largest: with the reference at the maximum it was 2^-25, and
+// thousands of states of 2^-26 each were lost whole while the row's sum kept them.
+// bf16 has float32's exponents.
+template <bool F16>
+struct Reference {
+  static constexpr float kBelow = F16 ? 7.f : 0.f, kLimit = F16 ? 15.f : 8.f;
+};
 
 struct CrossParams {
   const int32_t* cu_q;
@@ -279,9 +289,9 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
       if (!exchange(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2,
                     [](float a, float b) { return fmaxf(a, b); }, m_tile))
         return;
-      const bool need = m_tile > m_used + kRescale;
+      const bool need = m_tile > m_used + Reference<F16>::kLimit;
       if (__any_sync(0xffffffffu, need)) {
-        const float mn = need ? m_tile : m_used;
+        const float mn = need ? m_tile - Reference<F16>::kBelow : m_used;
         if (kt != first) {  // P(t - 1) V is done: S(t) was issued after it
           const float corr = mn == -INFINITY ? 1.f : ex2(m_used - mn);
           lsum *= corr;
@@ -352,9 +362,9 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
           mx[j & 3] = max3(mx[j & 3], __uint_as_float(s[0][j]), __uint_as_float(s[1][j]));
         // scale > 0: the maximum commutes with it
         const float m_tile = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-        const bool need = m_tile > m_used + kRescale;
+        const bool need = m_tile > m_used + Reference<F16>::kLimit;
         if (__any_sync(0xffffffffu, need)) {
-          const float mn = need ? m_tile : m_used;
+          const float mn = need ? m_tile - Reference<F16>::kBelow : m_used;
           if (kt != first) {  // P(t - 1) V is done: S(t) was issued after it
             const float corr = mn == -INFINITY ? 1.f : ex2(m_used - mn);
             lsum *= corr;
@@ -370,8 +380,8 @@ __device__ __forceinline__ void softmax_role(const CrossParams& p, const CrossBa
           }
           m_used = mn;
         }
-        // P = 2^(s scale - m), at most 2^8, rounded to 16 bits for the tensor
-        // cores (half a step of each weight); the row sum takes it unrounded
+        // P = 2^(s scale - m), at most 2^8 (fp16: 2^15), rounded to 16 bits for the tensor
+        // cores (half a step of each weight, fp16: or 2^-25); the row sum takes it unrounded
         const float nref = -safe_ref(m_used);
         const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), nref2 = pair(nref, nref);
 #pragma unroll
