@@ -19,18 +19,22 @@
 //    value is found by bisection and its ties in order.
 //  * A second kernel, a CTA per request, merges the slices' lists: of their front
 //    entries it finds a bound as the slices do, and orders by counting what reaches it.
+//    Where more reach it than there is room for, one warp takes the best front entry of
+//    all lists, place after place.
 //
 // A score decides between candidates that may lie close together, so it is held
 // as an unevaluated pair of floats: s - m - log l by error-free sums, the
 // logarithm split in exponent and mantissa.  What is left is the rounding of the
 // sum of exponentials, about 2^-23 relative.
 //
-// Measured, calls in a row.  One request of four beams, 32K bf16 logits: 6.9 us, two
-// launches' latency.  8 of four beams, 151936 float32 logits: 10.2 us.  16 of five,
-// 50257 fp16 logits from odd addresses: 11.3 us.  64 of eight, 128256 bf16 logits: 41.8
+// Measured, calls in a row.  One request of four beams, 32K bf16 logits: 6.8 us, two
+// launches' latency.  8 of four beams, 151936 float32 logits: 10.0 us.  16 of five,
+// 50257 fp16 logits from odd addresses: 11.2 us.  64 of eight, 128256 bf16 logits: 40.5
 // us (117 MB: 17.3 at the rate of a copy); there the slices take 34 us, of which the
 // load and the maxima 20.5, the exponentials 4.7, the candidates and their order 9:
-// issue is active 63 % of the time, and the short phases wait at barriers.
+// issue is active 63 % of the time, and the short phases wait at barriers.  One request
+// of many beams that keep many takes the warp's way through the lists: 16 beams keeping
+// 32 of 32K 91 us, of 128K 149; 32 beams keeping 64 of 128K 300.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -560,8 +564,12 @@ __device__ __forceinline__ void write_place(const SelectParams& p, const Row* ro
   if (p.out_ended) p.out_ended[at] = !none && (rows[w].kind == 2 || token == p.end_token);
 }
 
-// Where more entries are level than there is room for: the best front entry of
-// all lists, one place after another (one warp, a lane takes every 32nd list).
+// Where more entries reach the bound than there is room for: the best front entry of
+// all lists, one place after another (one warp, a lane takes every 32nd list).  That is
+// so where many are level, and where the bound is low: past 128 lists it comes from 64
+// maxima of four threads' fronts, of which it is the 32nd or 64th where as many are
+// kept, and from fewer where beams do not live (a first step) or lie far apart.
+// About 3 us a place (256 lists), 5 (928).
 __device__ __noinline__ void merge_one_by_one(const SelectParams& p, const Row* rows, const float2* best, int b,
                                               uint8_t* depth) {
   const int lane = threadIdx.x & 31, lists = p.beams * p.slices;

@@ -27,9 +27,9 @@
 // columns and a long request's tiles lie side by side, so a CTA's warps share what
 // each of them has found.
 //
-// Measured, calls in a row: 4 beams of 2100 positions 5.3 us, a launch's latency
+// Measured, calls in a row: 4 beams of 2100 positions 5.5 us, a launch's latency
 // and five round trips.  32 requests of eight beams with up to 32768 positions, each
-// call on a new state: 11.8 us when all go on, 16 us when a fifth of the requests begins
+// call on a new state: 11.8 us when all go on, 16.4 us when a fifth of the requests begins
 // or ends in the call (35.6 us with every column by lanes, 24.4 us with all rows of such
 // a tile read again).
 #include <limits.h>

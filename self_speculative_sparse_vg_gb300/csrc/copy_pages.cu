@@ -7,8 +7,8 @@
 // a layer's few pages.
 //
 // Measured: 32 rows' pages of one layer (8 heads of 128) 3.9 us a call, 2.3 on the
-// device; 128 rows' of 32 layers, 161 MB moved, 28.5 us a call, 27.4 in a graph (5.9
-// TB/s; 256 threads a page 29.7).
+// device; 128 rows' of 32 layers, 161 MB moved, 26 - 30 us a call, 27.4 in a graph
+// (5.9 TB/s; 256 threads a page 29.7).
 #include "vg_device.cuh"
 #include "vg_host.h"
 

@@ -40,8 +40,9 @@
 // requests to up to 6404 masked states, 32/8 heads of 128: 30 us for 121 MB, both
 // HBM between a start of 4 us and a merge of 4 (64 requests of 6144 states stream at
 // 6.5 - 6.8 TB/s).  4777 tokens of five prompts to 129 - 6404 states, 32/8 heads of
-// 128: 262 us, 1300 TFLOP/s; the tensor pipe is active 62 % of the time, since S,
-// P and O fill tensor memory and a warpgroup's softmax and products alternate.
+// 128: 272 us, 1250 TFLOP/s (262 in a graph); the tensor pipe is active 62 % of the
+// time, since S, P and O fill tensor memory and a warpgroup's softmax and products
+// alternate.
 #include <limits.h>
 #include <math.h>
 
